@@ -66,7 +66,7 @@ typedef enum {
   MOE_ERR_HIP = 5           /* a HIP launch or runtime call failed           */
 } moe_status_t;
 
-typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_E8M0 = 3 } moe_dtype_t;
+typedef enum { MOE_F32 = 0, MOE_BF16 = 1, MOE_E4M3 = 2, MOE_E8M0 = 3, MOE_E2M1 = 4 } moe_dtype_t;
 
 /* Device-side data errors OR-ed into *err_flag by moe_route (forced routing). */
 #define MOE_FLAG_INDEX_RANGE 1  /* a forced expert index outside [0, E)      */
@@ -483,6 +483,106 @@ moe_status_t moe_grouped_gemm_bwd_mx_parts(const moe_mx_bwd_args* args, unsigned
  * the forward-to-backward state is the fp8 copies (xq, xqT, hqT) and yp.
  */
 moe_status_t moe_grouped_gemm_recompute_gu_mx(const moe_mx_fwd_args* args, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Root-mean-square norm in front of the layer, with the residual's addition.
+ * ---------------------------------------------------------------------------
+ * moe_rmsnorm_fwd: for every row t of [T,d], in fp32 and rounded once per
+ * output,
+ *   v = x + res,  rstd = 1 / sqrt(mean_c v^2 + eps),  y = v * rstd * w
+ *   res (nullable): the residual; without it v = x.
+ *   s   (nullable): v rounded to dt, the residual of the next block.
+ *   y   (nullable if q is given): the normed rows in dt.
+ *   q, qs (nullable, together; d a multiple of 32): y's MXFP8 copy, rowwise,
+ *       in mx_quantize's encoding and layout (q [T,d]; qs ceil(d/128) * T * 4
+ *       bytes, 4-byte aligned, places past the last block 0), taken from the
+ *       fp32 values; a NaN keeps the NaN code.  It feeds the scaled grouped
+ *       GEMMs as xq / xs.
+ *   rstd (nullable): [T] f32, for the backward.
+ * w [d] dt.  eps finite and >= 0.  s may be x or res, and y may be x or res if
+ * s is neither the same buffer; nothing else may overlap.  T = 0 writes
+ * nothing.  d * element size at most 128 KiB.
+ */
+moe_status_t moe_rmsnorm_fwd(const void* x, const void* res, const void* w, int T, int d, float eps, int dt, void* s,
+                             void* y, uint8_t* q, uint8_t* qs, float* rstd, void* stream);
+/*
+ * moe_rmsnorm_bwd: gradients of moe_rmsnorm_fwd given dy, from the stored s
+ * (x where there was no residual) and rstd; with g = dy * w, xh = s * rstd,
+ *   dx = rstd * (g - xh * mean_c(g * xh)) + ds      (x's and the residual's)
+ *   dw = sum_t dy * xh                              (fixed order, one rounding)
+ * ds (nullable): the gradient that reaches s itself.  dx may be dy or ds.
+ * T = 0 gives dw = 0.  ws: moe_rmsnorm_bwd_workspace_size(T, d) bytes; calls
+ * that may run concurrently need separate workspaces.
+ */
+size_t moe_rmsnorm_bwd_workspace_size(int T, int d);
+moe_status_t moe_rmsnorm_bwd(const void* dy, const void* ds, const void* s, const void* w, const float* rstd, int T,
+                             int d, int dt, void* dx, void* dw, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * 4-bit weights: E2M1 elements (+-0, 1/2, 1, 3/2, 2, 3, 4, 6) with one E8M0
+ * scale per 32 consecutive values of a row, s = clamp(floor(log2(amax)) - 2,
+ * -127, 127) from the exponent bits (s = -127 for an all-zero block); elements
+ * v / 2^s rounded to nearest even, saturated to +-6, sign of zero kept.  A
+ * block that holds an infinity or NaN gets scale byte 255 and zero codes and
+ * stands for 32 NaNs.
+ *   q [rows, cols/2] u8: two codes a byte, the even column in the low half
+ *   s [ceil(cols/128)][rows][4] u8: mx_quantize's K-chunk-major scales; places
+ *     past a row's last block are written as 0
+ * ---------------------------------------------------------------------------
+ * mx_quantize_e2m1: in [rows, cols] (dt MOE_F32 or MOE_BF16) to q and s.
+ * mx_dequantize_e2m1: q and s to the values they stand for, in dt (exact in
+ *   either, but for values under the type's smallest).
+ * cols a multiple of 32; q 16-byte, s 4-byte aligned; rows * cols < 2^34.
+ */
+moe_status_t mx_quantize_e2m1(const void* in, int dt, int rows, int cols, uint8_t* q, uint8_t* s, void* stream);
+moe_status_t mx_dequantize_e2m1(const uint8_t* q, const uint8_t* s, int dt, int rows, int cols, void* out,
+                                void* stream);
+/*
+ * mx_linear_e2m1: y[t,:] = W x[t] for 0 <= T <= 64 tokens and a 4-bit matrix W
+ * of n rows and K columns (q, s as mx_quantize_e2m1 writes them for [n,K]);
+ * x [T,K], y [T,n] bf16, fp32 accumulation, one rounding.  K a multiple of 32.
+ */
+moe_status_t mx_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
+                            void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * moe_few_fwd: the whole layer, forward, for a few tokens (0 <= T <= 64): a
+ * decode step or a short draft, where the experts' weights are all the traffic
+ * there is.  The same layer as moe_router_logits + moe_route + moe_permute +
+ * moe_grouped_gemm_fwd + moe_combine, without their buffers:
+ *   p = softmax(x wr^T); topk_idx, topk_w as moe_route (ties to the lower
+ *   expert, not renormalised); y[t] = sum_j topk_w[t,j] W2[e] (silu(W1[e] x[t])
+ *   * (W3[e] x[t])), e = topk_idx[t,j].
+ * The hidden vectors are not rounded to dt in between (they keep at least 16
+ * mantissa bits), so y is the closer of the two to the exact sum.
+ *   dt: type of x, wr and y.  wt: type of w1, w3 [E,h,d] and w2 [E,d,h]: dt, or
+ *   MOE_E2M1 with dt MOE_BF16: then each is packed as mx_quantize_e2m1 packs
+ *   [E*h,d] and [E*d,h], w1s, w3s, w2s are their scales, and d and h must be
+ *   multiples of 32.  d, h <= 65536.
+ *   n_live (nullable, 4-byte aligned): how many of the T tokens are there, read
+ *   on the device (clamped to [0, T]), so that one captured call serves every
+ *   smaller batch.  Rows of y, topk_idx and topk_w from *n_live on are left as
+ *   they were, and their x is not used.
+ *   topk_idx [T,k] i32, topk_w [T,k] f32 (nullable).
+ *   y must not overlap x.
+ *   ws: moe_few_workspace_size(T, d, E, k, h) bytes (not kept between calls);
+ *   calls that may run concurrently need separate workspaces.
+ */
+typedef struct {
+  int T, d, E, k, h, dt, wt;
+  const void* x; const void* wr;
+  const void* w1; const void* w3; const void* w2;
+  const uint8_t* w1s; const uint8_t* w3s; const uint8_t* w2s; /* MOE_E2M1 only  */
+  const int32_t* n_live;
+  void* y; int32_t* topk_idx; float* topk_w;
+  void* ws; size_t ws_bytes;
+} moe_few_args;
+
+size_t moe_few_workspace_size(int T, int d, int E, int k, int h);
+moe_status_t moe_few_fwd(const moe_few_args* args, void* stream);
 
 #ifdef __cplusplus
 }

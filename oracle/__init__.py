@@ -28,6 +28,8 @@ are stated at each function.
 Modules:
   moe_ref  -- routing, dispatch, SwiGLU experts, combine, and the backward.
   mx_ref   -- MXFP8 (OCP E4M3FN elements, E8M0 block scales) quantisation.
+  norm_ref -- root-mean-square norm with the residual's addition.
+  mx4_ref  -- 4-bit weights (OCP E2M1 elements, E8M0 block scales).
   sampled_ref -- single tokens' and single experts' outputs of the full-size
               layer (the same definitions, for sampled parity at full size).
 

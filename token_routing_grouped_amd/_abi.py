@@ -15,7 +15,7 @@ import torch
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libtrg_moe.so")
 
-MOE_F32, MOE_BF16 = 0, 1
+MOE_F32, MOE_BF16, MOE_E2M1 = 0, 1, 4
 FLAG_INDEX_RANGE, FLAG_DUPLICATE = 1, 2
 _DT = {torch.float32: MOE_F32, torch.bfloat16: MOE_BF16}
 
@@ -62,6 +62,14 @@ _SIGS = {
     "moe_grouped_gemm_bwd_mx": ([_P, _P], _I),
     "moe_grouped_gemm_bwd_mx_parts": ([_P, ctypes.c_uint, _P], _I),
     "moe_grouped_gemm_fwd_mx_parts": ([_P, ctypes.c_uint, _P], _I),
+    "moe_rmsnorm_fwd": ([_P, _P, _P, _I, _I, ctypes.c_float, _I, _P, _P, _P, _P, _P, _P], _I),
+    "moe_rmsnorm_bwd_workspace_size": ([_I, _I], _Z),
+    "moe_rmsnorm_bwd": ([_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "mx_quantize_e2m1": ([_P, _I, _I, _I, _P, _P, _P], _I),
+    "mx_dequantize_e2m1": ([_P, _P, _I, _I, _I, _P, _P], _I),
+    "mx_linear_e2m1": ([_P, _P, _P, _I, _I, _I, _P, _P], _I),
+    "moe_few_workspace_size": ([_I, _I, _I, _I, _I], _Z),
+    "moe_few_fwd": ([_P, _P], _I),
 }
 
 
@@ -80,6 +88,14 @@ class MxBwdArgs(ctypes.Structure):
                                         "xqT", "xsT", "w1tq", "w1ts", "w3tq", "w3ts", "w2tq", "w2ts", "dgu", "dguq",
                                         "dgus", "dguqT", "dgusT", "dxp", "dw1", "dw3", "dw2", "ws")] + \
         [("ws_bytes", ctypes.c_size_t)] + [(n, ctypes.c_void_p) for n in ("dy", "topk_w", "src")] + [("k", ctypes.c_int)]
+
+
+class FewArgs(ctypes.Structure):
+    """moe_few_args (include/moe.h)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("T", "d", "E", "k", "h", "dt", "wt")] + \
+        [(n, ctypes.c_void_p) for n in ("x", "wr", "w1", "w3", "w2", "w1s", "w3s", "w2s", "n_live", "y", "topk_idx",
+                                        "topk_w", "ws")] + [("ws_bytes", ctypes.c_size_t)]
+
 
 EXPORTED = tuple(_SIGS)
 
@@ -449,3 +465,145 @@ def moe_grouped_gemm_bwd_mx_parts(parts, **kw):
     """A subset (MOE_BWD_* mask) of moe_grouped_gemm_bwd_mx's four GEMMs."""
     a = _fill(MxBwdArgs(), **kw)
     _check(lib().moe_grouped_gemm_bwd_mx_parts(ctypes.byref(a), parts, _stream()), "moe_grouped_gemm_bwd_mx_parts")
+
+
+# ---------------------------------------------------------------------------
+# norm, 4-bit weights, the layer for a few tokens
+# ---------------------------------------------------------------------------
+
+def _arg(t, dtype, numel, name):
+    """Device address of a tensor that must have this type and size and live on
+    the current device (the library launches there); None stays None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise MoeError(f"{name}: tensor on {t.device}, expected the GPU")
+    if t.get_device() != torch.cuda.current_device():
+        raise MoeError(f"{name}: tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    if t.dtype != dtype:
+        raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != numel:
+        raise MoeError(f"{name} must have {numel} elements, got {t.numel()}")
+    if not t.is_contiguous():
+        raise MoeError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _matrix(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise MoeError(f"{name} must be a matrix")
+    return t.shape
+
+
+def _ws_arg(ws):
+    return _arg(ws, torch.uint8, ws.numel(), "ws")
+
+
+def mx_scale_bytes(rows: int, cols: int) -> int:
+    """Bytes of the rowwise scales of a [rows, cols] matrix (K-chunk major)."""
+    return -(-cols // 128) * rows * 4
+
+
+def moe_rmsnorm_bwd_workspace_size(T: int, d: int) -> int:
+    return int(lib().moe_rmsnorm_bwd_workspace_size(T, d))
+
+
+def moe_few_workspace_size(T: int, d: int, E: int, k: int, h: int) -> int:
+    return int(lib().moe_few_workspace_size(T, d, E, k, h))
+
+
+def moe_rmsnorm_fwd(x, w, eps, y, res=None, s=None, q=None, qs=None, rstd=None):
+    """y = rmsnorm(x + res) * w; s = x + res, MXFP8 copy q / qs of y and rstd
+    where given."""
+    T, d = _matrix(x, "x")
+    n, dt = T * d, x.dtype
+    _check(lib().moe_rmsnorm_fwd(_arg(x, dt, n, "x"), _arg(res, dt, n, "res"), _arg(w, dt, d, "w"), T, d, eps, _dt(x),
+                                 _arg(s, dt, n, "s"), _arg(y, dt, n, "y"), _arg(q, torch.uint8, n, "q"),
+                                 _arg(qs, torch.uint8, mx_scale_bytes(T, d), "qs"),
+                                 _arg(rstd, torch.float32, T, "rstd"), _stream()), "moe_rmsnorm_fwd")
+
+
+def moe_rmsnorm_bwd(dy, s, w, rstd, dx, dw, ws, ds=None):
+    """dx (with ds, the gradient reaching s itself, added) and dw of
+    moe_rmsnorm_fwd from its s and rstd."""
+    T, d = _matrix(s, "s")
+    n, dt = T * d, s.dtype
+    _check(lib().moe_rmsnorm_bwd(_arg(dy, dt, n, "dy"), _arg(ds, dt, n, "ds"), _arg(s, dt, n, "s"),
+                                 _arg(w, dt, d, "w"), _arg(rstd, torch.float32, T, "rstd"), T, d, _dt(s),
+                                 _arg(dx, dt, n, "dx"), _arg(dw, dt, d, "dw"), _ws_arg(ws), ws.numel(), _stream()),
+           "moe_rmsnorm_bwd")
+
+
+def mx_quantize_e2m1(x, q, s):
+    """4-bit codes q [rows, cols/2] and scales s of x [rows, cols]."""
+    rows, cols = _matrix(x, "x")
+    _check(lib().mx_quantize_e2m1(_arg(x, x.dtype, rows * cols, "x"), _dt(x), rows, cols,
+                                  _arg(q, torch.uint8, rows * cols // 2, "q"),
+                                  _arg(s, torch.uint8, mx_scale_bytes(rows, cols), "s"), _stream()), "mx_quantize_e2m1")
+
+
+def mx_dequantize_e2m1(q, s, out):
+    """The values that 4-bit codes and scales stand for, in out's type."""
+    rows, cols = _matrix(out, "out")
+    _check(lib().mx_dequantize_e2m1(_arg(q, torch.uint8, rows * cols // 2, "q"),
+                                    _arg(s, torch.uint8, mx_scale_bytes(rows, cols), "s"), _dt(out), rows, cols,
+                                    _arg(out, out.dtype, rows * cols, "out"), _stream()), "mx_dequantize_e2m1")
+
+
+def mx_linear_e2m1(x, q, s, y):
+    """y [T, n] = x [T, K] W^T for a 4-bit W [n, K] and at most 64 tokens."""
+    T, K = _matrix(x, "x")
+    Ty, n = _matrix(y, "y")
+    if Ty != T:
+        raise MoeError(f"y must have {T} rows, got {Ty}")
+    bf = torch.bfloat16
+    _check(lib().mx_linear_e2m1(_arg(x, bf, T * K, "x"), _arg(q, torch.uint8, n * K // 2, "q"),
+                                _arg(s, torch.uint8, mx_scale_bytes(n, K), "s"), T, n, K, _arg(y, bf, T * n, "y"),
+                                _stream()), "mx_linear_e2m1")
+
+
+def few_args(k, wr, w1, w3, w2, ws, w1s=None, w3s=None, w2s=None):
+    """A FewArgs with the weights' and the workspace's fields filled in and
+    checked; moe_few_fwd fills in the rest.  The caller keeps the tensors."""
+    E, d = _matrix(wr, "wr")
+    dt = wr.dtype
+    if not isinstance(w1, torch.Tensor) or w1.dim() != 3:
+        raise MoeError("w1 must be [E, h, d], or packed [E, h, d/2]")
+    h = w1.shape[1]
+    a = FewArgs(d=d, E=E, k=k, h=h, dt=_dt(wr), wt=_dt(wr))
+    a.wr = _arg(wr, dt, E * d, "wr")
+    packed = w1.dtype == torch.uint8
+    if packed:
+        a.wt = MOE_E2M1
+        n, wdt = E * h * d // 2, torch.uint8
+        for name, t, rows, cols in (("w1s", w1s, E * h, d), ("w3s", w3s, E * h, d), ("w2s", w2s, E * d, h)):
+            if t is None:
+                raise MoeError(f"{name} is needed with packed weights")
+            setattr(a, name, _arg(t, torch.uint8, mx_scale_bytes(rows, cols), name))
+    else:
+        n, wdt = E * h * d, dt
+        if w1s is not None or w3s is not None or w2s is not None:
+            raise MoeError("scales go with packed weights only")
+    for name, t, shape in (("w1", w1, (E, h, d)), ("w3", w3, (E, h, d)), ("w2", w2, (E, d, h))):
+        want = (shape[0], shape[1], shape[2] // 2) if packed else shape
+        if not isinstance(t, torch.Tensor) or tuple(t.shape) != want:
+            raise MoeError(f"{name} must be {list(want)}")
+        setattr(a, name, _arg(t, wdt, n, name))
+    a.ws, a.ws_bytes = _ws_arg(ws), ws.numel()
+    return a
+
+
+def moe_few_fwd(a, x, y, topk_idx=None, topk_w=None, n_live=None):
+    """The layer for the few tokens x [T, d] (a: few_args(...)) into y [T, d]."""
+    T, d = _matrix(x, "x")
+    if d != a.d:
+        raise MoeError(f"x must have {a.d} columns, got {d}")
+    dt = torch.float32 if a.dt == MOE_F32 else torch.bfloat16
+    a.T = T
+    a.x, a.y = _arg(x, dt, T * d, "x"), _arg(y, dt, T * d, "y")
+    a.topk_idx = _arg(topk_idx, torch.int32, T * a.k, "topk_idx")
+    a.topk_w = _arg(topk_w, torch.float32, T * a.k, "topk_w")
+    a.n_live = _arg(n_live, torch.int32, 1, "n_live")
+    _check(lib().moe_few_fwd(ctypes.byref(a), _stream()), "moe_few_fwd")

@@ -19,7 +19,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB_NAME = "libtrg_moe.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
-SOURCES = ["api.hip", "route.hip", "permute.hip", "router.hip", "gemm_bf16.hip", "ggemm.hip", "ggemm_mx.hip", "mx.hip", "gemm_f32.hip", "balance.hip"]
+SOURCES = ["api.hip", "route.hip", "permute.hip", "router.hip", "gemm_bf16.hip", "ggemm.hip", "ggemm_mx.hip", "mx.hip", "gemm_f32.hip", "balance.hip",
+           "norm.hip", "mx4.hip", "few.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

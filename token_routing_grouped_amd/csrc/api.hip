@@ -658,4 +658,163 @@ moe_status_t moe_grouped_gemm_bwd_mx_parts(const moe_mx_bwd_args* a, unsigned pa
   return ggemm_bwd_mx_impl("moe_grouped_gemm_bwd_mx_parts", a, parts, stream);
 }
 
+// ---- norm ------------------------------------------------------------------
+static moe_status_t check_norm_dims(const char* fn, int T, int d, int dt) {
+  TRY(check_dt(fn, dt));
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T must be >= 0", fn);
+  TRY(check_row(fn, "d", d, dt));
+  // a row is held in registers: 16 waves of 64 lanes, eight 16-byte pieces each
+  if ((long)d * esize(dt) > 16L * 64 * 8 * 16)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: d * element size must be at most 128 KiB", fn);
+  return MOE_OK;
+}
+
+moe_status_t moe_rmsnorm_fwd(const void* x, const void* res, const void* w, int T, int d, float eps, int dt, void* s,
+                             void* y, uint8_t* q, uint8_t* qs, float* rstd, void* stream) {
+  const char* fn = "moe_rmsnorm_fwd";
+  TRY(check_norm_dims(fn, T, d, dt));
+  if (!(eps >= 0.0f) || eps > 1e30f) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  if (T == 0) return ok();
+  if ((q == nullptr) != (qs == nullptr)) return fail(MOE_ERR_INVALID_ARG, "%s: q and qs go together", fn);
+  if (y == nullptr && q == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: nothing to write (y and q are null)", fn);
+  if (q != nullptr && d % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: q needs d %% 32 == 0", fn);
+  TRY(check_ptrs(fn, {{"x", x}, {"w", w}}));
+  TRY(check_optional_aligned(fn, {{"res", res}, {"s", s}, {"y", y}, {"q", q}}));
+  if (((uintptr_t)qs & 3) || ((uintptr_t)rstd & 3))
+    return fail(MOE_ERR_ALIGNMENT, "%s: qs and rstd must be 4-byte aligned", fn);
+  if (s != nullptr && s == y) return fail(MOE_ERR_INVALID_ARG, "%s: s and y must be different buffers", fn);
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_rmsnorm_fwd(x, res, w, T, d, eps, dt == MOE_BF16, s, y, q, qs, rstd,
+                                                (hipStream_t)stream));
+}
+
+size_t moe_rmsnorm_bwd_workspace_size(int T, int d) {
+  if (T < 0 || d < 1) return 0;
+  return trg::rmsnorm_bwd_ws_bytes(T, d);
+}
+
+moe_status_t moe_rmsnorm_bwd(const void* dy, const void* ds, const void* s, const void* w, const float* rstd, int T,
+                             int d, int dt, void* dx, void* dw, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_rmsnorm_bwd";
+  TRY(check_norm_dims(fn, T, d, dt));
+  TRY(check_ptrs(fn, {{"w", w}, {"dw", dw}}));
+  if (T > 0) {
+    TRY(check_ptrs(fn, {{"dy", dy}, {"s", s}, {"dx", dx}}));
+    TRY(check_optional_aligned(fn, {{"ds", ds}}));
+    if (rstd == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: rstd is null", fn);
+    if ((uintptr_t)rstd & 3) return fail(MOE_ERR_ALIGNMENT, "%s: rstd must be 4-byte aligned", fn);
+  }
+  const size_t need = trg::rmsnorm_bwd_ws_bytes(T, d);
+  if (ws == nullptr || ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, ws_bytes);
+  if (!aligned16(ws)) return fail(MOE_ERR_ALIGNMENT, "%s: ws is not 16-byte aligned", fn);
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_rmsnorm_bwd(dy, ds, s, w, rstd, T, d, dt == MOE_BF16, dx, dw, ws,
+                                                (hipStream_t)stream));
+}
+
+// ---- 4-bit weights -----------------------------------------------------------
+static moe_status_t check_e2m1(const char* fn, long rows, long cols, const uint8_t* q, const uint8_t* s) {
+  if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: rows must be >= 0", fn);
+  if (cols <= 0 || cols % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: cols must be a positive multiple of 32", fn);
+  // one thread per 16 bytes of fp32 values, in whole 128-value chunks
+  if (rows * ((cols + 127) / 128) >= (1L << 27)) return fail(MOE_ERR_UNSUPPORTED, "%s: problem too large", fn);
+  if (rows == 0) return MOE_OK;
+  TRY(check_ptrs(fn, {{"q", q}}));
+  if (s == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: s is null", fn);
+  if ((uintptr_t)s & 3) return fail(MOE_ERR_ALIGNMENT, "%s: s is not 4-byte aligned", fn);
+  return MOE_OK;
+}
+
+moe_status_t mx_quantize_e2m1(const void* in, int dt, int rows, int cols, uint8_t* q, uint8_t* s, void* stream) {
+  const char* fn = "mx_quantize_e2m1";
+  TRY(check_dt(fn, dt));
+  TRY(check_e2m1(fn, rows, cols, q, s));
+  if (rows == 0) return ok();
+  TRY(check_ptrs(fn, {{"in", in}}));
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_quantize_e2m1(in, dt == MOE_BF16, rows, cols, q, s, (hipStream_t)stream));
+}
+
+moe_status_t mx_dequantize_e2m1(const uint8_t* q, const uint8_t* s, int dt, int rows, int cols, void* out,
+                                void* stream) {
+  const char* fn = "mx_dequantize_e2m1";
+  TRY(check_dt(fn, dt));
+  TRY(check_e2m1(fn, rows, cols, q, s));
+  if (rows == 0) return ok();
+  TRY(check_ptrs(fn, {{"out", out}}));
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_dequantize_e2m1(q, s, dt == MOE_BF16, rows, cols, out, (hipStream_t)stream));
+}
+
+// ---- a few tokens --------------------------------------------------------------
+constexpr int kFewTokens = 64;     // a token is a bit of a 64-bit mask
+constexpr int kFewWidth = 65536;   // keeps row bytes and grids far inside 32 bits
+
+moe_status_t mx_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
+                            void* stream) {
+  const char* fn = "mx_linear_e2m1";
+  if (T < 0 || T > kFewTokens) return fail(MOE_ERR_INVALID_ARG, "%s: T must be in [0, %d]", fn, kFewTokens);
+  if (n < 1) return fail(MOE_ERR_INVALID_ARG, "%s: n must be >= 1", fn);
+  if (K > kFewWidth) return fail(MOE_ERR_UNSUPPORTED, "%s: K must be at most %d", fn, kFewWidth);
+  TRY(check_e2m1(fn, n, K, q, s));
+  if (T == 0) return ok();
+  TRY(check_ptrs(fn, {{"x", x}, {"y", y}}));
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_linear_e2m1(x, q, s, T, n, K, y, (hipStream_t)stream));
+}
+
+static moe_status_t check_few_dims(const char* fn, int T, int d, int E, int k, int h) {
+  if (T < 0 || T > kFewTokens) return fail(MOE_ERR_INVALID_ARG, "%s: T must be in [0, %d]", fn, kFewTokens);
+  if (E < 1 || E > 1024) return fail(MOE_ERR_INVALID_ARG, "%s: E must be in [1, 1024]", fn);
+  if (k < 1 || k > 32) return fail(MOE_ERR_INVALID_ARG, "%s: k must be in [1, 32]", fn);
+  if (k > E) return fail(MOE_ERR_INVALID_ARG, "%s: k (%d) > E (%d)", fn, k, E);
+  if (d < 1 || h < 1) return fail(MOE_ERR_INVALID_ARG, "%s: d and h must be positive", fn);
+  if (d > kFewWidth || h > kFewWidth)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: d and h must be at most %d", fn, kFewWidth);
+  return MOE_OK;
+}
+
+size_t moe_few_workspace_size(int T, int d, int E, int k, int h) {
+  if (check_few_dims("moe_few_workspace_size", T, d, E, k, h) != MOE_OK) return 0;
+  return trg::few_ws_bytes(T, E, k, h);
+}
+
+moe_status_t moe_few_fwd(const moe_few_args* a, void* stream) {
+  const char* fn = "moe_few_fwd";
+  if (!a) return fail(MOE_ERR_INVALID_ARG, "%s: args is null", fn);
+  TRY(check_dt(fn, a->dt));
+  TRY(check_few_dims(fn, a->T, a->d, a->E, a->k, a->h));
+  const bool w4 = a->wt == MOE_E2M1;
+  if (!w4 && a->wt != a->dt)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: wt must be dt or MOE_E2M1", fn);
+  if (w4 && a->dt != MOE_BF16) return fail(MOE_ERR_UNSUPPORTED, "%s: MOE_E2M1 weights need dt MOE_BF16", fn);
+  if (w4 && (a->d % 32 != 0 || a->h % 32 != 0))
+    return fail(MOE_ERR_INVALID_ARG, "%s: MOE_E2M1 weights need d %% 32 == 0 and h %% 32 == 0", fn);
+  TRY(check_row(fn, "d", a->d, a->dt));
+  TRY(check_row(fn, "h", a->h, a->dt));
+  if (a->T == 0) return ok();
+  TRY(check_ptrs(fn, {{"x", a->x}, {"wr", a->wr}, {"w1", a->w1}, {"w3", a->w3}, {"w2", a->w2}, {"y", a->y}}));
+  TRY(check_optional_aligned(fn, {{"topk_idx", a->topk_idx}, {"topk_w", a->topk_w}}));
+  if (w4) {
+    for (auto& p : {std::make_pair("w1s", a->w1s), std::make_pair("w3s", a->w3s), std::make_pair("w2s", a->w2s)}) {
+      if (p.second == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: %s is null", fn, p.first);
+      if ((uintptr_t)p.second & 3) return fail(MOE_ERR_ALIGNMENT, "%s: %s is not 4-byte aligned", fn, p.first);
+    }
+  }
+  if ((uintptr_t)a->n_live & 3) return fail(MOE_ERR_ALIGNMENT, "%s: n_live is not 4-byte aligned", fn);
+  const size_t need = trg::few_ws_bytes(a->T, a->E, a->k, a->h);
+  if (a->ws == nullptr || a->ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, a->ws_bytes);
+  if (!aligned16(a->ws)) return fail(MOE_ERR_ALIGNMENT, "%s: ws is not 16-byte aligned", fn);
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_few_fwd(*a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -43,6 +43,22 @@ size_t balance_ws_bytes(int T, int E);
 hipError_t launch_balance(const float* probs, const int* counts, int T, int E, int k, float alpha, float* stats,
                           float* aux_g, float* mean_probs, void* ws, hipStream_t s);
 
+// norm in front of the layer
+hipError_t launch_rmsnorm_fwd(const void* x, const void* res, const void* w, int rows, int d, float eps, bool bf16,
+                              void* s, void* y, uint8_t* q, uint8_t* qs, float* rstd, hipStream_t st);
+size_t rmsnorm_bwd_ws_bytes(int rows, int d);
+hipError_t launch_rmsnorm_bwd(const void* dy, const void* ds, const void* s, const void* w, const float* rstd, int rows,
+                              int d, bool bf16, void* dx, void* dw, void* ws, hipStream_t st);
+
+// the layer for a few tokens, and 4-bit weights
+size_t few_ws_bytes(int T, int E, int k, int h);
+hipError_t launch_few_fwd(const moe_few_args& a, hipStream_t st);
+hipError_t launch_quantize_e2m1(const void* in, bool bf16, int rows, int cols, uint8_t* q, uint8_t* s, hipStream_t st);
+hipError_t launch_dequantize_e2m1(const uint8_t* q, const uint8_t* s, bool bf16, int rows, int cols, void* out,
+                                  hipStream_t st);
+hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
+                              hipStream_t st);
+
 // grouped GEMMs
 size_t ggemm_ws_bytes(int E, int R, int d, int h);
 hipError_t launch_ggemm_fwd(const void* xp, const void* w1, const void* w3, const void* w2, const int* offsets,

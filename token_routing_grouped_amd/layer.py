@@ -336,3 +336,84 @@ class MoELayerGPU:
     def step(self, x, wr, w1, w3, w2, dy, forced_idx=None):
         self.forward(x, wr, w1, w3, w2, forced_idx)
         self.backward(dy, x, wr, w1, w3, w2)
+
+
+class MoEDecodeGPU:
+    """The layer's forward for a few tokens (at most T <= 64 at a time: decode
+    steps, short drafts) through moe_few_fwd, for one set of weights.
+
+    wr [E,d]; w1, w3 [E,h,d], w2 [E,d,h] in wr's type, or packed 4-bit (uint8
+    [E,h,d/2], [E,d,h/2]) with their scales w1s, w3s, w2s (mx_quantize_e2m1 of
+    the [E*h,d] and [E*d,h] matrices).  The tensors are the caller's: they are
+    kept by reference and read in place at every call, so they may be updated
+    in place but not moved.  norm_w [d]: forward() then takes the layer's input
+    before its norm, adds the residual and norms it first (moe_rmsnorm_fwd).
+
+    One object is one set of buffers: its calls belong on one stream.
+    """
+
+    def __init__(self, T: int, k: int, wr, w1, w3, w2, w1s=None, w3s=None, w2s=None, norm_w=None, eps: float = 1e-6):
+        E, d = wr.shape
+        dev = wr.device
+        self.T, self.d, self.E, self.k, self.h = T, d, E, k, w1.shape[1]
+        self.eps, self.norm_w = eps, norm_w
+        self.weights = (wr, w1, w3, w2, w1s, w3s, w2s)
+        nbytes = _abi.moe_few_workspace_size(T, d, E, k, self.h)
+        if nbytes == 0:
+            raise _abi.MoeError(_abi.lib().moe_last_error_string().decode())
+        self.ws = _abi.workspace(nbytes, dev)
+        self._args = _abi.few_args(k, wr, w1, w3, w2, self.ws, w1s, w3s, w2s)
+        self.y = torch.empty(T, d, dtype=wr.dtype, device=dev)
+        self.topk_idx = torch.empty(T, k, dtype=torch.int32, device=dev)
+        self.topk_w = torch.empty(T, k, dtype=torch.float32, device=dev)
+        self.s = self.xn = None
+        if norm_w is not None:
+            self.s, self.xn = torch.empty_like(self.y), torch.empty_like(self.y)
+
+    def forward(self, x, res=None, n_live=None):
+        """y [t,d] of x [t,d], t <= T, in self.y (with topk_idx, topk_w and,
+        with norm_w, the residual stream x + res in self.s).  n_live: a device
+        int32 with the number of tokens that are there; rows of y, topk_idx
+        and topk_w behind them are left as they were."""
+        t = x.shape[0]
+        if t > self.T:
+            raise _abi.MoeError(f"{t} tokens, but the buffers are for {self.T}")
+        y, idx, w, s, xn = self.y, self.topk_idx, self.topk_w, self.s, self.xn
+        if t != self.T:
+            y, idx, w = y[:t], idx[:t], w[:t]
+            if s is not None:
+                s, xn = s[:t], xn[:t]
+        if self.norm_w is not None:
+            _abi.moe_rmsnorm_fwd(x, self.norm_w, self.eps, xn, res=res, s=s)
+            x = xn
+        elif res is not None:
+            raise _abi.MoeError("a residual goes with norm_w")
+        _abi.moe_few_fwd(self._args, x, y, idx, w, n_live)
+        return y
+
+
+class MoEBlockGPU:
+    """The layer with its norm, for training: s = x + res, y = layer(rmsnorm(s)).
+
+    layer: a MoELayerGPU, whose weights stay the caller's.  forward() returns y
+    and leaves the residual stream in self.s; backward() takes y's gradient and
+    the one that reaches s from further on, and returns the gradient of x and
+    res (the same tensor); the norm weight's is in self.dnorm_w.
+    """
+
+    def __init__(self, layer: MoELayerGPU, eps: float = 1e-6):
+        self.layer, self.eps = layer, eps
+        T, d, dev = layer.T, layer.d, layer.y.device
+        e = lambda *n, dt=layer.dtype: torch.empty(*n, dtype=dt, device=dev)
+        self.s, self.xn, self.dx, self.dnorm_w = e(T, d), e(T, d), e(T, d), e(d)
+        self.rstd = e(T, dt=torch.float32)
+        self.ws_norm = _abi.workspace(_abi.moe_rmsnorm_bwd_workspace_size(T, d), dev)
+
+    def forward(self, x, norm_w, wr, w1, w3, w2, res=None):
+        _abi.moe_rmsnorm_fwd(x, norm_w, self.eps, self.xn, res=res, s=self.s, rstd=self.rstd)
+        return self.layer.forward(self.xn, wr, w1, w3, w2)
+
+    def backward(self, dy, norm_w, wr, w1, w3, w2, ds=None):
+        dxn = self.layer.backward(dy, self.xn, wr, w1, w3, w2)
+        _abi.moe_rmsnorm_bwd(dxn, self.s, norm_w, self.rstd, self.dx, self.dnorm_w, self.ws_norm, ds=ds)
+        return self.dx
