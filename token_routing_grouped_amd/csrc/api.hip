@@ -782,7 +782,7 @@ static moe_status_t check_few_dims(const char* fn, int T, int d, int E, int k, i
 
 size_t moe_few_workspace_size(int T, int d, int E, int k, int h) {
   if (check_few_dims("moe_few_workspace_size", T, d, E, k, h) != MOE_OK) return 0;
-  return trg::few_ws_bytes(T, E, k, h);
+  return trg::few_ws_bytes(T, d, E, k, h);
 }
 
 moe_status_t moe_few_fwd(const moe_few_args* a, void* stream) {
@@ -808,7 +808,7 @@ moe_status_t moe_few_fwd(const moe_few_args* a, void* stream) {
     }
   }
   if ((uintptr_t)a->n_live & 3) return fail(MOE_ERR_ALIGNMENT, "%s: n_live is not 4-byte aligned", fn);
-  const size_t need = trg::few_ws_bytes(a->T, a->E, a->k, a->h);
+  const size_t need = trg::few_ws_bytes(a->T, a->d, a->E, a->k, a->h);
   if (a->ws == nullptr || a->ws_bytes < need)
     return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, a->ws_bytes);
   if (!aligned16(a->ws)) return fail(MOE_ERR_ALIGNMENT, "%s: ws is not 16-byte aligned", fn);
