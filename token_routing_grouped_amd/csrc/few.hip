@@ -57,15 +57,17 @@ int hid_rows(int T, int E, int k) {
   const int R = T * k, S = R < E ? R : E;
   return in_prologue(T, k) ? S * T : R;
 }
-int logit_parts(int d, int es);
-int down_parts(int T, int d);
+// Partial sums that the router's logits come in: its E / 16 row tiles alone
+// would leave most of the chip idle.
+constexpr int kLogitParts = 8;
 
 struct FewLayout {
-  size_t n_active, slots, gate, logits, hid, part, bytes;
+  size_t n_active, slots, gate, logits, hid, pos, yp, bytes;
 };
 
 FewLayout few_layout(int T, int d, int E, int k, int h) {
   const size_t R = (size_t)T * k, S = R < (size_t)E ? R : (size_t)E;
+  const bool pro = in_prologue(T, k);
   FewLayout l;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -76,10 +78,10 @@ FewLayout few_layout(int T, int d, int E, int k, int h) {
   l.n_active = take(sizeof(int));
   l.slots = take(S * sizeof(FewSlot));
   l.gate = take(R * sizeof(float));
-  l.logits = take((size_t)logit_parts(d, 4) * T * E * sizeof(float));  // fp32 rows have the most lines
+  l.logits = take((size_t)kLogitParts * T * E * sizeof(float));
   l.hid = take((size_t)hid_rows(T, E, k) * h * sizeof(float));         // fp32, or the hi and lo bf16 halves
-  const int dp = down_parts(T, d);
-  l.part = take(dp > 1 ? (size_t)dp * T * d * sizeof(float) : 0);
+  l.pos = take(pro ? 0 : R * sizeof(int));
+  l.yp = take(pro ? 0 : R * d * sizeof(float));
   l.bytes = at;
   return l;
 }
@@ -131,21 +133,46 @@ TRG_DEV f32x4_t mma_piece(uint4 w, float sc, const uint4* x, f32x4_t acc) {
   }
 }
 
-TRG_DEV uint4 zero16() { return make_uint4(0, 0, 0, 0); }
+// The same with an operand in P parts (2: x and y are its halves): a 4-bit
+// piece is decoded once for both.
+template <int WT, int P>
+TRG_DEV f32x4_t mma_parts(uint4 w, float sc, const uint4* x, const uint4* y, f32x4_t acc) {
+  if constexpr (WT == kE2M1) {
+    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bf16x8_t a = e2m1x8(c[i], sc);
+      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf16x8(x[i]), acc, 0, 0, 0);
+      if constexpr (P == 2) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, as_bf16x8(y[i]), acc, 0, 0, 0);
+    }
+    return acc;
+  } else {
+    acc = mma_piece<WT>(w, sc, x, acc);
+    return P == 2 ? mma_piece<WT>(w, sc, y, acc) : acc;
+  }
+}
 
-// A lane's place in a weight matrix of n rows with rb bytes a row.
-struct WRow {
-  const char* p;        // its row
-  const uint8_t* s;     // E2M1: its row's scales in chunk 0
-  long sstride;         // E2M1: bytes from a 128-value chunk's scales to the next one's
+// A lane's place in a weight matrix: uniform bases (of an expert's matrix, and of
+// the whole matrix's scales) and 32-bit offsets (the caller's sizes keep an
+// expert's matrix and all scales of one under 2 GiB), so that a row costs two
+// registers.
+struct WBase {
+  const char* p;
+  const uint8_t* s;   // E2M1: scales
+  uint32_t first;     // E2M1: this matrix's first row among the n rows of the scales
+  uint32_t sstride;   // E2M1: bytes from a 128-value chunk's scales to the next one's, n * 4
 };
+struct WRow {
+  uint32_t off, soff;
+};
+// Matrix e of E matrices of `rows` rows of rb bytes.
 template <int WT>
-TRG_DEV WRow w_row(const void* w, const uint8_t* ws, long n, long row, int rb) {
-  WRow r;
-  r.p = (const char*)w + row * rb;
-  r.s = WT == kE2M1 ? ws + row * 4 : nullptr;
-  r.sstride = n * 4;
-  return r;
+TRG_DEV WBase w_base(const void* w, const uint8_t* ws, int e, int E, int rows, int rb) {
+  return {(const char*)w + (long)e * rows * rb, ws, (uint32_t)e * (uint32_t)rows, (uint32_t)E * (uint32_t)rows * 4u};
+}
+template <int WT>
+TRG_DEV WRow w_row(const WBase& b, int row, int rb) {
+  return {(uint32_t)row * (uint32_t)rb, WT == kE2M1 ? (b.first + (uint32_t)row) * 4u : 0u};
 }
 
 // One step's share of a weight row: two 16-byte pieces and their scale bytes.
@@ -158,17 +185,17 @@ struct WStep {
 // loaded from the row's last piece: every load is unconditional, so that the
 // compiler can count which of them it has to wait for.
 template <int WT>
-TRG_DEV WStep w_load(const WRow& r, int c, int q, int rb) {
+TRG_DEV WStep w_load(const WBase& b, const WRow& r, int c, int q, int rb) {
   WStep o;
   const int off = c * 128 + q * 32, last = rb - 16;
-  o.v[0] = *(const uint4*)(r.p + min(off, last));
-  o.v[1] = *(const uint4*)(r.p + min(off + 16, last));
+  o.v[0] = *(const uint4*)(b.p + (r.off + (uint32_t)min(off, last)));
+  o.v[1] = *(const uint4*)(b.p + (r.off + (uint32_t)min(off + 16, last)));
   o.sb = 0;
   if constexpr (WT == kE2M1) {
     // block b = off / 16, its byte in chunk b / 4; b is even, so both bytes of
     // the step are in one chunk (the second may be a place past the last block)
     const int bk = min(off, last) / 16 & ~1;
-    o.sb = *(const uint16_t*)(r.s + (long)(bk >> 2) * r.sstride + (bk & 3));
+    o.sb = *(const uint16_t*)(b.s + (r.soff + (uint32_t)(bk >> 2) * b.sstride + (uint32_t)(bk & 3)));
   }
   return o;
 }
@@ -190,15 +217,17 @@ template <int WT>
 struct XStep {
   uint4 v[2][Piece<WT>::kX];
 };
+// Piece i of the operand; xb: a uniform base, xo: the lane's column's row.
 template <int WT>
-TRG_DEV void x_load(const char* xr, int c, int q, int rb, XStep<WT>& o) {
-  const int off = c * 128 + q * 32;
+TRG_DEV void x_piece(const char* xb, uint32_t xo, int c, int q, int i, int rb, uint4* x) {
+  const char* p = xb + (xo + (uint32_t)(min(c * 128 + q * 32 + 16 * i, rb - 16) / 16 * (Piece<WT>::kK * Piece<WT>::kXE)));
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const char* p = xr + min(off + 16 * i, rb - 16) / 16 * (Piece<WT>::kK * Piece<WT>::kXE);
-#pragma unroll
-    for (int j = 0; j < Piece<WT>::kX; ++j) o.v[i][j] = *(const uint4*)(p + j * 16);
-  }
+  for (int j = 0; j < Piece<WT>::kX; ++j) x[j] = *(const uint4*)(p + j * 16);
+}
+template <int WT>
+TRG_DEV void x_load(const char* xb, uint32_t xo, int c, int q, int rb, XStep<WT>& o) {
+  x_piece<WT>(xb, xo, c, q, 0, rb, o.v[0]);
+  x_piece<WT>(xb, xo, c, q, 1, rb, o.v[1]);
 }
 template <int WT>
 TRG_DEV f32x4_t mma_step(const WStep& w, const XStep<WT>& x, f32x4_t acc) {
@@ -209,66 +238,61 @@ TRG_DEV f32x4_t mma_step(const WStep& w, const XStep<WT>& x, f32x4_t acc) {
 }
 
 // ---- products of NM 16-row tiles with NT * 16 columns --------------------------
-// acc[m][n] over lines c0, c0 + step, ... < c1 of the rows, U lines a batch.  A
-// batch's weights are loaded while the one before is multiplied; the tokens'
-// operand comes from the caches and is loaded where it is used.  With one tile
-// of columns only the lanes of columns that are `on` load it (a few tokens are
-// a few lanes); the others' registers hold anything: columns do not mix, and
-// theirs are not stored.
-template <int WT, int NM, int NT, int U>
-TRG_DEV void stream_tile(const WRow* wr, const char* const* xr, bool on, int rb, int c0, int c1, int step, int q,
-                         f32x4_t (*acc)[NT]) {
-  if (c0 >= c1) return;
+// acc[m][n] over lines c0, c0 + step, ... < c1 of the rows, U lines at a time:
+// all their weights are loaded (from HBM), then the tokens' operand (P parts,
+// xpart bytes apart; from the caches), XB pieces at a time where the registers
+// do not hold more.  The waves of a CU hide each other's loads: NM * U * 2 KB
+// a wave in flight is several times what HBM's latency needs.
+// Tile m is rows wr[m] of matrix wb[m % NB], NB bases.
+// With one tile of columns only the lanes of columns that are `on` load it (a
+// few tokens are a few lanes); the others' registers hold anything: columns do
+// not mix, and theirs are not stored.
+template <int WT, int NB, int NM, int NT, int U, int P>
+TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const uint32_t* xo, long xpart, bool on,
+                         int rb, int c0, int c1, int step, int q, f32x4_t (*acc)[NT]) {
+  constexpr int KX = Piece<WT>::kX;
+  constexpr int XB = 2 * U * P * KX <= 8 ? 2 * U : 1;  // pieces of the operand at once: at most 32 registers
   const int past = (rb + 127) >> 7;  // a line that is past every row's end
-  WStep w[U][NM];
-  auto line = [&](int c) { return c < c1 ? c : past; };
-  auto load_w = [&](int c, WStep (*o)[NM]) {
+  for (; c0 < c1; c0 += step * U) {
+    WStep w[U][NM];
+    int line[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < U; ++u) {
+      line[u] = c0 + u * step < c1 ? c0 + u * step : past;
 #pragma unroll
-      for (int m = 0; m < NM; ++m) o[u][m] = w_load<WT>(wr[m], line(c + u * step), q, rb);
-  };
-  auto load_x = [&](int c, int n, XStep<WT>* x) {
-#pragma unroll
-    for (int u = 0; u < U; ++u) x_load<WT>(xr[n], line(c + u * step), q, rb, x[u]);
-  };
-  auto multiply = [&](int c, int n, XStep<WT>* x) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int m = 0; m < NM; ++m) acc[m][n] = mma_step<WT>(w[u][m], x[u], acc[m][n]);
-  };
-  auto mask_w = [&](int c) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int m = 0; m < NM; ++m) w_mask<WT>(w[u][m], line(c + u * step), q, rb);
-  };
-  load_w(c0, w);
-  for (; c0 + step * U < c1; c0 += step * U) {
-    WStep wn[U][NM];
-    XStep<WT> x[U];
-    if (NT > 1 || on) load_x(c0, 0, x);
-    load_w(c0 + step * U, wn);
-    multiply(c0, 0, x);  // not the last batch: every line of it is inside
-#pragma unroll
-    for (int n = 1; n < NT; ++n) {
-      load_x(c0, n, x);
-      multiply(c0, n, x);
+      for (int m = 0; m < NM; ++m) w[u][m] = w_load<WT>(wb[m % NB], wr[m], line[u], q, rb);
     }
+    const bool whole = (line[U - 1] + 1) * 128 <= rb;  // lines rise, so all of them are
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int m = 0; m < NM; ++m) w[u][m] = wn[u][m];
-  }
-  XStep<WT> x[U];
-  if (NT > 1 || on) load_x(c0, 0, x);
-  mask_w(c0);
-  multiply(c0, 0, x);
+      for (int b = 0; b < 2 * U; b += XB) {
+        uint4 x[XB][P][KX];
+        if (NT > 1 || on) {
 #pragma unroll
-  for (int n = 1; n < NT; ++n) {
-    load_x(c0, n, x);
-    multiply(c0, n, x);
+          for (int i = 0; i < XB; ++i)
+#pragma unroll
+            for (int p = 0; p < P; ++p) x_piece<WT>(xb + p * xpart, xo[n], line[(b + i) / 2], q, (b + i) & 1, rb, x[i][p]);
+        }
+        if (n == 0 && b == 0 && !whole) {
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int m = 0; m < NM; ++m) w_mask<WT>(w[u][m], line[u], q, rb);
+        }
+#pragma unroll
+        for (int i = 0; i < XB; ++i) {
+          const int u = (b + i) / 2, z = (b + i) & 1;
+#pragma unroll
+          for (int m = 0; m < NM; ++m)
+            acc[m][n] = mma_parts<WT, P>(w[u][m].v[z], WT == kE2M1 ? e8m0((w[u][m].sb >> (8 * z)) & 255u) : 0.f,
+                                         x[i][0], x[i][P - 1], acc[m][n]);
+          // a piece's codes are decoded when it is used, not ahead
+          if (WT == kE2M1) __builtin_amdgcn_sched_barrier(0);
+        }
+        // or every block's operand is loaded at once, into scratch
+        if (XB < 2 * U || NT > 1) __builtin_amdgcn_sched_barrier(0);
+      }
   }
 }
 
@@ -302,18 +326,19 @@ __global__ __launch_bounds__(kThreads, NM* NT > 4 ? 2 : 4) void few_linear_kerne
   const int live = live_tokens(n_live, T);
   const int row0 = blockIdx.x * (16 * NM);
   const int c0 = blockIdx.y * part_lines, c1 = min((rb + 127) >> 7, c0 + part_lines);
+  const WBase wb[1] = {w_base<WT>(w, ws, 0, 1, n, rb)};
   WRow wr[NM];
 #pragma unroll
-  for (int m = 0; m < NM; ++m) wr[m] = w_row<WT>(w, ws, n, min(row0 + m * 16 + r, n - 1), rb);
-  const char* xr[NT];
+  for (int m = 0; m < NM; ++m) wr[m] = w_row<WT>(wb[0], min(row0 + m * 16 + r, n - 1), rb);
+  uint32_t xo[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xr[i] = x + (long)min(i * 16 + r, T - 1) * xb;
+  for (int i = 0; i < NT; ++i) xo[i] = (uint32_t)min(i * 16 + r, T - 1) * (uint32_t)xb;
   f32x4_t acc[NM][NT];
 #pragma unroll
   for (int m = 0; m < NM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0, 0, 0, 0};
-  stream_tile<WT, NM, NT, U>(wr, xr, r < live, rb, c0 + wv, c1, kWaves, q, acc);
+  stream_tile<WT, 1, NM, NT, U, 1>(wb, wr, x, xo, 0, r < live, rb, c0 + wv, c1, kWaves, q, acc);
 #pragma unroll
   for (int m = 0; m < NM; ++m)
 #pragma unroll
@@ -347,26 +372,41 @@ TRG_DEV uint32_t wave_max_u32(uint32_t v) {
 
 // One wave routes token t: the k largest logits, ties to the lower expert, a
 // NaN never before a number (moe_route's rules), and their softmax values.
-// Logits come as `parts` partial sums [parts][T][E], added in order.  A logit
+// Logits come as partial sums [kLogitParts][T][E], added in order.  A logit
 // becomes a 32-bit key that orders like it (0 is below every key), so a round
 // is one wave maximum and the first lane of the first register that holds it:
 // expert e is lane e % 64, register e / 64.  sel, selw: this token's k places.
 template <int EPL>
-TRG_DEV void route_token(const float* __restrict__ logits, int parts, int T, int E, int k, int t, int lane, int* sel,
-                         float* selw, unsigned long long* mask) {
+TRG_DEV void route_token(const float* __restrict__ logits, int T, int E, int k, int t, int lane, int* sel, float* selw,
+                         unsigned long long* mask) {
   float v[EPL], p[EPL];
   uint32_t key[EPL];
   float m = -INFINITY, s = 0.f;
+  // all parts of eight registers' experts are in flight at once: one by one,
+  // each group would wait for its own trip past L2 (another XCD wrote them)
+  constexpr int B = EPL < 8 ? EPL : 8;
+#pragma unroll
+  for (int i0 = 0; i0 < EPL; i0 += B) {
+    float raw[B][kLogitParts];
+    const uint32_t row = (uint32_t)t * (uint32_t)E, plane = (uint32_t)T * (uint32_t)E;
+#pragma unroll
+    for (int i = 0; i < B; ++i)
+#pragma unroll
+      for (int a = 0; a < kLogitParts; ++a)
+        raw[i][a] = logits[row + (uint32_t)a * plane + (uint32_t)min(lane + 64 * (i0 + i), E - 1)];
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      v[i0 + i] = raw[i][0];
+#pragma unroll
+      for (int a = 1; a < kLogitParts; ++a) v[i0 + i] += raw[i][a];
+    }
+  }
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     const int e = lane + 64 * i;
-    float x = -INFINITY;
-    if (e < E) {
-      const float* L = logits + (long)t * E + e;
-      x = L[0];
-      for (int a = 1; a < parts; ++a) x += L[(long)a * T * E];
-    }
-    v[i] = (x != x) ? -INFINITY : x;
+    const float x = v[i];
+    v[i] = (x != x || e >= E) ? -INFINITY : x;
     m = fmaxf(m, v[i]);
     const uint32_t b = __float_as_uint(v[i] + 0.0f);  // -0 and 0 are equal
     key[i] = e < E ? ((b & 0x80000000u) ? ~b : b | 0x80000000u) : 0u;
@@ -406,11 +446,11 @@ TRG_DEV void route_token(const float* __restrict__ logits, int parts, int T, int
 // entries): one workgroup, a wave a token at a time; then the chosen experts'
 // token masks are compacted, in expert order, into slots.
 template <int EPL>
-__global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict__ logits, int parts, int T, int E,
-                                                         int k, const int* __restrict__ n_live,
-                                                         int* __restrict__ idx_out, float* __restrict__ w_out,
-                                                         int* __restrict__ n_active, FewSlot* __restrict__ slots,
-                                                         float* __restrict__ gate) {
+__global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict__ logits, int T, int E, int k,
+                                                         const int* __restrict__ n_live, int* __restrict__ idx_out,
+                                                         float* __restrict__ w_out, int* __restrict__ n_active,
+                                                         FewSlot* __restrict__ slots, float* __restrict__ gate,
+                                                         int* __restrict__ pos_out) {
   __shared__ unsigned long long mask[1024];
   __shared__ int first[1024];
   __shared__ int tmp[32];
@@ -421,7 +461,7 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict
   __syncthreads();
   const int live = live_tokens(n_live, T);
   for (int t = wv; t < live; t += 16)
-    route_token<EPL>(logits, parts, T, E, k, t, lane, sel + t * 32, selw + t * 32, mask);
+    route_token<EPL>(logits, T, E, k, t, lane, sel + t * 32, selw + t * 32, mask);
   __syncthreads();
   // experts with tokens, in order: (slots, entries) before each, in one scan
   const unsigned long long mk = mask[threadIdx.x];
@@ -434,7 +474,9 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict
   __syncthreads();
   for (int i = threadIdx.x; i < live * k; i += 1024) {
     const int t = i / k, j = i - t * k, e = sel[t * 32 + j];
-    gate[first[e] + __popcll(mask[e] & ((1ull << t) - 1))] = selw[t * 32 + j];
+    const int pos = first[e] + __popcll(mask[e] & ((1ull << t) - 1));
+    gate[pos] = selw[t * 32 + j];
+    pos_out[i] = pos;
     if (idx_out != nullptr) idx_out[i] = e;
     if (w_out != nullptr) w_out[i] = selw[t * 32 + j];
   }
@@ -452,43 +494,54 @@ TRG_DEV int nth_token(unsigned long long mask, int lane, int c) {
   return __builtin_amdgcn_ds_bpermute(c * 4, list);
 }
 
-// 16 rows of h for a slot's columns: both matrices' rows, shared by wk waves
-// along k, then h = gate * silu(g) * u.  red: this group's 2 * wk * 256 floats;
-// tid: thread within the group.
-template <int WT, int NT, int U>
-TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WRow* wr, int rb, unsigned long long mask,
-                     const float* gate, int cnt, int row0, int h, char* hid, long hid_n, long pos0, int wk, int kw,
-                     int tid, float* red) {
+// RM * 16 rows of h for a slot's columns: both matrices' rows, shared by wk
+// waves along k, then h = gate * silu(g) * u.  red: this group's 2 * wk * 256
+// floats; tid: thread within the group.
+template <int WT, int RM, int NT, int U>
+TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb, unsigned long long mask,
+                     const float* gate, int cnt, int col0, int row0, int h, char* hid, long hid_n, long pos0, int wk,
+                     int kw, int tid, float* red) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
-  const char* xr[NT];
+  WRow wr[2 * RM];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xr[i] = x + (long)nth_token(mask, lane, min(i * 16 + r, cnt - 1)) * xb;
-  f32x4_t acc[2][NT];
+  for (int m = 0; m < RM; ++m) {
+    const int row = min(row0 + m * 16 + r, h - 1);
+    wr[2 * m] = w_row<WT>(wb[0], row, rb);
+    wr[2 * m + 1] = w_row<WT>(wb[1], row, rb);
+  }
+  uint32_t xo[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) acc[0][i] = acc[1][i] = f32x4_t{0, 0, 0, 0};
-  stream_tile<WT, 2, NT, U>(wr, xr, r < cnt, rb, kw, (rb + 127) >> 7, wk, q, acc);
+  for (int i = 0; i < NT; ++i) xo[i] = (uint32_t)nth_token(mask, lane, min(col0 + i * 16 + r, cnt - 1)) * (uint32_t)xb;
+  f32x4_t acc[2 * RM][NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    if (i > 0) __syncthreads();
-    put_tile(red + kw * 256, lane, acc[0][i]);
-    put_tile(red + (wk + kw) * 256, lane, acc[1][i]);
-    __syncthreads();
-    for (int o = tid; o < 256; o += wk * 64) {
-      const int row = o & 15, col = o >> 4, c = i * 16 + col;
-      if (c < cnt && row0 + row < h) {
-        const float g = sum_tile(red, wk, row, col), u = sum_tile(red + wk * 256, wk, row, col);
-        const float v = gate[c] * (g / (1.0f + expf(-g)) * u);
-        const long at = (pos0 + c) * h + row0 + row;
-        if constexpr (WT == kF32) {
-          ((float*)hid)[at] = v;
-        } else {
-          const uint16_t hi = f2bf(v);
-          ((uint16_t*)hid)[at] = hi;
-          ((uint16_t*)hid)[hid_n + at] = f2bf(v - bf2f(hi));
+  for (int m = 0; m < 2 * RM; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0, 0, 0, 0};
+  stream_tile<WT, 2, 2 * RM, NT, U, 1>(wb, wr, x, xo, 0, r < cnt, rb, kw, (rb + 127) >> 7, wk, q, acc);
+#pragma unroll
+  for (int m = 0; m < RM; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (m + i > 0) __syncthreads();
+      put_tile(red + kw * 256, lane, acc[2 * m][i]);
+      put_tile(red + (wk + kw) * 256, lane, acc[2 * m + 1][i]);
+      __syncthreads();
+      for (int o = tid; o < 256; o += wk * 64) {
+        const int lr = o & 15, col = o >> 4, c = col0 + i * 16 + col, row = row0 + m * 16 + lr;
+        if (c < cnt && row < h) {
+          const float g = sum_tile(red, wk, lr, col), u = sum_tile(red + wk * 256, wk, lr, col);
+          const float v = gate[c] * (g / (1.0f + expf(-g)) * u);
+          const long at = (pos0 + c) * h + row;
+          if constexpr (WT == kF32) {
+            ((float*)hid)[at] = v;
+          } else {
+            const uint16_t hi = f2bf(v);
+            ((uint16_t*)hid)[at] = hi;
+            ((uint16_t*)hid)[hid_n + at] = f2bf(v - bf2f(hi));
+          }
         }
       }
     }
-  }
 }
 
 constexpr int kProTokens = kWaves;  // tokens and entries that the up projection routes itself
@@ -498,20 +551,20 @@ constexpr int kProEntries = 64;
 // instead of waiting for a launch that does it once; the slots' first
 // workgroups leave them for the down projection.  Slots are then in the order
 // of their first (token, place), a lane an entry, and slot s has hid rows s * T.
-template <int WT, int NT, int U, int EPL, bool PRO>
+template <int WT, int RM, int U, int EPL, bool PRO>
 __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     const char* __restrict__ x, int xb, const void* __restrict__ w1, const uint8_t* __restrict__ w1s,
     const void* __restrict__ w3, const uint8_t* __restrict__ w3s, int T, int E, int k, int h, int rb, int wk,
-    const float* __restrict__ logits, int parts, const int* __restrict__ n_live, int* __restrict__ idx_out,
+    const float* __restrict__ logits, const int* __restrict__ n_live, int* __restrict__ idx_out,
     float* __restrict__ w_out, int* __restrict__ n_active, FewSlot* __restrict__ slots, float* __restrict__ gate,
     char* __restrict__ hid, long hid_n) {
   const int G = kWaves / wk;  // row tiles of a workgroup
   __shared__ __attribute__((aligned(16))) float red[2 * kWaves * 256];
-  const int lane = threadIdx.x & 63, wv = wave_id(), r = lane & 15;
-  const int tiles = (h + 16 * G - 1) / (16 * G);
+  const int lane = threadIdx.x & 63, wv = wave_id();
+  const int tiles = (h + 16 * RM * G - 1) / (16 * RM * G);
   const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
   const int grp = wv / wk, kw = wv % wk, tid = threadIdx.x - grp * wk * 64;
-  const int row0 = (tile * G + grp) * 16;
+  const int row0 = (tile * G + grp) * 16 * RM;
   FewSlot sl;
   const float* gt;
   if constexpr (PRO) {
@@ -522,7 +575,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     const int live = live_tokens(n_live, T), entries = live * k;
     for (int e = threadIdx.x; e < EPL * 64; e += kThreads) mask[e] = 0;
     __syncthreads();
-    if (wv < live) route_token<EPL>(logits, parts, T, E, k, wv, lane, sel + wv * k, selw + wv * k, mask);
+    if (wv < live) route_token<EPL>(logits, T, E, k, wv, lane, sel + wv * k, selw + wv * k, mask);
     __syncthreads();
     // every wave: lane = entry (token lane / k, place lane % k)
     const int e = lane < entries ? sel[lane] : 0, t = lane / k;
@@ -549,37 +602,42 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     gt = gate + sl.off;
   }
   const int cnt = __popcll(sl.mask);
-  const long n = (long)E * h, row = (long)sl.e * h + min(row0 + r, h - 1);
-  const WRow wr[2] = {w_row<WT>(w1, w1s, n, row, rb), w_row<WT>(w3, w3s, n, row, rb)};
   float* rd = red + grp * 2 * wk * 256;
+  const WBase wb[2] = {w_base<WT>(w1, w1s, sl.e, E, h, rb), w_base<WT>(w3, w3s, sl.e, E, h, rb)};
   // a tile past the last row (row0 >= h) still takes part in the barriers
-#define TRG_TILE(N) \
-  up_tile<WT, N, (N == 1 ? U : 1)>(x, xb, wr, rb, sl.mask, gt, cnt, row0, h, hid, hid_n, sl.off, wk, kw, tid, rd)
-  if (NT == 1 || cnt <= 16) TRG_TILE(1);
-  else if (cnt <= 32) TRG_TILE((NT > 1 ? NT / 2 : 1));
-  else TRG_TILE(NT);
+#define TRG_TILE(RM, NT, U, ROW0) \
+  up_tile<WT, RM, NT, U>(x, xb, wb, rb, sl.mask, gt, cnt, c0, ROW0, h, hid, hid_n, sl.off, wk, kw, tid, rd)
+  int c0 = 0;
+  if (PRO || cnt <= 16) {
+    TRG_TILE(RM, 1, U, row0);
+  } else {
+    // more columns: their accumulators take the registers of the second row tile
+    constexpr int NT = WT == kE2M1 ? 2 : 4;
+    for (; c0 < cnt; c0 += 16 * NT)
+      for (int m = 0; m < RM; ++m) {
+        if (c0 + m > 0) __syncthreads();
+        if (cnt - c0 <= 32) TRG_TILE(1, 2, 1, row0 + 16 * m);
+        else TRG_TILE(1, NT, 1, row0 + 16 * m);
+      }
+  }
 #undef TRG_TILE
 }
 
-// ---- down projection ----------------------------------------------------------------
-// A workgroup takes 16 / KS rows of d and one part (blockIdx.y of gridDim.y) of
-// the items of all chosen experts: item f is KS lines of a row from line
-// f % nit * KS of slot f / nit.  A column is a token; an expert's item meets
-// only the columns of its own tokens.  With few tokens (T <= 16 / KS) the 16
-// rows and columns of the matrix instruction are KS groups: group g of rows
+// ---- down projection, at most 8 tokens -----------------------------------------------
+// A workgroup takes 16 / KS rows of d and all chosen experts: item f is KS
+// lines of a row, from line f % nit * KS of slot f / nit.  A column is a token;
+// an expert's item meets only the columns of its own tokens.  T <= 16 / KS: the
+// 16 rows and columns of the matrix instruction are KS groups; group g of rows
 // holds the same weight rows at the item's line g, group g of columns the
 // tokens at that line, and the blocks where the groups agree are summed at the
 // end: more, smaller row tiles, at the same loads.
-// PART: the sum goes to part[blockIdx.y] in fp32, else to y.
-template <int WT, int NT, int U, int KS, bool PART>
+template <int WT, int U, int KS>
 __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __restrict__ hid, long hid_n,
                                                                const void* __restrict__ w2,
                                                                const uint8_t* __restrict__ w2s, int E, int d, int h,
                                                                int rb, const int* __restrict__ n_active,
                                                                const FewSlot* __restrict__ slots, int T,
-                                                               const int* __restrict__ n_live, void* __restrict__ y,
-                                                               float* __restrict__ part) {
-  static_assert(KS == 1 || NT == 1, "line groups share one tile of columns");
+                                                               const int* __restrict__ n_live, void* __restrict__ y) {
   constexpr int P = WT == kF32 ? 1 : 2;  // parts of h
   constexpr int XE = Piece<WT>::kXE;
   constexpr int RT = 16 / KS, CT = 16 / KS;
@@ -592,29 +650,25 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
   const int ct = r % CT, kc = r / CT;                      // this lane's column: token and line group
   const int nall = (rb + 127) >> 7, nit = (nall + KS - 1) / KS;
   const int F = na * nit;
-  const int f1 = (int)((long)F * (blockIdx.y + 1) / gridDim.y);
-  const int f0 = (int)((long)F * blockIdx.y / gridDim.y) + wv;
-  f32x4_t acc[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+  f32x4_t acc = {0, 0, 0, 0};
   struct Items {
     WStep w[U];
     unsigned long long mask[U];
     int off[U], c[U];
   };
-  int s = f0 / nit, c = f0 - s * nit;  // the next item to load
-  // items f, f + kWaves, ...: one past the share's end repeats the share's last
-  // slot (so its loads are in bounds) for no token
+  int s = wv / nit, c = wv - s * nit;  // the next item to load
+  // items f, f + kWaves, ...: one past the end repeats the last slot (so its
+  // loads are in bounds) for no token
   auto load = [&](Items& o, int f) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const bool in = f + u * kWaves < f1;
+      const bool in = f + u * kWaves < F;
       const FewSlot sl = slots[in ? s : na - 1];
       o.mask[u] = in ? sl.mask : 0;
       o.off[u] = sl.off;
       o.c[u] = in ? c * KS : 0;
-      const WRow wr = w_row<WT>(w2, w2s, (long)E * d, (long)sl.e * d + row, rb);
-      o.w[u] = w_load<WT>(wr, o.c[u] + kr, q, rb);
+      const WBase wb = w_base<WT>(w2, w2s, sl.e, E, d, rb);
+      o.w[u] = w_load<WT>(wb, w_row<WT>(wb, row, rb), o.c[u] + kr, q, rb);
       c += kWaves;
       while (c >= nit) {
         c -= nit;
@@ -626,81 +680,140 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       w_mask<WT>(o.w[u], o.c[u] + kr, q, rb);
+      const bool on = (o.mask[u] >> ct) & 1;
+      const uint32_t xo = (uint32_t)(o.off[u] + __popcll(o.mask[u] & ((1ull << ct) - 1))) * (uint32_t)(h * XE);
+      XStep<WT> x[P];
+      if (on) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (NT > 1 && ((unsigned)(o.mask[u] >> (16 * n)) & 0xFFFFu) == 0) continue;  // the same for the whole wave
-        const int t = 16 * n + ct;
-        const bool on = (o.mask[u] >> t) & 1;
-        const long pos = o.off[u] + __popcll(o.mask[u] & ((1ull << t) - 1));
-        const char* hr = hid + pos * h * XE;
-        f32x4_t t4 = {0, 0, 0, 0};
-        // both parts' operands at once, or with several tiles of columns (whose
-        // accumulators need the registers) one after the other
-        constexpr int AT = NT > 1 ? 1 : P;
-#pragma unroll
-        for (int p0 = 0; p0 < P; p0 += AT) {
-          XStep<WT> x[AT];
-          if (on) {
-#pragma unroll
-            for (int p = 0; p < AT; ++p) x_load<WT>(hr + (p0 + p) * hid_n * XE, o.c[u] + kc, q, rb, x[p]);
-          }
-#pragma unroll
-          for (int p = 0; p < AT; ++p) t4 = mma_step<WT>(o.w[u], x[p], t4);
-        }
-        // columns of tokens that did not choose this expert are left alone, not
-        // given 0 * w: an infinite or NaN weight is its own tokens' matter
-#pragma unroll
-        for (int z = 0; z < 4; ++z) acc[n][z] = on ? acc[n][z] + t4[z] : acc[n][z];
+        for (int p = 0; p < P; ++p) x_load<WT>(hid + p * hid_n * XE, xo, o.c[u] + kc, q, rb, x[p]);
       }
+      f32x4_t t = {0, 0, 0, 0};
+#pragma unroll
+      for (int p = 0; p < P; ++p) t = mma_step<WT>(o.w[u], x[p], t);
+      // columns of tokens that did not choose this expert are left alone, not
+      // given 0 * w: an infinite or NaN weight is its own tokens' matter
+#pragma unroll
+      for (int z = 0; z < 4; ++z) acc[z] = on ? acc[z] + t[z] : acc[z];
     }
   };
-  if (f0 < f1) {
+  if (wv < F) {
     Items a, b;
-    load(a, f0);
-    int f = f0;
-    for (; f + kWaves * U < f1; f += kWaves * U) {
-      load(b, f + kWaves * U);
+    load(a, wv);
+    for (int f = wv + kWaves * U; f < F; f += kWaves * U) {
+      load(b, f);
       multiply(a);
       a = b;
     }
     multiply(a);
   }
+  put_tile(red + wv * 256, lane, acc);
+  __syncthreads();
+  const int orow = threadIdx.x % RT, t = threadIdx.x / RT;
+  if (threadIdx.x < RT * CT && t < live && row0 + orow < d) {
+    float v = 0.f;
 #pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    if (i > 0) __syncthreads();
-    put_tile(red + wv * 256, lane, acc[i]);
-    __syncthreads();
-    const int orow = threadIdx.x % RT, col = threadIdx.x / RT, t = i * 16 + col;
-    if (threadIdx.x < RT * CT && t < live && row0 + orow < d) {
-      float v = 0.f;
-#pragma unroll
-      for (int g = 0; g < KS; ++g) v += sum_tile(red, kWaves, g * RT + orow, g * CT + col);
-      const long at = (long)t * d + row0 + orow;
-      if constexpr (PART) part[(long)blockIdx.y * T * d + at] = v;
-      else if constexpr (WT == kF32) ((float*)y)[at] = v;
-      else ((uint16_t*)y)[at] = f2bf(v);
-    }
+    for (int g = 0; g < KS; ++g) v += sum_tile(red, kWaves, g * RT + orow, g * CT + t);
+    const long at = (long)t * d + row0 + orow;
+    if constexpr (WT == kF32) ((float*)y)[at] = v;
+    else ((uint16_t*)y)[at] = f2bf(v);
   }
 }
 
-// y = the parts' sum, in order.
+// ---- down projection, more tokens ------------------------------------------------------
+// As the up projection: workgroup (slot, row tiles of d), columns the slot's own
+// tokens, lines shared by wk waves; every entry's row goes out in fp32 and the
+// join adds each token's k rows in order.  Those rows are R d floats, out and
+// in: 3 % of the weights' bytes with two tokens an expert at h = 1024 and 4
+// bits, 0.25 % in bf16 at h = 2048.
+template <int WT, int RM, int NT, int U>
+TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb, int rb, int cnt, int col0, int row0,
+                       int d, int h, long pos0, int wk, int kw, int tid, float* red, float* __restrict__ yp) {
+  constexpr int P = WT == kF32 ? 1 : 2, XE = Piece<WT>::kXE;
+  const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
+  WRow wr[RM];
+#pragma unroll
+  for (int m = 0; m < RM; ++m) wr[m] = w_row<WT>(wb[0], min(row0 + m * 16 + r, d - 1), rb);
+  uint32_t xo[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) xo[i] = (uint32_t)(pos0 + min(col0 + i * 16 + r, cnt - 1)) * (uint32_t)(h * XE);
+  f32x4_t acc[RM][NT];
+#pragma unroll
+  for (int m = 0; m < RM; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0, 0, 0, 0};
+  stream_tile<WT, 1, RM, NT, U, P>(wb, wr, hid, xo, hid_n * XE, r < cnt, rb, kw, (rb + 127) >> 7, wk, q, acc);
+#pragma unroll
+  for (int m = 0; m < RM; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+      if (m + i > 0) __syncthreads();
+      put_tile(red + kw * 256, lane, acc[m][i]);
+      __syncthreads();
+      for (int o = tid; o < 256; o += wk * 64) {
+        const int lr = o & 15, col = o >> 4, c = col0 + i * 16 + col, row = row0 + m * 16 + lr;
+        if (c < cnt && row < d) yp[(pos0 + c) * d + row] = sum_tile(red, wk, lr, col);
+      }
+    }
+}
+
+template <int WT, int RM, int U>
+__global__ __launch_bounds__(kThreads, 4) void few_down_rows_kernel(const char* __restrict__ hid, long hid_n,
+                                                                    const void* __restrict__ w2,
+                                                                    const uint8_t* __restrict__ w2s, int E, int d,
+                                                                    int h, int rb, int wk,
+                                                                    const int* __restrict__ n_active,
+                                                                    const FewSlot* __restrict__ slots,
+                                                                    float* __restrict__ yp) {
+  __shared__ __attribute__((aligned(16))) float red[kWaves * 256];
+  const int wv = wave_id(), G = kWaves / wk;
+  const int tiles = (d + 16 * RM * G - 1) / (16 * RM * G);
+  const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
+  const int grp = wv / wk, kw = wv % wk, tid = threadIdx.x - grp * wk * 64;
+  const int row0 = (tile * G + grp) * 16 * RM;
+  const int na = *n_active;
+  const FewSlot sl = slots[slot];  // in bounds; meaningful if slot < na
+  if (slot >= na) return;
+  const int cnt = __popcll(sl.mask);
+  float* rd = red + grp * wk * 256;
+  const WBase wb[1] = {w_base<WT>(w2, w2s, sl.e, E, d, rb)};
+#define TRG_TILE(RM, NT, U, ROW0) \
+  down_tile<WT, RM, NT, U>(hid, hid_n, wb, rb, cnt, c0, ROW0, d, h, sl.off, wk, kw, tid, rd, yp)
+  int c0 = 0;
+  if (cnt <= 16) {
+    TRG_TILE(RM, 1, U, row0);
+  } else {
+    constexpr int NT = WT == kE2M1 ? 2 : 4;
+    for (; c0 < cnt; c0 += 16 * NT)
+      for (int m = 0; m < RM; m += 2) {
+        if (c0 + m > 0) __syncthreads();
+        if (cnt - c0 <= 32) TRG_TILE(2, 2, 1, row0 + 16 * m);
+        else TRG_TILE(2, NT, 1, row0 + 16 * m);
+      }
+  }
+#undef TRG_TILE
+}
+
+// y[t] = sum over its k entries' rows, in the order of its choices.
 template <class OUT>
-__global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__ part, int parts, int T, int d,
-                                                       const int* __restrict__ n_live, OUT* __restrict__ y) {
-  const long i = ((long)blockIdx.x * 256 + threadIdx.x) * 4;  // d is a multiple of 4
-  if (i >= (long)live_tokens(n_live, T) * d) return;
-  float4 a = *(const float4*)(part + i);
-  for (int p = 1; p < parts; ++p) {
-    const float4 b = *(const float4*)(part + (long)p * T * d + i);
+__global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__ yp, const int* __restrict__ pos, int T,
+                                                       int d, int k, const int* __restrict__ n_live,
+                                                       OUT* __restrict__ y) {
+  const int i = (blockIdx.x * 256 + threadIdx.x) * 4;  // d is a multiple of 4
+  const int t = blockIdx.y;
+  if (i >= d || t >= live_tokens(n_live, T)) return;
+  float4 a = make_float4(0, 0, 0, 0);
+  for (int j = 0; j < k; ++j) {
+    const float4 b = *(const float4*)(yp + (long)pos[t * k + j] * d + i);
     a.x += b.x;
     a.y += b.y;
     a.z += b.z;
     a.w += b.w;
   }
-  Elt<OUT>::st(y + i, a.x);
-  Elt<OUT>::st(y + i + 1, a.y);
-  Elt<OUT>::st(y + i + 2, a.z);
-  Elt<OUT>::st(y + i + 3, a.w);
+  OUT* o = y + (long)t * d + i;
+  Elt<OUT>::st(o, a.x);
+  Elt<OUT>::st(o + 1, a.y);
+  Elt<OUT>::st(o + 2, a.z);
+  Elt<OUT>::st(o + 3, a.w);
 }
 
 template <int WT, int NM, int NT, int U, class OUT>
@@ -712,54 +825,16 @@ hipError_t linear_nt(const void* x, const void* w, const uint8_t* ws, int T, int
   return hipGetLastError();
 }
 
-// Partial sums of the router's logits: enough workgroups that a wave has about
-// one line (E / 16 tiles alone leave most of the chip idle).
-int logit_parts(int d, int es) {
-  const int lines = (d * es + 127) / 128;
-  const int p = (lines + kWaves - 1) / kWaves;
-  return p < 1 ? 1 : (p > 8 ? 8 : p);
-}
-
-// Parts of the down projection (1: straight to y).
-int down_parts(int T, int d) {
-  if (T <= 8) return 1;
-  const int tiles = (d + 15) / 16;
-  const int p = 1024 / tiles;
-  return p < 2 ? 2 : (p > 8 ? 8 : p);
-}
-
-// Waves that share a row tile of the up projection: as many as leave each wave
-// about 16 KB of weights.
-int up_waves(int T, int E, int k, int h, int rb) {
-  (void)T; (void)E; (void)k; (void)h;
-  const int bytes = 32 * rb;  // a tile's: 16 rows of both matrices
-  return bytes >= 8 * 12288 ? 8 : (bytes >= 4 * 8192 ? 4 : 2);
-}
+// Waves that share a row tile along k, from a weight row's bytes: a wave needs
+// some lines to itself, and long rows need the waves (one wave a 12 KB row has
+// too few loads in flight).  Measured, us a pass with 8 / 4 / 2 / 1 waves in
+// both projections: 24 tokens, rows of 12 and 4 KB 1856 / 1954 / 1993 / 1986;
+// 61 tokens, rows of 1 KB and 512 bytes 124 / 115 / 114 / 119 (the up projection
+// varied) and 126 / 113 / 115 / 113 (the down); one token, rows of 4 KB 18.9 /
+// 21.4 / 29.2 / 45.3.
+int row_waves(int rb) { return rb >= 4096 ? 8 : 4; }
 
 bool in_prologue(int T, int k) { return T <= kProTokens && T * k <= kProEntries; }
-
-template <int WT, int NT, int U>
-hipError_t up_any(const moe_few_args& a, int rb, int xb, int slots_max, const float* logits, int parts, int* n_active,
-                  FewSlot* slots, float* gate, char* hid, long hid_n, hipStream_t st) {
-  const int wk = up_waves(a.T, a.E, a.k, a.h, rb), G = kWaves / wk;
-  const unsigned grid = (unsigned)slots_max * ((a.h + 16 * G - 1) / (16 * G));
-#define TRG_UP(EPL, PRO)                                                                                             \
-  few_up_kernel<WT, NT, U, EPL, PRO><<<grid, kThreads, 0, st>>>((const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.T, \
-                                                                a.E, a.k, a.h, rb, wk, logits, parts, a.n_live,     \
-                                                                a.topk_idx, a.topk_w, n_active, slots, gate, hid,   \
-                                                                hid_n)
-  if constexpr (NT == 1) {
-    if (in_prologue(a.T, a.k)) {
-      if (a.E <= 128) TRG_UP(2, true);
-      else if (a.E <= 512) TRG_UP(8, true);
-      else TRG_UP(16, true);
-      return hipGetLastError();
-    }
-  }
-  TRG_UP(1, false);
-#undef TRG_UP
-  return hipGetLastError();
-}
 
 template <int WT>
 hipError_t few_any(const moe_few_args& a, hipStream_t st) {
@@ -771,20 +846,21 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   float* gate = (float*)(ws + l.gate);
   float* logits = (float*)(ws + l.logits);
   char* hid = ws + l.hid;
-  float* part = (float*)(ws + l.part);
+  int* pos = (int*)(ws + l.pos);
+  float* yp = (float*)(ws + l.yp);
+  const bool pro = in_prologue(a.T, a.k);
   const int R = a.T * a.k, slots_max = R < a.E ? R : a.E;
   const long hid_n = (long)hid_rows(a.T, a.E, a.k) * a.h;
-  const int lp = logit_parts(a.d, XE);
   constexpr int RT = WT == kF32 ? kF32 : kBF16;  // the router's weights are in x's type
   const int xb = a.d * XE;
-  hipError_t e = a.T <= 16   ? linear_nt<RT, 1, 1, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, lp, a.n_live, logits, st)
-                 : a.T <= 32 ? linear_nt<RT, 1, 2, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, lp, a.n_live, logits, st)
-                             : linear_nt<RT, 1, 4, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, lp, a.n_live, logits, st);
+  hipError_t e = a.T <= 16   ? linear_nt<RT, 1, 1, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, kLogitParts, a.n_live, logits, st)
+                 : a.T <= 32 ? linear_nt<RT, 1, 2, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, kLogitParts, a.n_live, logits, st)
+                             : linear_nt<RT, 1, 4, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, kLogitParts, a.n_live, logits, st);
   if (e != hipSuccess) return e;
-  if (!in_prologue(a.T, a.k)) {
+  if (!pro) {
 #define TRG_ROUTE(N)                                                                                                  \
-  few_route_kernel<N><<<1, 1024, 0, st>>>(logits, lp, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, n_active, slots, \
-                                          gate)
+  few_route_kernel<N><<<1, 1024, 0, st>>>(logits, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, n_active, slots, \
+                                          gate, pos)
     if (a.E <= 64) TRG_ROUTE(1);
     else if (a.E <= 128) TRG_ROUTE(2);
     else if (a.E <= 512) TRG_ROUTE(8);
@@ -796,25 +872,39 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   // bytes of a weight row
   const int rb1 = WT == kE2M1 ? a.d / 2 : a.d * XE, rb2 = WT == kE2M1 ? a.h / 2 : a.h * XE;
   constexpr int U = WT == kE2M1 ? 1 : 2;
-  e = a.T <= 16 ? up_any<WT, 1, U>(a, rb1, xb, slots_max, logits, lp, n_active, slots, gate, hid, hid_n, st)
-                : up_any<WT, 4, U>(a, rb1, xb, slots_max, logits, lp, n_active, slots, gate, hid, hid_n, st);
-  if (e != hipSuccess) return e;
-  const int dp = down_parts(a.T, a.d);
-#define TRG_DOWN(NT, U, KS, PART)                                                                                     \
-  few_down_kernel<WT, NT, U, KS, PART><<<dim3((a.d + 16 / KS - 1) / (16 / KS), dp), kThreads, 0, st>>>(               \
-      hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, n_active, slots, a.T, a.n_live, a.y, part)
-  if (a.T <= 4) TRG_DOWN(1, U, 4, false);
-  else if (a.T <= 8) TRG_DOWN(1, U, 2, false);
-  else if (a.T <= 16) TRG_DOWN(1, U, 1, true);
-  else TRG_DOWN(4, U, 1, true);
-#undef TRG_DOWN
+  const int uw = row_waves(rb1), G = kWaves / uw;
+#define TRG_UP(RM, U, EPL, PRO)                                                                                       \
+  few_up_kernel<WT, RM, U, EPL, PRO><<<(unsigned)slots_max * ((a.h + 16 * RM * G - 1) / (16 * RM * G)), kThreads, 0,  \
+                                       st>>>((const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.T, a.E, a.k, a.h, rb1, \
+                                             uw, logits, a.n_live, a.topk_idx, a.topk_w, n_active, slots, gate, hid,  \
+                                             hid_n)
+  if (!pro) TRG_UP(2, U, 1, false);
+  else if (a.E <= 128) TRG_UP(1, 2 * U, 2, true);
+  else if (a.E <= 512) TRG_UP(1, 2 * U, 8, true);
+  else TRG_UP(1, 2 * U, 16, true);
+#undef TRG_UP
   e = hipGetLastError();
-  if (e != hipSuccess || dp == 1) return e;
-  const unsigned jg = (unsigned)(((long)a.T * a.d / 4 + 255) / 256);
+  if (e != hipSuccess) return e;
+#define TRG_DOWN(KS)                                                                                                \
+  few_down_kernel<WT, U, KS><<<(a.d + 16 / KS - 1) / (16 / KS), kThreads, 0, st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, \
+                                                                                   a.h, rb2, n_active, slots, a.T,  \
+                                                                                   a.n_live, a.y)
+  if (pro) {
+    if (a.T <= 4) TRG_DOWN(4);
+    else TRG_DOWN(2);
+    return hipGetLastError();
+  }
+#undef TRG_DOWN
+  const int dw = row_waves(rb2), rows = 64 * (kWaves / dw);
+  few_down_rows_kernel<WT, 4, 1><<<(unsigned)slots_max * ((a.d + rows - 1) / rows), kThreads, 0, st>>>(
+      hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, dw, n_active, slots, yp);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 jg((a.d / 4 + 255) / 256, a.T);
   if constexpr (WT == kF32)
-    few_join_kernel<float><<<jg, 256, 0, st>>>(part, dp, a.T, a.d, a.n_live, (float*)a.y);
+    few_join_kernel<float><<<jg, 256, 0, st>>>(yp, pos, a.T, a.d, a.k, a.n_live, (float*)a.y);
   else
-    few_join_kernel<uint16_t><<<jg, 256, 0, st>>>(part, dp, a.T, a.d, a.n_live, (uint16_t*)a.y);
+    few_join_kernel<uint16_t><<<jg, 256, 0, st>>>(yp, pos, a.T, a.d, a.k, a.n_live, (uint16_t*)a.y);
   return hipGetLastError();
 }
 
