@@ -354,96 +354,101 @@ __global__ __launch_bounds__(kThreads, NM* NT > 4 ? 2 : 4) void few_linear_kerne
 }
 
 // ---- routing ---------------------------------------------------------------------
-// Largest of v over the wave (0 is the identity), known to every lane: five
-// steps inside the vector registers (rows of 16, then the rows' ends).
+// Reductions over the wave inside the vector registers: within rows of 16 lanes,
+// then over the rows' last lanes; lane 63 has the result.  Lanes without a
+// partner combine with 0, the identity of both.
 template <int CTRL>
 TRG_DEV uint32_t max_dpp(uint32_t v) {
   return max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false));
 }
+template <int CTRL>
+TRG_DEV float sum_dpp(float v) {
+  return v + __uint_as_float(__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+// row_shr 1, 2, 4, 8, row_bcast 15, 31
 TRG_DEV uint32_t wave_max_u32(uint32_t v) {
-  v = max_dpp<0x111>(v);  // row_shr:1
-  v = max_dpp<0x112>(v);  // row_shr:2
-  v = max_dpp<0x114>(v);  // row_shr:4
-  v = max_dpp<0x118>(v);  // row_shr:8
-  v = max_dpp<0x142>(v);  // row_bcast:15
-  v = max_dpp<0x143>(v);  // row_bcast:31
-  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+  v = max_dpp<0x118>(max_dpp<0x114>(max_dpp<0x112>(max_dpp<0x111>(v))));
+  return (uint32_t)__builtin_amdgcn_readlane((int)max_dpp<0x143>(max_dpp<0x142>(v)), 63);
+}
+TRG_DEV float wave_sum_dpp(float v) {
+  v = sum_dpp<0x118>(sum_dpp<0x114>(sum_dpp<0x112>(sum_dpp<0x111>(v))));
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sum_dpp<0x143>(sum_dpp<0x142>(v))), 63));
 }
 
-// One wave routes token t: the k largest logits, ties to the lower expert, a
-// NaN never before a number (moe_route's rules), and their softmax values.
-// Logits come as partial sums [kLogitParts][T][E], added in order.  A logit
-// becomes a 32-bit key that orders like it (0 is below every key), so a round
-// is one wave maximum and the first lane of the first register that holds it:
-// expert e is lane e % 64, register e / 64.  sel, selw: this token's k places.
+// One wave routes token t from its logits (v[i] of lane l: expert l + 64 i): the
+// k largest, ties to the lower expert, a NaN never before a number (moe_route's
+// rules), and their softmax values.  A logit becomes a 32-bit key that orders
+// like it (0 is below every key), so a round is one wave maximum and the first
+// lane of the first register that holds it.  sel, selw: this token's k places.
 template <int EPL>
-TRG_DEV void route_token(const float* __restrict__ logits, int T, int E, int k, int t, int lane, int* sel, float* selw,
+TRG_DEV void route_token(float* v, int E, int k, int t, int lane, uint16_t* sel, float* selw,
                          unsigned long long* mask) {
-  float v[EPL], p[EPL];
-  uint32_t key[EPL];
-  float m = -INFINITY, s = 0.f;
-  // all parts of eight registers' experts are in flight at once: one by one,
-  // each group would wait for its own trip past L2 (another XCD wrote them)
-  constexpr int B = EPL < 8 ? EPL : 8;
-#pragma unroll
-  for (int i0 = 0; i0 < EPL; i0 += B) {
-    float raw[B][kLogitParts];
-    const uint32_t row = (uint32_t)t * (uint32_t)E, plane = (uint32_t)T * (uint32_t)E;
-#pragma unroll
-    for (int i = 0; i < B; ++i)
-#pragma unroll
-      for (int a = 0; a < kLogitParts; ++a)
-        raw[i][a] = logits[row + (uint32_t)a * plane + (uint32_t)min(lane + 64 * (i0 + i), E - 1)];
-    __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-    for (int i = 0; i < B; ++i) {
-      v[i0 + i] = raw[i][0];
-#pragma unroll
-      for (int a = 1; a < kLogitParts; ++a) v[i0 + i] += raw[i][a];
-    }
-  }
+  float p[EPL];
+  uint32_t key[EPL], top = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = lane + 64 * i;
-    const float x = v[i];
-    v[i] = (x != x || e >= E) ? -INFINITY : x;
-    m = fmaxf(m, v[i]);
-    const uint32_t b = __float_as_uint(v[i] + 0.0f);  // -0 and 0 are equal
-    key[i] = e < E ? ((b & 0x80000000u) ? ~b : b | 0x80000000u) : 0u;
+    const bool in = lane + 64 * i < E;
+    v[i] = (v[i] != v[i] || !in) ? -INFINITY : v[i] + 0.0f;  // -0 and 0 are equal
+    const uint32_t b = __float_as_uint(v[i]);
+    key[i] = in ? ((b & 0x80000000u) ? ~b : b | 0x80000000u) : 0u;
+    top = max(top, key[i]);
   }
-  m = wave_max(m);
+  top = wave_max_u32(top);
+  const float m = __uint_as_float((top & 0x80000000u) ? top & 0x7FFFFFFFu : ~top);  // the largest logit
+  float s = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
     p[i] = lane + 64 * i < E ? expf(v[i] - m) : 0.f;
     s += p[i];
   }
-  s = wave_sum(s);
+  s = wave_sum_dpp(s);
   for (int j = 0; j < k; ++j) {
-    uint32_t b = key[0];
-#pragma unroll
-    for (int i = 1; i < EPL; ++i) b = max(b, key[i]);
-    b = wave_max_u32(b);
     bool found = false;  // the same for the whole wave
+    uint32_t next = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const unsigned long long at = __ballot(key[i] == b);
+      const unsigned long long at = __ballot(key[i] == top);
       if (!found && at != 0) {
         found = true;
         const int l = __ffsll((unsigned long long)at) - 1;
         if (lane == l) {
           const int e = l + 64 * i;
           key[i] = 0;
-          sel[j] = e;
+          sel[j] = (uint16_t)e;
           selw[j] = p[i] / s;
           atomicOr(&mask[e], 1ull << t);  // integer: the order does not matter
         }
       }
+      next = max(next, key[i]);
     }
+    if (j + 1 < k) top = wave_max_u32(next);
   }
 }
 
+// out[j] = the router's partial logits at at[j] (of plane = T E values), added in
+// order.  All N * kLogitParts loads are in flight at once: one by one, each
+// group would wait for its own trip past L2 (other XCDs wrote them).
+template <int N>
+TRG_DEV void add_logits(const float* __restrict__ logits, uint32_t plane, const uint32_t* at, float* out) {
+  float raw[N][kLogitParts];
+#pragma unroll
+  for (int j = 0; j < N; ++j)
+#pragma unroll
+    for (int a = 0; a < kLogitParts; ++a) raw[j][a] = logits[at[j] + (uint32_t)a * plane];
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    out[j] = raw[j][0];
+#pragma unroll
+    for (int a = 1; a < kLogitParts; ++a) out[j] += raw[j][a];
+  }
+}
+
+constexpr int kRouteChunk = 8192;  // logits in LDS at a time
+
 // Routing in a launch of its own (more than kProTokens tokens or kProEntries
-// entries): one workgroup, a wave a token at a time; then the chosen experts'
+// entries): one workgroup adds the partial logits of as many tokens as fit into
+// LDS, a wave routes a token at a time from there; then the chosen experts'
 // token masks are compacted, in expert order, into slots.
 template <int EPL>
 __global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict__ logits, int T, int E, int k,
@@ -452,16 +457,35 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict
                                                          FewSlot* __restrict__ slots, float* __restrict__ gate,
                                                          int* __restrict__ pos_out) {
   __shared__ unsigned long long mask[1024];
+  __shared__ float chunk[kRouteChunk];
   __shared__ int first[1024];
   __shared__ int tmp[32];
-  __shared__ int sel[64 * 32];
+  __shared__ uint16_t sel16[64 * 32];
   __shared__ float selw[64 * 32];
   const int lane = threadIdx.x & 63, wv = wave_id();
   mask[threadIdx.x] = 0;
-  __syncthreads();
   const int live = live_tokens(n_live, T);
-  for (int t = wv; t < live; t += 16)
-    route_token<EPL>(logits, T, E, k, t, lane, sel + t * 32, selw + t * 32, mask);
+  const int per = kRouteChunk / E;  // tokens a chunk: at least 8
+  for (int t0 = 0; t0 < live; t0 += per) {
+    const int nt = min(per, live - t0), n = nt * E;
+    uint32_t at[kRouteChunk / 1024];
+    float sum[kRouteChunk / 1024];
+#pragma unroll
+    for (int j = 0; j < kRouteChunk / 1024; ++j)
+      at[j] = (uint32_t)(t0 * E + min((int)threadIdx.x + 1024 * j, n - 1));
+    add_logits<kRouteChunk / 1024>(logits, (uint32_t)T * (uint32_t)E, at, sum);
+    __syncthreads();  // the chunk before has been read
+#pragma unroll
+    for (int j = 0; j < kRouteChunk / 1024; ++j)
+      if ((int)threadIdx.x + 1024 * j < n) chunk[threadIdx.x + 1024 * j] = sum[j];
+    __syncthreads();
+    for (int t = wv; t < nt; t += 16) {
+      float v[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) v[i] = chunk[t * E + min(lane + 64 * i, E - 1)];
+      route_token<EPL>(v, E, k, t0 + t, lane, sel16 + (t0 + t) * 32, selw + (t0 + t) * 32, mask);
+    }
+  }
   __syncthreads();
   // experts with tokens, in order: (slots, entries) before each, in one scan
   const unsigned long long mk = mask[threadIdx.x];
@@ -473,7 +497,7 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict
   if (threadIdx.x == 0) *n_active = total >> 16;
   __syncthreads();
   for (int i = threadIdx.x; i < live * k; i += 1024) {
-    const int t = i / k, j = i - t * k, e = sel[t * 32 + j];
+    const int t = i / k, j = i - t * k, e = sel16[t * 32 + j];
     const int pos = first[e] + __popcll(mask[e] & ((1ull << t) - 1));
     gate[pos] = selw[t * 32 + j];
     pos_out[i] = pos;
@@ -494,13 +518,13 @@ TRG_DEV int nth_token(unsigned long long mask, int lane, int c) {
   return __builtin_amdgcn_ds_bpermute(c * 4, list);
 }
 
-// RM * 16 rows of h for a slot's columns: both matrices' rows, shared by wk
-// waves along k, then h = gate * silu(g) * u.  red: this group's 2 * wk * 256
-// floats; tid: thread within the group.
+// RM * 16 rows of h for a slot's columns: both matrices' rows, shared by the
+// workgroup's wk waves along k (this one is kw), then h = gate * silu(g) * u.
+// red: 2 * wk * 256 floats.
 template <int WT, int RM, int NT, int U>
 TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb, unsigned long long mask,
                      const float* gate, int cnt, int col0, int row0, int h, char* hid, long hid_n, long pos0, int wk,
-                     int kw, int tid, float* red) {
+                     int kw, float* red) {
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   WRow wr[2 * RM];
 #pragma unroll
@@ -526,7 +550,7 @@ TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb
       put_tile(red + kw * 256, lane, acc[2 * m][i]);
       put_tile(red + (wk + kw) * 256, lane, acc[2 * m + 1][i]);
       __syncthreads();
-      for (int o = tid; o < 256; o += wk * 64) {
+      for (int o = threadIdx.x; o < 256; o += wk * 64) {
         const int lr = o & 15, col = o >> 4, c = col0 + i * 16 + col, row = row0 + m * 16 + lr;
         if (c < cnt && row < h) {
           const float g = sum_tile(red, wk, lr, col), u = sum_tile(red + wk * 256, wk, lr, col);
@@ -546,36 +570,59 @@ TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb
 
 constexpr int kProTokens = kWaves;  // tokens and entries that the up projection routes itself
 constexpr int kProEntries = 64;
+constexpr int kProRouter = 65536;
 
 // PRO: every workgroup routes the (few) tokens in its prologue, a wave a token,
 // instead of waiting for a launch that does it once; the slots' first
-// workgroups leave them for the down projection.  Slots are then in the order
+// workgroups leave them for the down projection.  ROUTER: it computes their
+// logits too (at most 16 experts and kProRouter bytes of router weights, which
+// every workgroup reads).  Slots are then in the order
 // of their first (token, place), a lane an entry, and slot s has hid rows s * T.
-template <int WT, int RM, int U, int EPL, bool PRO>
+template <int WT, int RM, int U, int EPL, bool PRO, bool ROUTER>
 __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     const char* __restrict__ x, int xb, const void* __restrict__ w1, const uint8_t* __restrict__ w1s,
-    const void* __restrict__ w3, const uint8_t* __restrict__ w3s, int T, int E, int k, int h, int rb, int wk,
-    const float* __restrict__ logits, const int* __restrict__ n_live, int* __restrict__ idx_out,
+    const void* __restrict__ w3, const uint8_t* __restrict__ w3s, const void* __restrict__ wr, int T,
+    int E, int k, int h, int rb, const float* __restrict__ logits, const int* __restrict__ n_live, int* __restrict__ idx_out,
     float* __restrict__ w_out, int* __restrict__ n_active, FewSlot* __restrict__ slots, float* __restrict__ gate,
     char* __restrict__ hid, long hid_n) {
-  const int G = kWaves / wk;  // row tiles of a workgroup
+  const int wk = blockDim.x >> 6;  // all its waves share a row tile
   __shared__ __attribute__((aligned(16))) float red[2 * kWaves * 256];
   const int lane = threadIdx.x & 63, wv = wave_id();
-  const int tiles = (h + 16 * RM * G - 1) / (16 * RM * G);
+  const int tiles = (h + 16 * RM - 1) / (16 * RM);
   const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
-  const int grp = wv / wk, kw = wv % wk, tid = threadIdx.x - grp * wk * 64;
-  const int row0 = (tile * G + grp) * 16 * RM;
+  const int row0 = tile * 16 * RM;
   FewSlot sl;
   const float* gt;
   if constexpr (PRO) {
     __shared__ unsigned long long mask[EPL * 64];
-    __shared__ int sel[kProEntries];
+    __shared__ uint16_t sel[kProEntries];
     __shared__ float selw[kProEntries];
     __shared__ float mygate[kProTokens];
     const int live = live_tokens(n_live, T), entries = live * k;
-    for (int e = threadIdx.x; e < EPL * 64; e += kThreads) mask[e] = 0;
-    __syncthreads();
-    if (wv < live) route_token<EPL>(logits, T, E, k, wv, lane, sel + wv * k, selw + wv * k, mask);
+    for (int e = threadIdx.x; e < EPL * 64; e += kThreads) mask[e] = 0;  // launched with kThreads
+    float v[EPL];
+    if constexpr (ROUTER) {
+      // at most 16 experts: one row tile, its lines shared by the waves
+      constexpr int RT = WT == kF32 ? kF32 : kBF16;  // the router's weights are in x's type
+      const int r = lane & 15, q = lane >> 4;
+      const WBase wb[1] = {w_base<RT>(wr, nullptr, 0, 1, E, xb)};
+      const WRow row[1] = {w_row<RT>(wb[0], min(r, E - 1), xb)};
+      const uint32_t xo[1] = {(uint32_t)min(r, T - 1) * (uint32_t)xb};
+      f32x4_t acc[1][1] = {{{0, 0, 0, 0}}};
+      stream_tile<RT, 1, 1, 1, 4, 1>(wb, row, x, xo, 0, r < live, xb, wv, (xb + 127) >> 7, kWaves, q, acc);
+      put_tile(red + wv * 256, lane, acc[0][0]);
+      __syncthreads();
+      v[0] = sum_tile(red, kWaves, lane & 15, wv);
+    } else {
+      uint32_t at[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) at[i] = (uint32_t)(min(wv, T - 1) * E + min(lane + 64 * i, E - 1));
+      constexpr int B = EPL < 4 ? EPL : 4;
+#pragma unroll
+      for (int i = 0; i < EPL; i += B) add_logits<B>(logits, (uint32_t)T * (uint32_t)E, at + i, v + i);
+      __syncthreads();
+    }
+    if (wv < live) route_token<EPL>(v, E, k, wv, lane, sel + wv * k, selw + wv * k, mask);
     __syncthreads();
     // every wave: lane = entry (token lane / k, place lane % k)
     const int e = lane < entries ? sel[lane] : 0, t = lane / k;
@@ -602,11 +649,9 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     gt = gate + sl.off;
   }
   const int cnt = __popcll(sl.mask);
-  float* rd = red + grp * 2 * wk * 256;
   const WBase wb[2] = {w_base<WT>(w1, w1s, sl.e, E, h, rb), w_base<WT>(w3, w3s, sl.e, E, h, rb)};
-  // a tile past the last row (row0 >= h) still takes part in the barriers
 #define TRG_TILE(RM, NT, U, ROW0) \
-  up_tile<WT, RM, NT, U>(x, xb, wb, rb, sl.mask, gt, cnt, c0, ROW0, h, hid, hid_n, sl.off, wk, kw, tid, rd)
+  up_tile<WT, RM, NT, U>(x, xb, wb, rb, sl.mask, gt, cnt, c0, ROW0, h, hid, hid_n, sl.off, wk, wv, red)
   int c0 = 0;
   if (PRO || cnt <= 16) {
     TRG_TILE(RM, 1, U, row0);
@@ -636,8 +681,9 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
                                                                const void* __restrict__ w2,
                                                                const uint8_t* __restrict__ w2s, int E, int d, int h,
                                                                int rb, const int* __restrict__ n_active,
-                                                               const FewSlot* __restrict__ slots, int T,
-                                                               const int* __restrict__ n_live, void* __restrict__ y) {
+                                                               const FewSlot* __restrict__ slots, int slots_max,
+                                                               int T, const int* __restrict__ n_live,
+                                                               void* __restrict__ y) {
   constexpr int P = WT == kF32 ? 1 : 2;  // parts of h
   constexpr int XE = Piece<WT>::kXE;
   constexpr int RT = 16 / KS, CT = 16 / KS;
@@ -657,17 +703,18 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
     int off[U], c[U];
   };
   int s = wv / nit, c = wv - s * nit;  // the next item to load
-  // items f, f + kWaves, ...: one past the end repeats the last slot (so its
-  // loads are in bounds) for no token
+  // items f, f + kWaves, ...: one past the end reads expert 0 (so its loads are
+  // in bounds) for no token
   auto load = [&](Items& o, int f) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const bool in = f + u * kWaves < F;
-      const FewSlot sl = slots[in ? s : na - 1];
+      // read without waiting for n_active; from there on slots hold anything
+      const FewSlot sl = slots[min(s, slots_max - 1)];
       o.mask[u] = in ? sl.mask : 0;
-      o.off[u] = sl.off;
+      o.off[u] = in ? sl.off : 0;
       o.c[u] = in ? c * KS : 0;
-      const WBase wb = w_base<WT>(w2, w2s, sl.e, E, d, rb);
+      const WBase wb = w_base<WT>(w2, w2s, in ? sl.e : 0, E, d, rb);
       o.w[u] = w_load<WT>(wb, w_row<WT>(wb, row, rb), o.c[u] + kr, q, rb);
       c += kWaves;
       while (c >= nit) {
@@ -696,9 +743,9 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
       for (int z = 0; z < 4; ++z) acc[z] = on ? acc[z] + t[z] : acc[z];
     }
   };
+  Items a, b;
+  load(a, wv);
   if (wv < F) {
-    Items a, b;
-    load(a, wv);
     for (int f = wv + kWaves * U; f < F; f += kWaves * U) {
       load(b, f);
       multiply(a);
@@ -727,7 +774,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
 // bits, 0.25 % in bf16 at h = 2048.
 template <int WT, int RM, int NT, int U>
 TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb, int rb, int cnt, int col0, int row0,
-                       int d, int h, long pos0, int wk, int kw, int tid, float* red, float* __restrict__ yp) {
+                       int d, int h, long pos0, int wk, int kw, float* red, float* __restrict__ yp) {
   constexpr int P = WT == kF32 ? 1 : 2, XE = Piece<WT>::kXE;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   WRow wr[RM];
@@ -749,7 +796,7 @@ TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb
       if (m + i > 0) __syncthreads();
       put_tile(red + kw * 256, lane, acc[m][i]);
       __syncthreads();
-      for (int o = tid; o < 256; o += wk * 64) {
+      for (int o = threadIdx.x; o < 256; o += wk * 64) {
         const int lr = o & 15, col = o >> 4, c = col0 + i * 16 + col, row = row0 + m * 16 + lr;
         if (c < cnt && row < d) yp[(pos0 + c) * d + row] = sum_tile(red, wk, lr, col);
       }
@@ -760,24 +807,21 @@ template <int WT, int RM, int U>
 __global__ __launch_bounds__(kThreads, 4) void few_down_rows_kernel(const char* __restrict__ hid, long hid_n,
                                                                     const void* __restrict__ w2,
                                                                     const uint8_t* __restrict__ w2s, int E, int d,
-                                                                    int h, int rb, int wk,
-                                                                    const int* __restrict__ n_active,
+                                                                    int h, int rb, const int* __restrict__ n_active,
                                                                     const FewSlot* __restrict__ slots,
                                                                     float* __restrict__ yp) {
   __shared__ __attribute__((aligned(16))) float red[kWaves * 256];
-  const int wv = wave_id(), G = kWaves / wk;
-  const int tiles = (d + 16 * RM * G - 1) / (16 * RM * G);
+  const int wv = wave_id(), wk = blockDim.x >> 6;
+  const int tiles = (d + 16 * RM - 1) / (16 * RM);
   const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
-  const int grp = wv / wk, kw = wv % wk, tid = threadIdx.x - grp * wk * 64;
-  const int row0 = (tile * G + grp) * 16 * RM;
+  const int row0 = tile * 16 * RM;
   const int na = *n_active;
   const FewSlot sl = slots[slot];  // in bounds; meaningful if slot < na
   if (slot >= na) return;
   const int cnt = __popcll(sl.mask);
-  float* rd = red + grp * wk * 256;
   const WBase wb[1] = {w_base<WT>(w2, w2s, sl.e, E, d, rb)};
 #define TRG_TILE(RM, NT, U, ROW0) \
-  down_tile<WT, RM, NT, U>(hid, hid_n, wb, rb, cnt, c0, ROW0, d, h, sl.off, wk, kw, tid, rd, yp)
+  down_tile<WT, RM, NT, U>(hid, hid_n, wb, rb, cnt, c0, ROW0, d, h, sl.off, wk, wv, red, yp)
   int c0 = 0;
   if (cnt <= 16) {
     TRG_TILE(RM, 1, U, row0);
@@ -827,11 +871,9 @@ hipError_t linear_nt(const void* x, const void* w, const uint8_t* ws, int T, int
 
 // Waves that share a row tile along k, from a weight row's bytes: a wave needs
 // some lines to itself, and long rows need the waves (one wave a 12 KB row has
-// too few loads in flight).  Measured, us a pass with 8 / 4 / 2 / 1 waves in
-// both projections: 24 tokens, rows of 12 and 4 KB 1856 / 1954 / 1993 / 1986;
-// 61 tokens, rows of 1 KB and 512 bytes 124 / 115 / 114 / 119 (the up projection
-// varied) and 126 / 113 / 115 / 113 (the down); one token, rows of 4 KB 18.9 /
-// 21.4 / 29.2 / 45.3.
+// too few loads in flight).  Measured, us a pass with 8 / 4 / 2 / 1 waves: 24
+// tokens, rows of 12 and 4 KB 1843 / 1926 / 2018 / 2029; 61 tokens, rows of 1 KB
+// and 512 bytes 132 / 108 / 110 / 117.
 int row_waves(int rb) { return rb >= 4096 ? 8 : 4; }
 
 bool in_prologue(int T, int k) { return T <= kProTokens && T * k <= kProEntries; }
@@ -851,12 +893,17 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   const bool pro = in_prologue(a.T, a.k);
   const int R = a.T * a.k, slots_max = R < a.E ? R : a.E;
   const long hid_n = (long)hid_rows(a.T, a.E, a.k) * a.h;
-  constexpr int RT = WT == kF32 ? kF32 : kBF16;  // the router's weights are in x's type
   const int xb = a.d * XE;
-  hipError_t e = a.T <= 16   ? linear_nt<RT, 1, 1, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, kLogitParts, a.n_live, logits, st)
-                 : a.T <= 32 ? linear_nt<RT, 1, 2, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, kLogitParts, a.n_live, logits, st)
-                             : linear_nt<RT, 1, 4, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, kLogitParts, a.n_live, logits, st);
-  if (e != hipSuccess) return e;
+  const bool router = pro && a.E <= 16 && a.E * xb <= kProRouter;
+  hipError_t e = hipSuccess;
+  if (!router) {
+    constexpr int RT = WT == kF32 ? kF32 : kBF16;
+#define TRG_LOGITS(NT) \
+  linear_nt<RT, 1, NT, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, kLogitParts, a.n_live, logits, st)
+    e = a.T <= 16 ? TRG_LOGITS(1) : a.T <= 32 ? TRG_LOGITS(2) : TRG_LOGITS(4);
+#undef TRG_LOGITS
+    if (e != hipSuccess) return e;
+  }
   if (!pro) {
 #define TRG_ROUTE(N)                                                                                                  \
   few_route_kernel<N><<<1, 1024, 0, st>>>(logits, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, n_active, slots, \
@@ -872,32 +919,32 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   // bytes of a weight row
   const int rb1 = WT == kE2M1 ? a.d / 2 : a.d * XE, rb2 = WT == kE2M1 ? a.h / 2 : a.h * XE;
   constexpr int U = WT == kE2M1 ? 1 : 2;
-  const int uw = row_waves(rb1), G = kWaves / uw;
-#define TRG_UP(RM, U, EPL, PRO)                                                                                       \
-  few_up_kernel<WT, RM, U, EPL, PRO><<<(unsigned)slots_max * ((a.h + 16 * RM * G - 1) / (16 * RM * G)), kThreads, 0,  \
-                                       st>>>((const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.T, a.E, a.k, a.h, rb1, \
-                                             uw, logits, a.n_live, a.topk_idx, a.topk_w, n_active, slots, gate, hid,  \
+#define TRG_UP(RM, U, EPL, PRO, ROUTER)                                                                                       \
+  few_up_kernel<WT, RM, U, EPL, PRO, ROUTER><<<(unsigned)slots_max * ((a.h + 16 * RM - 1) / (16 * RM)),                       \
+                                       PRO ? kThreads : 64 * row_waves(rb1), 0, st>>>(                                \
+                                             (const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.wr, a.T, a.E, a.k, a.h, rb1, \
+                                             logits, a.n_live, a.topk_idx, a.topk_w, n_active, slots, gate, hid,  \
                                              hid_n)
-  if (!pro) TRG_UP(2, U, 1, false);
-  else if (a.E <= 128) TRG_UP(1, 2 * U, 2, true);
-  else if (a.E <= 512) TRG_UP(1, 2 * U, 8, true);
-  else TRG_UP(1, 2 * U, 16, true);
+  if (!pro) TRG_UP(2, U, 1, false, false);
+  else if (router) TRG_UP(1, 2 * U, 1, true, true);
+  else if (a.E <= 128) TRG_UP(1, 2 * U, 2, true, false);
+  else if (a.E <= 512) TRG_UP(1, 2 * U, 8, true, false);
+  else TRG_UP(1, 2 * U, 16, true, false);
 #undef TRG_UP
   e = hipGetLastError();
   if (e != hipSuccess) return e;
 #define TRG_DOWN(KS)                                                                                                \
   few_down_kernel<WT, U, KS><<<(a.d + 16 / KS - 1) / (16 / KS), kThreads, 0, st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, \
-                                                                                   a.h, rb2, n_active, slots, a.T,  \
-                                                                                   a.n_live, a.y)
+                                                                                   a.h, rb2, n_active, slots,       \
+                                                                                   slots_max, a.T, a.n_live, a.y)
   if (pro) {
     if (a.T <= 4) TRG_DOWN(4);
     else TRG_DOWN(2);
     return hipGetLastError();
   }
 #undef TRG_DOWN
-  const int dw = row_waves(rb2), rows = 64 * (kWaves / dw);
-  few_down_rows_kernel<WT, 4, 1><<<(unsigned)slots_max * ((a.d + rows - 1) / rows), kThreads, 0, st>>>(
-      hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, dw, n_active, slots, yp);
+  few_down_rows_kernel<WT, 4, 1><<<(unsigned)slots_max * ((a.d + 63) / 64), 64 * row_waves(rb2), 0, st>>>(
+      hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, n_active, slots, yp);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 jg((a.d / 4 + 255) / 256, a.T);
@@ -920,14 +967,33 @@ hipError_t launch_few_fwd(const moe_few_args& a, hipStream_t st) {
 
 hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
                               hipStream_t st) {
-  // four row tiles a wave once there are rows enough for two workgroups a CU:
-  // the tokens' operand, four times the weights' bytes, is then read once for
-  // 64 rows
+  // Row tiles a wave: the tokens' operand, four times the weights' bytes, is
+  // read once for all of them, but the chip works in rounds of as many
+  // workgroups as it holds (two a CU, one where the accumulators are large), so
+  // the count with the fewest tiles in sequence wins, the larger of two equal
+  // ones.  Measured for 13 tokens and 24576 x 6144 (1536 tiles): 1 / 2 / 3 / 4
+  // tiles 37.6 / 24.8 / 22.8 / 25.8 us.
+  const long tiles = (n + 15) / 16;
+  const int nt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  int nm = 1;
+  long best = 0;
+  for (int m = 1; m <= 4; ++m) {
+    const long held = 256 * (m * nt > 4 ? 1 : 2), groups = (tiles + m - 1) / m;
+    const long seq = (groups + held - 1) / held * m;
+    if (m == 1 || seq <= best) {
+      best = seq;
+      nm = m;
+    }
+  }
+#define TRG_NT(NM) return nt == 1 ? TRG_LINEAR(NM, 1) : nt == 2 ? TRG_LINEAR(NM, 2) : TRG_LINEAR(NM, 4)
 #define TRG_LINEAR(NM, NT) \
   linear_nt<kE2M1, NM, NT, 1, uint16_t>(x, q, s, T, n, K / 2, K * 2, 1, nullptr, (uint16_t*)y, st)
-  if (n >= 64 * 384) return T <= 16 ? TRG_LINEAR(4, 1) : T <= 32 ? TRG_LINEAR(4, 2) : TRG_LINEAR(4, 4);
-  return T <= 16 ? TRG_LINEAR(1, 1) : T <= 32 ? TRG_LINEAR(1, 2) : TRG_LINEAR(1, 4);
+  if (nm == 1) TRG_NT(1);
+  if (nm == 2) TRG_NT(2);
+  if (nm == 3) TRG_NT(3);
+  TRG_NT(4);
 #undef TRG_LINEAR
+#undef TRG_NT
 }
 
 }  // namespace trg
