@@ -568,7 +568,8 @@ moe_status_t mx_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, i
  *   they were, and their x is not used.
  *   topk_idx [T,k] i32, topk_w [T,k] f32 (nullable).
  *   y must not overlap x.
- *   ws: moe_few_workspace_size(T, d, E, k, h) bytes (not kept between calls);
+ *   ws: moe_few_workspace_size(T, d, E, k, h) bytes, enough for every smaller T
+ *   too (nothing is kept in it between calls);
  *   calls that may run concurrently need separate workspaces.
  */
 typedef struct {

@@ -782,7 +782,7 @@ static moe_status_t check_few_dims(const char* fn, int T, int d, int E, int k, i
 
 size_t moe_few_workspace_size(int T, int d, int E, int k, int h) {
   if (check_few_dims("moe_few_workspace_size", T, d, E, k, h) != MOE_OK) return 0;
-  return trg::few_ws_bytes(T, d, E, k, h);
+  return trg::few_ws_bytes_up_to(T, d, E, k, h);
 }
 
 moe_status_t moe_few_fwd(const moe_few_args* a, void* stream) {

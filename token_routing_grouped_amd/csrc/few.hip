@@ -53,13 +53,21 @@ struct FewSlot {
 // Rows of the hidden buffer: an entry's own, or (routing in the up
 // projection's prologue) T for every slot.
 bool in_prologue(int T, int k);
+bool tokens_down(int T, bool pro);  // few_down_kernel, not few_down_rows_kernel
 int hid_rows(int T, int E, int k) {
   const int R = T * k, S = R < E ? R : E;
   return in_prologue(T, k) ? S * T : R;
 }
-// Partial sums that the router's logits come in: its E / 16 row tiles alone
-// would leave most of the chip idle.
+// Partial sums that the router's logits come in (its E / 16 row tiles alone would
+// leave most of the chip idle): as many as leave each of a workgroup's 8 waves a
+// line.  Whoever adds them reads them all, so no more than that.  One part of 16
+// waves with two lines each measured 12.8 us instead of 5.0 (61 tokens, 128
+// experts, d = 2048).
 constexpr int kLogitParts = 8;
+int logit_parts(int row_bytes) {
+  const int p = ((row_bytes + 127) / 128 + 7) / 8;
+  return p < 1 ? 1 : (p > kLogitParts ? kLogitParts : p);
+}
 
 struct FewLayout {
   size_t n_active, slots, gate, logits, hid, pos, yp, bytes;
@@ -78,10 +86,11 @@ FewLayout few_layout(int T, int d, int E, int k, int h) {
   l.n_active = take(sizeof(int));
   l.slots = take(S * sizeof(FewSlot));
   l.gate = take(R * sizeof(float));
-  l.logits = take((size_t)kLogitParts * T * E * sizeof(float));
+  l.logits = take((size_t)logit_parts(d * 4) * T * E * sizeof(float));  // fp32 rows have the most lines
   l.hid = take((size_t)hid_rows(T, E, k) * h * sizeof(float));         // fp32, or the hi and lo bf16 halves
-  l.pos = take(pro ? 0 : R * sizeof(int));
-  l.yp = take(pro ? 0 : R * d * sizeof(float));
+  const bool rows = !tokens_down(T, pro);
+  l.pos = take(rows ? R * sizeof(int) : 0);
+  l.yp = take(rows ? (size_t)hid_rows(T, E, k) * d * sizeof(float) : 0);
   l.bytes = at;
   return l;
 }
@@ -237,25 +246,88 @@ TRG_DEV f32x4_t mma_step(const WStep& w, const XStep<WT>& x, f32x4_t acc) {
   return acc;
 }
 
+// ---- the tokens' operand of 4-bit lines, through LDS ---------------------------
+// A line of 4-bit weights meets 512 bytes of every token, and a lane needs 16 of
+// each 128: loaded directly, 64 lanes touch up to 64 cache lines an instruction,
+// eight times the same ones, and the address unit, not HBM, sets the pace (13
+// tokens, 24576 x 6144: 24.3 us, of which 15.6 are left without these loads;
+// staged 16.4).  So a wave copies them to its own kStage bytes of LDS, whole
+// cache lines an instruction, and its lanes read their pieces there: with one
+// part of the operand a line at a time, with two (the hidden vector's halves)
+// a piece of it, 256 bytes a token and part.  Place s of token n is stored at s
+// ^ n, so that the 16 tokens' reads of one place fall into different banks.  No
+// barrier: the buffer is one wave's, and its LDS instructions run in order.
+constexpr int kStage = 8192;
+
+// In two steps, so that the weights' loads can go out in between.  xo: lane r's
+// row offset of column r, which repeats the last column where there is none;
+// the first XN * (tokens an instruction) columns are copied.
+template <int P, int XN>
+struct Stage {
+  static constexpr int LT = P == 1 ? 32 : 16;  // lanes (16-byte places) a token
+  static constexpr int TI = 64 / LT;           // tokens an instruction
+  uint4 g[XN][P];
+};
+template <int P, int XN>
+TRG_DEV void stage_load(Stage<P, XN>& o, const char* xb, long xpart, uint32_t xo, int line, int piece, int row_bytes) {
+  constexpr int LT = Stage<P, XN>::LT, TI = Stage<P, XN>::TI;
+  const int lane = threadIdx.x & 63, s = lane % LT;
+  const int in_line = P == 1 ? s * 16 : (s >> 2) * 128 + piece * 64 + (s & 3) * 16;
+  const uint32_t off = (uint32_t)min(line * 512 + in_line, row_bytes - 16);
+#pragma unroll
+  for (int t = 0; t < XN; ++t) {
+    const uint32_t at = (uint32_t)__builtin_amdgcn_ds_bpermute((t * TI + lane / LT) * 4, (int)xo) + off;
+#pragma unroll
+    for (int p = 0; p < P; ++p) o.g[t][p] = *(const uint4*)(xb + p * xpart + at);
+  }
+}
+template <int P, int XN>
+TRG_DEV void stage_store(const Stage<P, XN>& o, char* xl) {
+  constexpr int LT = Stage<P, XN>::LT, TI = Stage<P, XN>::TI;
+  const int lane = threadIdx.x & 63, s = lane % LT;
+#pragma unroll
+  for (int t = 0; t < XN; ++t) {
+    const int tok = t * TI + lane / LT;
+#pragma unroll
+    for (int p = 0; p < P; ++p) *(uint4*)(xl + p * (kStage / 2) + tok * (LT * 16) + (s ^ tok) * 16) = o.g[t][p];
+  }
+}
+// Lane's four 16-byte parts of piece `piece` of part p.
+template <int P>
+TRG_DEV void staged_x(const char* xl, int r, int q, int piece, int p, uint4* x) {
+  constexpr int LT = P == 1 ? 32 : 16;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int s = P == 1 ? q * 8 + piece * 4 + j : q * 4 + j;
+    x[j] = *(const uint4*)(xl + p * (kStage / 2) + r * (LT * 16) + (s ^ r) * 16);
+  }
+}
+
 // ---- products of NM 16-row tiles with NT * 16 columns --------------------------
 // acc[m][n] over lines c0, c0 + step, ... < c1 of the rows, U lines at a time:
 // all their weights are loaded (from HBM), then the tokens' operand (P parts,
-// xpart bytes apart; from the caches), XB pieces at a time where the registers
-// do not hold more.  The waves of a CU hide each other's loads: NM * U * 2 KB
-// a wave in flight is several times what HBM's latency needs.
-// Tile m is rows wr[m] of matrix wb[m % NB], NB bases.
-// With one tile of columns only the lanes of columns that are `on` load it (a
-// few tokens are a few lanes); the others' registers hold anything: columns do
-// not mix, and theirs are not stored.
-template <int WT, int NB, int NM, int NT, int U, int P>
-TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const uint32_t* xo, long xpart, bool on,
-                         int rb, int c0, int c1, int step, int q, f32x4_t (*acc)[NT]) {
+// xpart bytes apart; from the caches).  The waves of a CU hide each other's
+// loads: NM * U * 2 KB a wave in flight is several times what HBM's latency
+// needs.  Tile m is rows wr[m] of matrix wb[m % NB], NB bases; cols: columns
+// that are there.
+// Only the lanes of those columns load the operand (a few tokens are a few
+// lanes); the others' registers hold anything: columns do not mix, and theirs
+// are not stored.  xl: the wave's staging buffer, XN the copying instructions
+// (4-bit weights; cols and more columns fit).
+template <int WT, int NB, int NM, int NT, int U, int P, int XN>
+TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const uint32_t* xo, long xpart, int cols,
+                         int rb, int c0, int c1, int step, int r, int q, f32x4_t (*acc)[NT], char* xl) {
   constexpr int KX = Piece<WT>::kX;
-  constexpr int XB = 2 * U * P * KX <= 8 ? 2 * U : 1;  // pieces of the operand at once: at most 32 registers
+  static_assert(WT != kE2M1 || U == 1, "a staging buffer holds one line");
+  constexpr int XB = WT == kE2M1 ? (P == 1 ? 2 : 1) : 2 * U;  // pieces of the operand at once
   const int past = (rb + 127) >> 7;  // a line that is past every row's end
   for (; c0 < c1; c0 += step * U) {
     WStep w[U][NM];
     int line[U];
+    // the first copy's loads go out before the weights', so that it is in LDS
+    // when they arrive
+    Stage<P, XN> st;
+    if constexpr (WT == kE2M1) stage_load<P, XN>(st, xb, xpart, xo[0], c0, 0, rb * 4);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       line[u] = c0 + u * step < c1 ? c0 + u * step : past;
@@ -268,7 +340,14 @@ TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const 
 #pragma unroll
       for (int b = 0; b < 2 * U; b += XB) {
         uint4 x[XB][P][KX];
-        if (NT > 1 || on) {
+        if constexpr (WT == kE2M1) {
+          if (n + b > 0) stage_load<P, XN>(st, xb, xpart, xo[n], c0, b, rb * 4);
+          stage_store<P, XN>(st, xl);
+#pragma unroll
+          for (int i = 0; i < XB; ++i)
+#pragma unroll
+            for (int p = 0; p < P; ++p) staged_x<P>(xl, r, q, b + i, p, x[i][p]);
+        } else if (NT > 1 || r < cols) {
 #pragma unroll
           for (int i = 0; i < XB; ++i)
 #pragma unroll
@@ -314,14 +393,16 @@ TRG_DEV int live_tokens(const int* n_live, int T) { return n_live != nullptr ? m
 // out[t, row] = <x[t], w[row]> for T <= NT * 16 columns.  A workgroup takes NM
 // tiles of 16 rows, its waves share the lines; blockIdx.y takes the part_lines
 // lines from blockIdx.y * part_lines and writes its own [T, n] of out.
-template <int WT, int NM, int NT, int U, class OUT>
-__global__ __launch_bounds__(kThreads, NM* NT > 4 ? 2 : 4) void few_linear_kernel(const char* __restrict__ x,
+template <int WT, int NM, int NT, int U, int XN, int WAVES, class OUT>
+__global__ __launch_bounds__(WAVES * 64, NT > 1 && NM* NT > 3 ? 2 : 4) void few_linear_kernel(const char* __restrict__ x,
                                                                  const void* __restrict__ w,
                                                                  const uint8_t* __restrict__ ws, int T, int n, int rb,
                                                                  int xb, int part_lines,
                                                                  const int* __restrict__ n_live,
                                                                  OUT* __restrict__ out) {
-  __shared__ __attribute__((aligned(16))) float red[kWaves * 256];
+  // the waves' staging buffers, then (1 KB a wave) their accumulators
+  __shared__ __attribute__((aligned(16))) char lds[WAVES * (WT == kE2M1 ? kStage : 1024)];
+  float* red = (float*)lds;
   const int lane = threadIdx.x & 63, wv = wave_id(), r = lane & 15, q = lane >> 4;
   const int live = live_tokens(n_live, T);
   const int row0 = blockIdx.x * (16 * NM);
@@ -338,18 +419,18 @@ __global__ __launch_bounds__(kThreads, NM* NT > 4 ? 2 : 4) void few_linear_kerne
   for (int m = 0; m < NM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0, 0, 0, 0};
-  stream_tile<WT, 1, NM, NT, U, 1>(wb, wr, x, xo, 0, r < live, rb, c0 + wv, c1, kWaves, q, acc);
+  stream_tile<WT, 1, NM, NT, U, 1, XN>(wb, wr, x, xo, 0, live, rb, c0 + wv, c1, WAVES, r, q, acc, lds + wv * kStage);
 #pragma unroll
   for (int m = 0; m < NM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      if (m + i > 0) __syncthreads();
+      if (WT == kE2M1 || m + i > 0) __syncthreads();
       put_tile(red + wv * 256, lane, acc[m][i]);
       __syncthreads();
       const int row = row0 + m * 16 + (threadIdx.x & 15), t = i * 16 + ((threadIdx.x >> 4) & 15);
       if (threadIdx.x < 256 && t < live && row < n)
         Elt<OUT>::st(out + ((long)blockIdx.y * T + t) * n + row,
-                     sum_tile(red, kWaves, threadIdx.x & 15, (threadIdx.x >> 4) & 15));
+                     sum_tile(red, WAVES, threadIdx.x & 15, (threadIdx.x >> 4) & 15));
     }
 }
 
@@ -402,45 +483,57 @@ TRG_DEV void route_token(float* v, int E, int k, int t, int lane, uint16_t* sel,
     s += p[i];
   }
   s = wave_sum_dpp(s);
+  int place[EPL], mine = 0;  // places of this lane's experts; lane j: the j-th choice
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) place[i] = -1;
   for (int j = 0; j < k; ++j) {
-    bool found = false;  // the same for the whole wave
+    // no branches: a round is a chain of dependent instructions as it is
+    int e = 0;
+#pragma unroll
+    for (int i = EPL - 1; i >= 0; --i) {
+      const unsigned long long at = __ballot(key[i] == top);
+      e = at != 0 ? 64 * i + __ffsll(at) - 1 : e;
+    }
+    mine = lane == j ? e : mine;
     uint32_t next = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const unsigned long long at = __ballot(key[i] == top);
-      if (!found && at != 0) {
-        found = true;
-        const int l = __ffsll((unsigned long long)at) - 1;
-        if (lane == l) {
-          const int e = l + 64 * i;
-          key[i] = 0;
-          sel[j] = (uint16_t)e;
-          selw[j] = p[i] / s;
-          atomicOr(&mask[e], 1ull << t);  // integer: the order does not matter
-        }
-      }
+      const bool hit = lane + 64 * i == e;
+      key[i] = hit ? 0u : key[i];
+      place[i] = hit ? j : place[i];
       next = max(next, key[i]);
     }
-    if (j + 1 < k) top = wave_max_u32(next);
+    top = wave_max_u32(next);
   }
+  if (lane < k) {
+    sel[lane] = (uint16_t)mine;
+    atomicOr(&mask[mine], 1ull << t);  // integer: the order does not matter
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i)
+    if (place[i] >= 0) selw[place[i]] = p[i] / s;
 }
 
 // out[j] = the router's partial logits at at[j] (of plane = T E values), added in
-// order.  All N * kLogitParts loads are in flight at once: one by one, each
-// group would wait for its own trip past L2 (other XCDs wrote them).
+// order; G parts of all N are in flight at once (other XCDs wrote them: every
+// trip goes past L2), past the last one it is loaded again and not added.
 template <int N>
-TRG_DEV void add_logits(const float* __restrict__ logits, uint32_t plane, const uint32_t* at, float* out) {
-  float raw[N][kLogitParts];
+TRG_DEV void add_logits(const float* __restrict__ logits, int parts, uint32_t plane, const uint32_t* at, float* out) {
+  constexpr int G = N <= 8 ? 4 : 2;
 #pragma unroll
-  for (int j = 0; j < N; ++j)
+  for (int j = 0; j < N; ++j) out[j] = 0.f;
+  for (int a0 = 0; a0 < parts; a0 += G) {
+    float raw[G][N];
 #pragma unroll
-    for (int a = 0; a < kLogitParts; ++a) raw[j][a] = logits[at[j] + (uint32_t)a * plane];
-  __builtin_amdgcn_sched_barrier(0);
+    for (int a = 0; a < G; ++a) {
+      const float* L = logits + (long)min(a0 + a, parts - 1) * plane;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    out[j] = raw[j][0];
+      for (int j = 0; j < N; ++j) raw[a][j] = L[at[j]];
+    }
 #pragma unroll
-    for (int a = 1; a < kLogitParts; ++a) out[j] += raw[j][a];
+    for (int a = 0; a < G; ++a)
+#pragma unroll
+      for (int j = 0; j < N; ++j) out[j] = a0 + a < parts ? out[j] + raw[a][j] : out[j];
   }
 }
 
@@ -451,7 +544,7 @@ constexpr int kRouteChunk = 8192;  // logits in LDS at a time
 // LDS, a wave routes a token at a time from there; then the chosen experts'
 // token masks are compacted, in expert order, into slots.
 template <int EPL>
-__global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict__ logits, int T, int E, int k,
+__global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict__ logits, int parts, int T, int E, int k,
                                                          const int* __restrict__ n_live, int* __restrict__ idx_out,
                                                          float* __restrict__ w_out, int* __restrict__ n_active,
                                                          FewSlot* __restrict__ slots, float* __restrict__ gate,
@@ -473,7 +566,7 @@ __global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict
 #pragma unroll
     for (int j = 0; j < kRouteChunk / 1024; ++j)
       at[j] = (uint32_t)(t0 * E + min((int)threadIdx.x + 1024 * j, n - 1));
-    add_logits<kRouteChunk / 1024>(logits, (uint32_t)T * (uint32_t)E, at, sum);
+    add_logits<kRouteChunk / 1024>(logits, parts, (uint32_t)T * (uint32_t)E, at, sum);
     __syncthreads();  // the chunk before has been read
 #pragma unroll
     for (int j = 0; j < kRouteChunk / 1024; ++j)
@@ -520,11 +613,12 @@ TRG_DEV int nth_token(unsigned long long mask, int lane, int c) {
 
 // RM * 16 rows of h for a slot's columns: both matrices' rows, shared by the
 // workgroup's wk waves along k (this one is kw), then h = gate * silu(g) * u.
-// red: 2 * wk * 256 floats.
-template <int WT, int RM, int NT, int U>
+// lds: 2 KB a wave (kStage with 4-bit weights).
+template <int WT, int RM, int NT, int U, int XN>
 TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb, unsigned long long mask,
                      const float* gate, int cnt, int col0, int row0, int h, char* hid, long hid_n, long pos0, int wk,
-                     int kw, float* red) {
+                     int kw, char* lds) {
+  float* red = (float*)lds;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   WRow wr[2 * RM];
 #pragma unroll
@@ -541,12 +635,13 @@ TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb
   for (int m = 0; m < 2 * RM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0, 0, 0, 0};
-  stream_tile<WT, 2, 2 * RM, NT, U, 1>(wb, wr, x, xo, 0, r < cnt, rb, kw, (rb + 127) >> 7, wk, q, acc);
+  stream_tile<WT, 2, 2 * RM, NT, U, 1, XN>(wb, wr, x, xo, 0, cnt - col0, rb, kw, (rb + 127) >> 7, wk, r, q, acc,
+                                       lds + kw * kStage);
 #pragma unroll
   for (int m = 0; m < RM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      if (m + i > 0) __syncthreads();
+      if (WT == kE2M1 || m + i > 0) __syncthreads();
       put_tile(red + kw * 256, lane, acc[2 * m][i]);
       put_tile(red + (wk + kw) * 256, lane, acc[2 * m + 1][i]);
       __syncthreads();
@@ -568,25 +663,25 @@ TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb
     }
 }
 
-constexpr int kProTokens = kWaves;  // tokens and entries that the up projection routes itself
-constexpr int kProEntries = 64;
-constexpr int kProRouter = 65536;
+constexpr int kProTokens = 2 * kWaves;  // tokens and entries that the up projection routes itself
+constexpr int kProEntries = 64;         // a lane an entry
+constexpr int kProRouter = 65536;       // bytes of router weights
 
-// PRO: every workgroup routes the (few) tokens in its prologue, a wave a token,
-// instead of waiting for a launch that does it once; the slots' first
-// workgroups leave them for the down projection.  ROUTER: it computes their
-// logits too (at most 16 experts and kProRouter bytes of router weights, which
-// every workgroup reads).  Slots are then in the order
-// of their first (token, place), a lane an entry, and slot s has hid rows s * T.
+// PRO: every workgroup routes the (few) tokens in its prologue, a wave a token or
+// two, instead of waiting for a launch that does it once; the slots' first
+// workgroups leave them, and (pos_out) where the join finds their rows.  ROUTER:
+// it computes their logits too (at most 16 experts and kProRouter bytes of
+// router weights, which every workgroup reads).  Slots are then in the order of
+// their first (token, place), and slot s has hid rows s * T.
 template <int WT, int RM, int U, int EPL, bool PRO, bool ROUTER>
 __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     const char* __restrict__ x, int xb, const void* __restrict__ w1, const uint8_t* __restrict__ w1s,
-    const void* __restrict__ w3, const uint8_t* __restrict__ w3s, const void* __restrict__ wr, int T,
-    int E, int k, int h, int rb, const float* __restrict__ logits, const int* __restrict__ n_live, int* __restrict__ idx_out,
-    float* __restrict__ w_out, int* __restrict__ n_active, FewSlot* __restrict__ slots, float* __restrict__ gate,
-    char* __restrict__ hid, long hid_n) {
+    const void* __restrict__ w3, const uint8_t* __restrict__ w3s, const void* __restrict__ wr, int T, int E, int k,
+    int h, int rb, const float* __restrict__ logits, int parts, const int* __restrict__ n_live,
+    int* __restrict__ idx_out, float* __restrict__ w_out, int* __restrict__ n_active, FewSlot* __restrict__ slots,
+    float* __restrict__ gate, int* __restrict__ pos_out, char* __restrict__ hid, long hid_n) {
   const int wk = blockDim.x >> 6;  // all its waves share a row tile
-  __shared__ __attribute__((aligned(16))) float red[2 * kWaves * 256];
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // lds_bytes<WT>(waves, 2)
   const int lane = threadIdx.x & 63, wv = wave_id();
   const int tiles = (h + 16 * RM - 1) / (16 * RM);
   const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
@@ -600,7 +695,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     __shared__ float mygate[kProTokens];
     const int live = live_tokens(n_live, T), entries = live * k;
     for (int e = threadIdx.x; e < EPL * 64; e += kThreads) mask[e] = 0;  // launched with kThreads
-    float v[EPL];
+    float* red = (float*)lds;
     if constexpr (ROUTER) {
       // at most 16 experts: one row tile, its lines shared by the waves
       constexpr int RT = WT == kF32 ? kF32 : kBF16;  // the router's weights are in x's type
@@ -609,20 +704,23 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
       const WRow row[1] = {w_row<RT>(wb[0], min(r, E - 1), xb)};
       const uint32_t xo[1] = {(uint32_t)min(r, T - 1) * (uint32_t)xb};
       f32x4_t acc[1][1] = {{{0, 0, 0, 0}}};
-      stream_tile<RT, 1, 1, 1, 4, 1>(wb, row, x, xo, 0, r < live, xb, wv, (xb + 127) >> 7, kWaves, q, acc);
+      stream_tile<RT, 1, 1, 1, 4, 1, 1>(wb, row, x, xo, 0, live, xb, wv, (xb + 127) >> 7, kWaves, r, q, acc, nullptr);
       put_tile(red + wv * 256, lane, acc[0][0]);
-      __syncthreads();
-      v[0] = sum_tile(red, kWaves, lane & 15, wv);
-    } else {
-      uint32_t at[EPL];
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) at[i] = (uint32_t)(min(wv, T - 1) * E + min(lane + 64 * i, E - 1));
-      constexpr int B = EPL < 4 ? EPL : 4;
-#pragma unroll
-      for (int i = 0; i < EPL; i += B) add_logits<B>(logits, (uint32_t)T * (uint32_t)E, at + i, v + i);
-      __syncthreads();
     }
-    if (wv < live) route_token<EPL>(v, E, k, wv, lane, sel + wv * k, selw + wv * k, mask);
+    __syncthreads();
+#pragma unroll 1
+    for (int tk = wv; tk < live; tk += kWaves) {
+      float v[EPL];
+      if constexpr (ROUTER) {
+        v[0] = sum_tile(red, kWaves, lane & 15, tk);
+      } else {
+        uint32_t at[EPL];
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) at[i] = (uint32_t)(tk * E + min(lane + 64 * i, E - 1));
+        add_logits<EPL>(logits, parts, (uint32_t)T * (uint32_t)E, at, v);
+      }
+      route_token<EPL>(v, E, k, tk, lane, sel + tk * k, selw + tk * k, mask);
+    }
     __syncthreads();
     // every wave: lane = entry (token lane / k, place lane % k)
     const int e = lane < entries ? sel[lane] : 0, t = lane / k;
@@ -639,7 +737,11 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     sl.e = __builtin_amdgcn_readfirstlane(__shfl(e, at, 64));
     sl.mask = mask[sl.e];
     sl.off = slot * T;
-    if (wv == 0 && lane < entries && e == sl.e) mygate[__popcll(sl.mask & ((1ull << t) - 1))] = selw[lane];
+    if (wv == 0 && lane < entries && e == sl.e) {
+      const int rank = __popcll(sl.mask & ((1ull << t) - 1));
+      mygate[rank] = selw[lane];
+      if (tile == 0 && pos_out != nullptr) pos_out[lane] = sl.off + rank;
+    }
     if (tile == 0 && threadIdx.x == 0) slots[slot] = sl;
     gt = mygate;  // read after the products' barrier
   } else {
@@ -650,20 +752,30 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
   }
   const int cnt = __popcll(sl.mask);
   const WBase wb[2] = {w_base<WT>(w1, w1s, sl.e, E, h, rb), w_base<WT>(w3, w3s, sl.e, E, h, rb)};
-#define TRG_TILE(RM, NT, U, ROW0) \
-  up_tile<WT, RM, NT, U>(x, xb, wb, rb, sl.mask, gt, cnt, c0, ROW0, h, hid, hid_n, sl.off, wk, wv, red)
+#define TRG_TILE(RM, NT, U, XN, ROW0) \
+  up_tile<WT, RM, NT, U, XN>(x, xb, wb, rb, sl.mask, gt, cnt, c0, ROW0, h, hid, hid_n, sl.off, wk, wv, lds)
   int c0 = 0;
-  if (PRO || cnt <= 16) {
-    TRG_TILE(RM, 1, U, row0);
+  if constexpr (PRO) {
+    if (WT == kE2M1 && cnt > 2) TRG_TILE(RM, 1, U, 8, row0);
+    else TRG_TILE(RM, 1, U, 1, row0);
+  } else if constexpr (WT == kE2M1) {
+    // 4-bit rows are read again for every 16 tokens (from L2): the accumulators
+    // of more columns and the staging do not fit into the registers together
+    if (cnt <= 4) TRG_TILE(RM, 1, U, 2, row0);
+    else
+      for (; c0 < cnt; c0 += 16) {
+        if (c0 > 0) __syncthreads();
+        TRG_TILE(RM, 1, U, 8, row0);
+      }
+  } else if (cnt <= 16) {
+    TRG_TILE(RM, 1, U, 1, row0);
   } else {
     // more columns: their accumulators take the registers of the second row tile
-    constexpr int NT = WT == kE2M1 ? 2 : 4;
-    for (; c0 < cnt; c0 += 16 * NT)
-      for (int m = 0; m < RM; ++m) {
-        if (c0 + m > 0) __syncthreads();
-        if (cnt - c0 <= 32) TRG_TILE(1, 2, 1, row0 + 16 * m);
-        else TRG_TILE(1, NT, 1, row0 + 16 * m);
-      }
+    for (int m = 0; m < RM; ++m) {
+      if (m > 0) __syncthreads();
+      if (cnt <= 32) TRG_TILE(1, 2, 1, 1, row0 + 16 * m);
+      else TRG_TILE(1, 4, 1, 1, row0 + 16 * m);
+    }
   }
 #undef TRG_TILE
 }
@@ -772,9 +884,10 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
 // join adds each token's k rows in order.  Those rows are R d floats, out and
 // in: 3 % of the weights' bytes with two tokens an expert at h = 1024 and 4
 // bits, 0.25 % in bf16 at h = 2048.
-template <int WT, int RM, int NT, int U>
+template <int WT, int RM, int NT, int U, int XN>
 TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb, int rb, int cnt, int col0, int row0,
-                       int d, int h, long pos0, int wk, int kw, float* red, float* __restrict__ yp) {
+                       int d, int h, long pos0, int wk, int kw, char* lds, float* __restrict__ yp) {
+  float* red = (float*)lds;
   constexpr int P = WT == kF32 ? 1 : 2, XE = Piece<WT>::kXE;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   WRow wr[RM];
@@ -788,12 +901,13 @@ TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb
   for (int m = 0; m < RM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0, 0, 0, 0};
-  stream_tile<WT, 1, RM, NT, U, P>(wb, wr, hid, xo, hid_n * XE, r < cnt, rb, kw, (rb + 127) >> 7, wk, q, acc);
+  stream_tile<WT, 1, RM, NT, U, P, XN>(wb, wr, hid, xo, hid_n * XE, cnt - col0, rb, kw, (rb + 127) >> 7, wk, r, q, acc,
+                                   lds + kw * kStage);
 #pragma unroll
   for (int m = 0; m < RM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-      if (m + i > 0) __syncthreads();
+      if (WT == kE2M1 || m + i > 0) __syncthreads();
       put_tile(red + kw * 256, lane, acc[m][i]);
       __syncthreads();
       for (int o = threadIdx.x; o < 256; o += wk * 64) {
@@ -810,7 +924,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_rows_kernel(const char* 
                                                                     int h, int rb, const int* __restrict__ n_active,
                                                                     const FewSlot* __restrict__ slots,
                                                                     float* __restrict__ yp) {
-  __shared__ __attribute__((aligned(16))) float red[kWaves * 256];
+  extern __shared__ __attribute__((aligned(16))) char lds[];  // lds_bytes<WT>(waves, 1)
   const int wv = wave_id(), wk = blockDim.x >> 6;
   const int tiles = (d + 16 * RM - 1) / (16 * RM);
   const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
@@ -820,19 +934,24 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_rows_kernel(const char* 
   if (slot >= na) return;
   const int cnt = __popcll(sl.mask);
   const WBase wb[1] = {w_base<WT>(w2, w2s, sl.e, E, d, rb)};
-#define TRG_TILE(RM, NT, U, ROW0) \
-  down_tile<WT, RM, NT, U>(hid, hid_n, wb, rb, cnt, c0, ROW0, d, h, sl.off, wk, wv, red, yp)
+#define TRG_TILE(RM, NT, U, XN, ROW0) \
+  down_tile<WT, RM, NT, U, XN>(hid, hid_n, wb, rb, cnt, c0, ROW0, d, h, sl.off, wk, wv, lds, yp)
   int c0 = 0;
-  if (cnt <= 16) {
-    TRG_TILE(RM, 1, U, row0);
-  } else {
-    constexpr int NT = WT == kE2M1 ? 2 : 4;
-    for (; c0 < cnt; c0 += 16 * NT)
-      for (int m = 0; m < RM; m += 2) {
-        if (c0 + m > 0) __syncthreads();
-        if (cnt - c0 <= 32) TRG_TILE(2, 2, 1, row0 + 16 * m);
-        else TRG_TILE(2, NT, 1, row0 + 16 * m);
+  if constexpr (WT == kE2M1) {
+    if (cnt <= 4) TRG_TILE(RM, 1, U, 1, row0);
+    else
+      for (; c0 < cnt; c0 += 16) {
+        if (c0 > 0) __syncthreads();
+        TRG_TILE(RM, 1, U, 4, row0);
       }
+  } else if (cnt <= 16) {
+    TRG_TILE(RM, 1, U, 1, row0);
+  } else {
+    for (int m = 0; m < RM; m += 2) {
+      if (m > 0) __syncthreads();
+      if (cnt <= 32) TRG_TILE(2, 2, 1, 1, row0 + 16 * m);
+      else TRG_TILE(2, 4, 1, 1, row0 + 16 * m);
+    }
   }
 #undef TRG_TILE
 }
@@ -846,12 +965,22 @@ __global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__
   const int t = blockIdx.y;
   if (i >= d || t >= live_tokens(n_live, T)) return;
   float4 a = make_float4(0, 0, 0, 0);
-  for (int j = 0; j < k; ++j) {
-    const float4 b = *(const float4*)(yp + (long)pos[t * k + j] * d + i);
-    a.x += b.x;
-    a.y += b.y;
-    a.z += b.z;
-    a.w += b.w;
+  constexpr int B = 8;  // rows in flight; past the last one it is loaded again and not added
+  for (int j0 = 0; j0 < k; j0 += B) {
+    int p[B];
+    float4 b[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) p[j] = pos[t * k + min(j0 + j, k - 1)];
+#pragma unroll
+    for (int j = 0; j < B; ++j) b[j] = *(const float4*)(yp + (long)p[j] * d + i);
+#pragma unroll
+    for (int j = 0; j < B; ++j)
+      if (j0 + j < k) {
+        a.x += b[j].x;
+        a.y += b[j].y;
+        a.z += b[j].z;
+        a.w += b[j].w;
+      }
   }
   OUT* o = y + (long)t * d + i;
   Elt<OUT>::st(o, a.x);
@@ -860,21 +989,35 @@ __global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__
   Elt<OUT>::st(o + 3, a.w);
 }
 
-template <int WT, int NM, int NT, int U, class OUT>
+template <int WT, int NM, int NT, int U, int XN, int WAVES, class OUT>
 hipError_t linear_nt(const void* x, const void* w, const uint8_t* ws, int T, int n, int rb, int xb, int parts,
                      const int* n_live, OUT* out, hipStream_t st) {
   const int lines = (rb + 127) / 128, pl = (lines + parts - 1) / parts;
-  few_linear_kernel<WT, NM, NT, U, OUT><<<dim3((n + 16 * NM - 1) / (16 * NM), parts), kThreads, 0, st>>>(
+  few_linear_kernel<WT, NM, NT, U, XN, WAVES, OUT><<<dim3((n + 16 * NM - 1) / (16 * NM), parts), WAVES * 64, 0, st>>>(
       (const char*)x, w, ws, T, n, rb, xb, pl, n_live, out);
   return hipGetLastError();
 }
 
-// Waves that share a row tile along k, from a weight row's bytes: a wave needs
-// some lines to itself, and long rows need the waves (one wave a 12 KB row has
-// too few loads in flight).  Measured, us a pass with 8 / 4 / 2 / 1 waves: 24
-// tokens, rows of 12 and 4 KB 1843 / 1926 / 2018 / 2029; 61 tokens, rows of 1 KB
-// and 512 bytes 132 / 108 / 110 / 117.
-int row_waves(int rb) { return rb >= 4096 ? 8 : 4; }
+// Waves that share a row tile along k, from a weight row's bytes and the row
+// tiles there may be: long rows need the waves (a wave by itself has too few
+// loads in flight), short ones leave a wave too little to do, and with many
+// tiles the chip is full without them.  Measured, us a pass with 8 / 4 / 2 / 1
+// waves: 24 tokens, 384 experts, rows of 12 and 4 KB 1843 / 1926 / 2018 / 2029; 61
+// tokens, 128 experts, rows of 4 and 2 KB 260 / 268 / 276 / 270, of 1 KB and 512
+// bytes (4 bits) 141 / 108 / 101 / 104; 16 tokens, 8 experts, 4 bits 26.7 / 26.6 /
+// 29.8 / 37.5.
+int row_waves(int rb, long tiles) { return rb >= 4096 ? 8 : (rb <= 1024 && tiles >= 4096 ? 2 : 4); }
+
+// LDS of a product's workgroup: the waves' accumulators of `tiles` matrices, or
+// their staging buffers.
+template <int WT>
+size_t lds_bytes(int waves, int tiles) {
+  return (size_t)waves * (WT == kE2M1 ? kStage : tiles * 1024);
+}
+
+// The down projection over tokens writes y itself, in one launch; its tiles of 4
+// or 8 rows need T <= 8.
+bool tokens_down(int T, bool pro) { return pro && T <= 8; }
 
 bool in_prologue(int T, int k) { return T <= kProTokens && T * k <= kProEntries; }
 
@@ -895,18 +1038,19 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   const long hid_n = (long)hid_rows(a.T, a.E, a.k) * a.h;
   const int xb = a.d * XE;
   const bool router = pro && a.E <= 16 && a.E * xb <= kProRouter;
+  const int parts = logit_parts(xb);
   hipError_t e = hipSuccess;
   if (!router) {
     constexpr int RT = WT == kF32 ? kF32 : kBF16;
 #define TRG_LOGITS(NT) \
-  linear_nt<RT, 1, NT, 1, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, kLogitParts, a.n_live, logits, st)
+  linear_nt<RT, 1, NT, 1, 1, kWaves, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, parts, a.n_live, logits, st)
     e = a.T <= 16 ? TRG_LOGITS(1) : a.T <= 32 ? TRG_LOGITS(2) : TRG_LOGITS(4);
 #undef TRG_LOGITS
     if (e != hipSuccess) return e;
   }
   if (!pro) {
 #define TRG_ROUTE(N)                                                                                                  \
-  few_route_kernel<N><<<1, 1024, 0, st>>>(logits, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, n_active, slots, \
+  few_route_kernel<N><<<1, 1024, 0, st>>>(logits, parts, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, n_active, slots, \
                                           gate, pos)
     if (a.E <= 64) TRG_ROUTE(1);
     else if (a.E <= 128) TRG_ROUTE(2);
@@ -918,18 +1062,22 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   }
   // bytes of a weight row
   const int rb1 = WT == kE2M1 ? a.d / 2 : a.d * XE, rb2 = WT == kE2M1 ? a.h / 2 : a.h * XE;
-  constexpr int U = WT == kE2M1 ? 1 : 2;
+  constexpr int U = WT == kE2M1 ? 1 : 2, UP = WT == kE2M1 ? 1 : 4;  // lines at a time
+  constexpr int UR = WT == kE2M1 ? 1 : 2;                             // row tiles a wave
+  const long up_tiles = (long)slots_max * ((a.h + 15) / 16), down_tiles = (long)slots_max * ((a.d + 15) / 16);
+  const int uw = pro ? kWaves : row_waves(rb1, up_tiles), dw = row_waves(rb2, down_tiles);
 #define TRG_UP(RM, U, EPL, PRO, ROUTER)                                                                                       \
   few_up_kernel<WT, RM, U, EPL, PRO, ROUTER><<<(unsigned)slots_max * ((a.h + 16 * RM - 1) / (16 * RM)),                       \
-                                       PRO ? kThreads : 64 * row_waves(rb1), 0, st>>>(                                \
+                                       uw * 64, lds_bytes<WT>(uw, 2), st>>>(                                          \
                                              (const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.wr, a.T, a.E, a.k, a.h, rb1, \
-                                             logits, a.n_live, a.topk_idx, a.topk_w, n_active, slots, gate, hid,  \
-                                             hid_n)
-  if (!pro) TRG_UP(2, U, 1, false, false);
-  else if (router) TRG_UP(1, 2 * U, 1, true, true);
-  else if (a.E <= 128) TRG_UP(1, 2 * U, 2, true, false);
-  else if (a.E <= 512) TRG_UP(1, 2 * U, 8, true, false);
-  else TRG_UP(1, 2 * U, 16, true, false);
+                                             logits, parts, a.n_live, a.topk_idx, a.topk_w, n_active, slots, gate, \
+                                             tokens_down(a.T, pro) ? nullptr : pos, hid, hid_n)
+  if (!pro && (UR == 1 || up_tiles < 1024)) TRG_UP(1, U, 1, false, false);  // two a wave would leave CUs idle
+  else if (!pro) TRG_UP(UR, U, 1, false, false);
+  else if (router) TRG_UP(1, UP, 1, true, true);
+  else if (a.E <= 128) TRG_UP(1, UP, 2, true, false);
+  else if (a.E <= 512) TRG_UP(1, UP, 8, true, false);
+  else TRG_UP(1, UP, 16, true, false);
 #undef TRG_UP
   e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -937,13 +1085,14 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   few_down_kernel<WT, U, KS><<<(a.d + 16 / KS - 1) / (16 / KS), kThreads, 0, st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, \
                                                                                    a.h, rb2, n_active, slots,       \
                                                                                    slots_max, a.T, a.n_live, a.y)
-  if (pro) {
+  if (tokens_down(a.T, pro)) {
     if (a.T <= 4) TRG_DOWN(4);
     else TRG_DOWN(2);
     return hipGetLastError();
   }
 #undef TRG_DOWN
-  few_down_rows_kernel<WT, 4, 1><<<(unsigned)slots_max * ((a.d + 63) / 64), 64 * row_waves(rb2), 0, st>>>(
+  few_down_rows_kernel<WT, 4, 1><<<(unsigned)slots_max * ((a.d + 63) / 64), 64 * dw, lds_bytes<WT>(dw, 1),
+                                   st>>>(
       hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, n_active, slots, yp);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
@@ -958,6 +1107,14 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
 }  // namespace
 
 size_t few_ws_bytes(int T, int d, int E, int k, int h) { return few_layout(T, d, E, k, h).bytes; }
+size_t few_ws_bytes_up_to(int T, int d, int E, int k, int h) {
+  size_t most = 0;  // not always the largest batch's: smaller ones may take another path
+  for (int t = 1; t <= T; ++t) {
+    const size_t b = few_layout(t, d, E, k, h).bytes;
+    most = b > most ? b : most;
+  }
+  return most;
+}
 
 hipError_t launch_few_fwd(const moe_few_args& a, hipStream_t st) {
   if (a.wt == MOE_E2M1) return few_any<kE2M1>(a, st);
@@ -967,27 +1124,28 @@ hipError_t launch_few_fwd(const moe_few_args& a, hipStream_t st) {
 
 hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
                               hipStream_t st) {
-  // Row tiles a wave: the tokens' operand, four times the weights' bytes, is
-  // read once for all of them, but the chip works in rounds of as many
-  // workgroups as it holds (two a CU, one where the accumulators are large), so
-  // the count with the fewest tiles in sequence wins, the larger of two equal
-  // ones.  Measured for 13 tokens and 24576 x 6144 (1536 tiles): 1 / 2 / 3 / 4
-  // tiles 37.6 / 24.8 / 22.8 / 25.8 us.
+  // Row tiles a wave: more read the tokens' operand fewer times, fewer leave less
+  // of the chip idle at the end.  The model: a workgroup costs its row tiles plus
+  // the staging of its column tiles, a CU does ceil(workgroups / 256) of them.
+  // Measured, 24576 x 6144 (1536 tiles), with 1 / 2 / 3 / 4 row tiles: 13 tokens
+  // 22.4 / 17.1 / 16.5 / 20.2 us, 32 tokens 34.7 / 29.7 / 26.2 / 30.6, 64 tokens
+  // 60.8 / 47.2 / 37.8 / 57.6; 6144 x 2048, 64 tokens 9.9 / 8.1 / 9.5 / 12.9.
   const long tiles = (n + 15) / 16;
   const int nt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
   int nm = 1;
   long best = 0;
   for (int m = 1; m <= 4; ++m) {
-    const long held = 256 * (m * nt > 4 ? 1 : 2), groups = (tiles + m - 1) / m;
-    const long seq = (groups + held - 1) / held * m;
-    if (m == 1 || seq <= best) {
-      best = seq;
+    const long cost = ((tiles + m - 1) / m + 255) / 256 * (m + nt);
+    if (m == 1 || cost < best) {
+      best = cost;
       nm = m;
     }
   }
-#define TRG_NT(NM) return nt == 1 ? TRG_LINEAR(NM, 1) : nt == 2 ? TRG_LINEAR(NM, 2) : TRG_LINEAR(NM, 4)
-#define TRG_LINEAR(NM, NT) \
-  linear_nt<kE2M1, NM, NT, 1, uint16_t>(x, q, s, T, n, K / 2, K * 2, 1, nullptr, (uint16_t*)y, st)
+#define TRG_LINEAR(NM, NT, XN) \
+  linear_nt<kE2M1, NM, NT, 1, XN, kWaves, uint16_t>(x, q, s, T, n, K / 2, K * 2, 1, nullptr, (uint16_t*)y, st)
+#define TRG_NT(NM)                                                                                           \
+  return T <= 4 ? TRG_LINEAR(NM, 1, 2) : nt == 1 ? TRG_LINEAR(NM, 1, 8) : nt == 2 ? TRG_LINEAR(NM, 2, 8) \
+                                                                                  : TRG_LINEAR(NM, 4, 8)
   if (nm == 1) TRG_NT(1);
   if (nm == 2) TRG_NT(2);
   if (nm == 3) TRG_NT(3);

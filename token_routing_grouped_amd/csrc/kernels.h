@@ -51,7 +51,8 @@ hipError_t launch_rmsnorm_bwd(const void* dy, const void* ds, const void* s, con
                               int d, bool bf16, void* dx, void* dw, void* ws, hipStream_t st);
 
 // the layer for a few tokens, and 4-bit weights
-size_t few_ws_bytes(int T, int d, int E, int k, int h);
+size_t few_ws_bytes(int T, int d, int E, int k, int h);        // of a call with T tokens
+size_t few_ws_bytes_up_to(int T, int d, int E, int k, int h);  // of every call with 0 to T tokens
 hipError_t launch_few_fwd(const moe_few_args& a, hipStream_t st);
 hipError_t launch_quantize_e2m1(const void* in, bool bf16, int rows, int cols, uint8_t* q, uint8_t* s, hipStream_t st);
 hipError_t launch_dequantize_e2m1(const uint8_t* q, const uint8_t* s, bool bf16, int rows, int cols, void* out,
