@@ -157,9 +157,9 @@ def _expect(t, dtype, name):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _stream():
+def _stream(dev=None):
     if _raw_stream is not None:
-        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device()))
+        return ctypes.c_void_p(_raw_stream(torch.cuda.current_device() if dev is None else dev))
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
@@ -478,19 +478,25 @@ def moe_grouped_gemm_bwd_mx_parts(parts, **kw):
 # norm, 4-bit weights, the layer for a few tokens
 # ---------------------------------------------------------------------------
 
-def _arg(t, dtype, numel, name):
+def _device(t):
+    """The current device's number, -1 where a host tensor says that there is
+    no call to make (asking would start the GPU runtime)."""
+    return torch.cuda.current_device() if isinstance(t, torch.Tensor) and t.is_cuda else -1
+
+
+def _arg(t, dtype, numel, name, dev):
     """Device address of a tensor that must have this type and size and live on
-    the current device (the library launches there); None stays None."""
+    the current device, dev (the library launches there); None stays None."""
     if t is None:
         return None
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == torch.cuda.current_device() \
-            and t.dtype is dtype and t.numel() == numel and t.is_contiguous():
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev and t.dtype is dtype \
+            and t.numel() == numel and t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
         raise MoeError(f"{name}: tensor on {t.device}, expected the GPU")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise MoeError(f"{name}: tensor on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     if t.dtype != dtype:
         raise MoeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -505,8 +511,8 @@ def _matrix(t, name):
     return t.shape
 
 
-def _ws_arg(ws):
-    return _arg(ws, torch.uint8, ws.numel(), "ws")
+def _ws_arg(ws, dev):
+    return _arg(ws, torch.uint8, ws.numel(), "ws", dev)
 
 
 def mx_scale_bytes(rows: int, cols: int) -> int:
@@ -526,38 +532,41 @@ def moe_rmsnorm_fwd(x, w, eps, y, res=None, s=None, q=None, qs=None, rstd=None):
     """y = rmsnorm(x + res) * w; s = x + res, MXFP8 copy q / qs of y and rstd
     where given."""
     T, d = _matrix(x, "x")
-    n, dt = T * d, x.dtype
-    _check(lib().moe_rmsnorm_fwd(_arg(x, dt, n, "x"), _arg(res, dt, n, "res"), _arg(w, dt, d, "w"), T, d, eps, _dt(x),
-                                 _arg(s, dt, n, "s"), _arg(y, dt, n, "y"), _arg(q, torch.uint8, n, "q"),
-                                 _arg(qs, torch.uint8, mx_scale_bytes(T, d), "qs"),
-                                 _arg(rstd, torch.float32, T, "rstd"), _stream()), "moe_rmsnorm_fwd")
+    n, dt, dev = T * d, x.dtype, _device(x)
+    _check(lib().moe_rmsnorm_fwd(_arg(x, dt, n, "x", dev), _arg(res, dt, n, "res", dev), _arg(w, dt, d, "w", dev), T,
+                                 d, eps, _dt(x), _arg(s, dt, n, "s", dev), _arg(y, dt, n, "y", dev), _arg(q, torch.uint8, n, "q", dev),
+                                 _arg(qs, torch.uint8, mx_scale_bytes(T, d), "qs", dev),
+                                 _arg(rstd, torch.float32, T, "rstd", dev), _stream(dev)), "moe_rmsnorm_fwd")
 
 
 def moe_rmsnorm_bwd(dy, s, w, rstd, dx, dw, ws, ds=None):
     """dx (with ds, the gradient reaching s itself, added) and dw of
     moe_rmsnorm_fwd from its s and rstd."""
     T, d = _matrix(s, "s")
-    n, dt = T * d, s.dtype
-    _check(lib().moe_rmsnorm_bwd(_arg(dy, dt, n, "dy"), _arg(ds, dt, n, "ds"), _arg(s, dt, n, "s"),
-                                 _arg(w, dt, d, "w"), _arg(rstd, torch.float32, T, "rstd"), T, d, _dt(s),
-                                 _arg(dx, dt, n, "dx"), _arg(dw, dt, d, "dw"), _ws_arg(ws), ws.numel(), _stream()),
-           "moe_rmsnorm_bwd")
+    n, dt, dev = T * d, s.dtype, _device(s)
+    _check(lib().moe_rmsnorm_bwd(_arg(dy, dt, n, "dy", dev), _arg(ds, dt, n, "ds", dev), _arg(s, dt, n, "s", dev),
+                                 _arg(w, dt, d, "w", dev), _arg(rstd, torch.float32, T, "rstd", dev), T, d, _dt(s),
+                                 _arg(dx, dt, n, "dx", dev), _arg(dw, dt, d, "dw", dev), _ws_arg(ws, dev), ws.numel(),
+                                 _stream(dev)), "moe_rmsnorm_bwd")
 
 
 def mx_quantize_e2m1(x, q, s):
     """4-bit codes q [rows, cols/2] and scales s of x [rows, cols]."""
     rows, cols = _matrix(x, "x")
-    _check(lib().mx_quantize_e2m1(_arg(x, x.dtype, rows * cols, "x"), _dt(x), rows, cols,
-                                  _arg(q, torch.uint8, rows * cols // 2, "q"),
-                                  _arg(s, torch.uint8, mx_scale_bytes(rows, cols), "s"), _stream()), "mx_quantize_e2m1")
+    dev = _device(x)
+    _check(lib().mx_quantize_e2m1(_arg(x, x.dtype, rows * cols, "x", dev), _dt(x), rows, cols,
+                                  _arg(q, torch.uint8, rows * cols // 2, "q", dev),
+                                  _arg(s, torch.uint8, mx_scale_bytes(rows, cols), "s", dev), _stream(dev)),
+           "mx_quantize_e2m1")
 
 
 def mx_dequantize_e2m1(q, s, out):
     """The values that 4-bit codes and scales stand for, in out's type."""
     rows, cols = _matrix(out, "out")
-    _check(lib().mx_dequantize_e2m1(_arg(q, torch.uint8, rows * cols // 2, "q"),
-                                    _arg(s, torch.uint8, mx_scale_bytes(rows, cols), "s"), _dt(out), rows, cols,
-                                    _arg(out, out.dtype, rows * cols, "out"), _stream()), "mx_dequantize_e2m1")
+    dev = _device(out)
+    _check(lib().mx_dequantize_e2m1(_arg(q, torch.uint8, rows * cols // 2, "q", dev),
+                                    _arg(s, torch.uint8, mx_scale_bytes(rows, cols), "s", dev), _dt(out), rows, cols,
+                                    _arg(out, out.dtype, rows * cols, "out", dev), _stream(dev)), "mx_dequantize_e2m1")
 
 
 def mx_linear_e2m1(x, q, s, y):
@@ -566,22 +575,22 @@ def mx_linear_e2m1(x, q, s, y):
     Ty, n = _matrix(y, "y")
     if Ty != T:
         raise MoeError(f"y must have {T} rows, got {Ty}")
-    bf = torch.bfloat16
-    _check(lib().mx_linear_e2m1(_arg(x, bf, T * K, "x"), _arg(q, torch.uint8, n * K // 2, "q"),
-                                _arg(s, torch.uint8, mx_scale_bytes(n, K), "s"), T, n, K, _arg(y, bf, T * n, "y"),
-                                _stream()), "mx_linear_e2m1")
+    bf, dev = torch.bfloat16, _device(x)
+    _check(lib().mx_linear_e2m1(_arg(x, bf, T * K, "x", dev), _arg(q, torch.uint8, n * K // 2, "q", dev),
+                                _arg(s, torch.uint8, mx_scale_bytes(n, K), "s", dev), T, n, K,
+                                _arg(y, bf, T * n, "y", dev), _stream(dev)), "mx_linear_e2m1")
 
 
 def few_args(k, wr, w1, w3, w2, ws, w1s=None, w3s=None, w2s=None):
     """A FewArgs with the weights' and the workspace's fields filled in and
     checked; moe_few_fwd fills in the rest.  The caller keeps the tensors."""
     E, d = _matrix(wr, "wr")
-    dt = wr.dtype
+    dt, dev = wr.dtype, _device(wr)
     if not isinstance(w1, torch.Tensor) or w1.dim() != 3:
         raise MoeError("w1 must be [E, h, d], or packed [E, h, d/2]")
     h = w1.shape[1]
     a = FewArgs(d=d, E=E, k=k, h=h, dt=_dt(wr), wt=_dt(wr))
-    a.wr = _arg(wr, dt, E * d, "wr")
+    a.wr = _arg(wr, dt, E * d, "wr", dev)
     packed = w1.dtype == torch.uint8
     if packed:
         a.wt = MOE_E2M1
@@ -589,7 +598,7 @@ def few_args(k, wr, w1, w3, w2, ws, w1s=None, w3s=None, w2s=None):
         for name, t, rows, cols in (("w1s", w1s, E * h, d), ("w3s", w3s, E * h, d), ("w2s", w2s, E * d, h)):
             if t is None:
                 raise MoeError(f"{name} is needed with packed weights")
-            setattr(a, name, _arg(t, torch.uint8, mx_scale_bytes(rows, cols), name))
+            setattr(a, name, _arg(t, torch.uint8, mx_scale_bytes(rows, cols), name, dev))
     else:
         n, wdt = E * h * d, dt
         if w1s is not None or w3s is not None or w2s is not None:
@@ -598,8 +607,8 @@ def few_args(k, wr, w1, w3, w2, ws, w1s=None, w3s=None, w2s=None):
         want = (shape[0], shape[1], shape[2] // 2) if packed else shape
         if not isinstance(t, torch.Tensor) or tuple(t.shape) != want:
             raise MoeError(f"{name} must be {list(want)}")
-        setattr(a, name, _arg(t, wdt, n, name))
-    a.ws, a.ws_bytes = _ws_arg(ws), ws.numel()
+        setattr(a, name, _arg(t, wdt, n, name, dev))
+    a.ws, a.ws_bytes = _ws_arg(ws, dev), ws.numel()
     return a
 
 
@@ -608,10 +617,10 @@ def moe_few_fwd(a, x, y, topk_idx=None, topk_w=None, n_live=None):
     T, d = _matrix(x, "x")
     if d != a.d:
         raise MoeError(f"x must have {a.d} columns, got {d}")
-    dt = torch.float32 if a.dt == MOE_F32 else torch.bfloat16
+    dt, dev = torch.float32 if a.dt == MOE_F32 else torch.bfloat16, _device(x)
     a.T = T
-    a.x, a.y = _arg(x, dt, T * d, "x"), _arg(y, dt, T * d, "y")
-    a.topk_idx = _arg(topk_idx, torch.int32, T * a.k, "topk_idx")
-    a.topk_w = _arg(topk_w, torch.float32, T * a.k, "topk_w")
-    a.n_live = _arg(n_live, torch.int32, 1, "n_live")
-    _check(lib().moe_few_fwd(ctypes.byref(a), _stream()), "moe_few_fwd")
+    a.x, a.y = _arg(x, dt, T * d, "x", dev), _arg(y, dt, T * d, "y", dev)
+    a.topk_idx = _arg(topk_idx, torch.int32, T * a.k, "topk_idx", dev)
+    a.topk_w = _arg(topk_w, torch.float32, T * a.k, "topk_w", dev)
+    a.n_live = _arg(n_live, torch.int32, 1, "n_live", dev)
+    _check(lib().moe_few_fwd(ctypes.byref(a), _stream(dev)), "moe_few_fwd")

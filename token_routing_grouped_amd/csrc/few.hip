@@ -319,7 +319,6 @@ TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const 
                          int rb, int c0, int c1, int step, int r, int q, f32x4_t (*acc)[NT], char* xl) {
   constexpr int KX = Piece<WT>::kX;
   static_assert(WT != kE2M1 || U == 1, "a staging buffer holds one line");
-  constexpr int XB = WT == kE2M1 ? (P == 1 ? 2 : 1) : 2 * U;  // pieces of the operand at once
   const int past = (rb + 127) >> 7;  // a line that is past every row's end
   for (; c0 < c1; c0 += step * U) {
     WStep w[U][NM];
@@ -335,43 +334,63 @@ TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const 
       for (int m = 0; m < NM; ++m) w[u][m] = w_load<WT>(wb[m % NB], wr[m], line[u], q, rb);
     }
     const bool whole = (line[U - 1] + 1) * 128 <= rb;  // lines rise, so all of them are
+    if constexpr (WT == kE2M1) {
+      constexpr int XB = P == 1 ? 2 : 1;  // pieces staged at once
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int b = 0; b < 2 * U; b += XB) {
-        uint4 x[XB][P][KX];
-        if constexpr (WT == kE2M1) {
+        for (int b = 0; b < 2; b += XB) {
+          uint4 x[XB][P][KX];
           if (n + b > 0) stage_load<P, XN>(st, xb, xpart, xo[n], c0, b, rb * 4);
           stage_store<P, XN>(st, xl);
 #pragma unroll
           for (int i = 0; i < XB; ++i)
 #pragma unroll
             for (int p = 0; p < P; ++p) staged_x<P>(xl, r, q, b + i, p, x[i][p]);
-        } else if (NT > 1 || r < cols) {
+          if (n + b == 0 && !whole) {  // the first use of the weights: their loads are waited for here
 #pragma unroll
-          for (int i = 0; i < XB; ++i)
+            for (int m = 0; m < NM; ++m) w_mask<WT>(w[0][m], line[0], q, rb);
+          }
 #pragma unroll
-            for (int p = 0; p < P; ++p) x_piece<WT>(xb + p * xpart, xo[n], line[(b + i) / 2], q, (b + i) & 1, rb, x[i][p]);
+          for (int i = 0; i < XB; ++i) {
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+              acc[m][n] = mma_parts<WT, P>(w[0][m].v[b + i], e8m0((w[0][m].sb >> (8 * (b + i))) & 255u), x[i][0],
+                                           x[i][P - 1], acc[m][n]);
+            __builtin_amdgcn_sched_barrier(0);  // a piece's codes are decoded when it is used, not ahead
+          }
         }
-        if (n == 0 && b == 0 && !whole) {
+    } else {
+      // the operand of all columns at once: one trip to the caches a batch
+      constexpr int NB_X = NT * 2 * U * P <= 16 ? NT : 1;  // column tiles in registers: at most 64 of them
+#pragma unroll
+      for (int n0 = 0; n0 < NT; n0 += NB_X) {
+        uint4 x[NB_X][2 * U][P];
+        if (NT > 1 || r < cols) {
+#pragma unroll
+          for (int n = 0; n < NB_X; ++n)
+#pragma unroll
+            for (int i = 0; i < 2 * U; ++i)
+#pragma unroll
+              for (int p = 0; p < P; ++p) x_piece<WT>(xb + p * xpart, xo[n0 + n], line[i / 2], q, i & 1, rb, &x[n][i][p]);
+        }
+        if (n0 == 0 && !whole) {
 #pragma unroll
           for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int m = 0; m < NM; ++m) w_mask<WT>(w[u][m], line[u], q, rb);
         }
 #pragma unroll
-        for (int i = 0; i < XB; ++i) {
-          const int u = (b + i) / 2, z = (b + i) & 1;
+        for (int n = 0; n < NB_X; ++n)
 #pragma unroll
-          for (int m = 0; m < NM; ++m)
-            acc[m][n] = mma_parts<WT, P>(w[u][m].v[z], WT == kE2M1 ? e8m0((w[u][m].sb >> (8 * z)) & 255u) : 0.f,
-                                         x[i][0], x[i][P - 1], acc[m][n]);
-          // a piece's codes are decoded when it is used, not ahead
-          if (WT == kE2M1) __builtin_amdgcn_sched_barrier(0);
-        }
-        // or every block's operand is loaded at once, into scratch
-        if (XB < 2 * U || NT > 1) __builtin_amdgcn_sched_barrier(0);
+          for (int i = 0; i < 2 * U; ++i)
+#pragma unroll
+            for (int m = 0; m < NM; ++m)
+              acc[m][n0 + n] =
+                  mma_parts<WT, P>(w[i / 2][m].v[i & 1], 0.f, &x[n][i][0], &x[n][i][P - 1], acc[m][n0 + n]);
+        if (NB_X < NT) __builtin_amdgcn_sched_barrier(0);  // or all tiles' operands are loaded at once, into scratch
       }
+    }
   }
 }
 
@@ -773,7 +792,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     // more columns: their accumulators take the registers of the second row tile
     for (int m = 0; m < RM; ++m) {
       if (m > 0) __syncthreads();
-      if (cnt <= 32) TRG_TILE(1, 2, 1, 1, row0 + 16 * m);
+      if (cnt <= 32) TRG_TILE(1, 2, U, 1, row0 + 16 * m);
       else TRG_TILE(1, 4, 1, 1, row0 + 16 * m);
     }
   }
@@ -947,10 +966,11 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_rows_kernel(const char* 
   } else if (cnt <= 16) {
     TRG_TILE(RM, 1, U, 1, row0);
   } else {
-    for (int m = 0; m < RM; m += 2) {
+    constexpr int RN = RM > 2 ? 2 : RM;
+    for (int m = 0; m < RM; m += RN) {
       if (m > 0) __syncthreads();
-      if (cnt <= 32) TRG_TILE(2, 2, 1, 1, row0 + 16 * m);
-      else TRG_TILE(2, 4, 1, 1, row0 + 16 * m);
+      if (cnt <= 32) TRG_TILE(RN, 2, 1, 1, row0 + 16 * m);
+      else TRG_TILE(RN, 4, 1, 1, row0 + 16 * m);
     }
   }
 #undef TRG_TILE
@@ -1091,9 +1111,17 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
     return hipGetLastError();
   }
 #undef TRG_DOWN
-  few_down_rows_kernel<WT, 4, 1><<<(unsigned)slots_max * ((a.d + 63) / 64), 64 * dw, lds_bytes<WT>(dw, 1),
-                                   st>>>(
-      hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, n_active, slots, yp);
+  // Four row tiles a wave read the operand once for 64 rows; with few tiles that
+  // leaves CUs idle.  Measured with 1 / 2 / 4 a wave, 8 experts: 64 tokens 65.7 /
+  // 60.8 / 65.0 us in bf16 and 46.5 / 44.2 / 49.0 in 4 bits, 16 tokens 36.7 / 35.6 /
+  // 36.1; 128 experts, 61 tokens in 4 bits (4 a wave) 100, no more than 1 % apart.
+#define TRG_ROWS(RM, U)                                                                                             \
+  few_down_rows_kernel<WT, RM, U><<<(unsigned)slots_max * ((a.d + 16 * RM - 1) / (16 * RM)), 64 * dw,               \
+                                    lds_bytes<WT>(dw, 1), st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, n_active, \
+                                                                slots, yp)
+  if (down_tiles < 4096) TRG_ROWS(2, 1);
+  else TRG_ROWS(4, 1);
+#undef TRG_ROWS
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const dim3 jg((a.d / 4 + 255) / 256, a.T);

@@ -13,8 +13,8 @@
 // b%4, so a row's four scales of a 128-value chunk are one dword.  Places past
 // the row's last block hold 0.
 //
-// Both directions are one streaming pass bound by HBM: a lane takes one
-// 16-byte piece of the values, 4 (bf16) or 8 (fp32) lanes a block.
+// Both directions are one streaming pass bound by HBM: a lane takes 16-byte
+// pieces of the values, 4 (bf16) or 8 (fp32) lanes a block.
 #include "common.h"
 #include "kernels.h"
 
@@ -22,13 +22,13 @@ namespace trg {
 
 namespace {
 
-// Code of x (already divided by the block's scale), ties to the even code:
-// steps of 1/2 below 2, of 1 below 4, of 2 above.  Saturates at 6.
-TRG_DEV uint32_t e2m1_code(float x) {
-  const float a = fminf(fabsf(x), 6.0f);
-  const float lo = rintf(a * 2.0f), mid = rintf(a) + 2.0f, hi = rintf(a * 0.5f) + 4.0f;
-  const float m = a < 2.0f ? lo : (a < 4.0f ? mid : hi);
-  return (uint32_t)m | (__float_as_uint(x) >> 31 << 3);
+// Eight (or four) codes of values divided by the block's scale: gfx950's scaled
+// conversion divides by the scale operand (2^s; a float subnormal for s = -127),
+// rounds to nearest even and saturates at +-6, the format's rule.  The tests put
+// every bf16 pattern and the fp32 values beside every border through it.
+TRG_DEV uint32_t e2m1_codes4(const float* f, float scale, uint32_t old) {
+  uint32_t w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(old, f[0], f[1], scale, 0);
+  return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, f[2], f[3], scale, 1);
 }
 
 // Value of a code without its scale.
@@ -39,101 +39,135 @@ TRG_DEV float e2m1_value(uint32_t c) {
   return __uint_as_float(bits | (c >> 3) << 31);
 }
 
-// 2^n for n in [-126, 127].  The block exponents lie in [-127, 125], so 2^-s is
-// a normal float and the division by 2^s an exact multiplication.
-TRG_DEV float pow2n(int n) { return __uint_as_float((uint32_t)(n + 127) << 23); }
+// Value of a lane's neighbours inside a row of 16 lanes, in the vector registers.
+template <int CTRL>
+TRG_DEV uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, true);
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E;         // within four lanes
+constexpr int kHalfMirror = 0x141;                // lane i of eight <-> 7 - i
+constexpr int kRor4 = 0x124, kRor8 = 0x128;       // rotations of the row
 
-// One thread per 16-byte piece; pieces of a row are padded to whole 128-value
-// chunks so that a chunk is a run of lanes of one wave.
-template <class T>
+// N 16-byte pieces a thread, a workgroup's pieces apart, all loaded before the
+// first is used; pieces of a row are padded to whole 128-value chunks so that a
+// chunk is a run of lanes of one wave.
+template <class T, int N>
 __global__ __launch_bounds__(256) void quantize_e2m1_kernel(const T* __restrict__ in, int rows, int cols,
                                                             uint8_t* __restrict__ q, uint8_t* __restrict__ s) {
   constexpr int V = 16 / (int)sizeof(T);
   constexpr int LB = 32 / V;   // lanes a block
   constexpr int LC = 128 / V;  // lanes a chunk
-  const int nch = (cols + 127) / 128;
-  const long g = (long)blockIdx.x * 256 + threadIdx.x;
-  const long ch = g / LC;  // chunk: row-major over (row, chunk of the row)
-  const int l = (int)(g % LC);
-  const long row = ch / nch;
-  const int c0 = (int)(ch % nch) * 128 + l * V;
-  const bool in_row = row < rows && c0 < cols;  // cols is a multiple of 32: a whole block is in or out
-  float f[V];
-  if (in_row) {
-    unpack16<T>(*(const uint4*)(in + row * cols + c0), f);
-  } else {
+  const uint32_t nch = (uint32_t)(cols + 127) / 128;
+  const int l = (int)(threadIdx.x % LC);
+  uint4 raw[N];
+  uint32_t row[N], chunk[N];
+  bool in_row[N];
 #pragma unroll
-    for (int c = 0; c < V; ++c) f[c] = 0.f;
+  for (int n = 0; n < N; ++n) {
+    // chunks are numbered row-major over (row, chunk of the row); fewer than 2^27
+    const uint32_t ch = (uint32_t)(blockIdx.x * N + n) * (256 / LC) + threadIdx.x / LC;
+    row[n] = ch / nch;
+    chunk[n] = ch - row[n] * nch;
+    const int c0 = (int)chunk[n] * 128 + l * V;
+    in_row[n] = row[n] < (uint32_t)rows && c0 < cols;  // cols is a multiple of 32: a whole block is in or out
+    raw[n] = in_row[n] ? *(const uint4*)(in + (long)row[n] * cols + c0) : make_uint4(0, 0, 0, 0);
   }
-  uint32_t am = 0;  // magnitudes order like their bit patterns, infinity and NaN on top
 #pragma unroll
-  for (int c = 0; c < V; ++c) am = max(am, __float_as_uint(f[c]) & 0x7FFFFFFFu);
+  for (int n = 0; n < N; ++n) {
+    float f[V];
+    unpack16<T>(raw[n], f);
+    uint32_t am = 0;  // magnitudes order like their bit patterns, infinity and NaN on top
 #pragma unroll
-  for (int o = 1; o < LB; o <<= 1) am = max(am, (uint32_t)__shfl_xor((int)am, o, 64));
-  const int ex = (int)(am >> 23);
-  const bool bad = ex == 255;
-  const int se = ex == 0 ? -127 : max(ex - 129, -127);
-  uint32_t code = 0;
-  if (!bad) {
-    const float inv = pow2n(-se);
-#pragma unroll
-    for (int c = 0; c < V; ++c) code |= e2m1_code(f[c] * inv) << (4 * c);
+    for (int c = 0; c < V; ++c) am = max(am, __float_as_uint(f[c]) & 0x7FFFFFFFu);
+    am = max(am, dpp<kXor1>(am));
+    am = max(am, dpp<kXor2>(am));
+    if constexpr (LB == 8) am = max(am, dpp<kHalfMirror>(am));
+    const int ex = (int)(am >> 23);
+    const bool bad = ex == 255;
+    const int sb = max(ex - 2, 0);  // s + 127; a zero or subnormal block gets 0
+    const float scale = __uint_as_float(sb != 0 ? (uint32_t)sb << 23 : 0x00400000u);
+    uint32_t code = e2m1_codes4(f, scale, 0);
+    if constexpr (V == 8) code = (code & 0xFFFFu) | e2m1_codes4(f + 4, scale, 0) << 16;
+    if (bad) code = 0;
+    const int c0 = (int)chunk[n] * 128 + l * V;
+    if (in_row[n]) {
+      uint8_t* o = q + ((long)row[n] * cols + c0) / 2;
+      if constexpr (V == 8) *(uint32_t*)o = code;
+      else *(uint16_t*)o = (uint16_t)code;
+    }
+    // the chunk's four scale bytes as one dword
+    uint32_t sw = in_row[n] ? (uint32_t)(bad ? 255 : sb) << (8 * ((l / LB) & 3)) : 0u;
+    if constexpr (LC == 16) {
+      sw |= dpp<kRor4>(sw);
+      sw |= dpp<kRor8>(sw);
+    } else {
+      sw |= dpp<kRor8>(sw);
+      sw |= (uint32_t)__shfl_xor((int)sw, 16, 64);
+    }
+    if (l == 0 && row[n] < (uint32_t)rows) *(uint32_t*)(s + ((long)chunk[n] * rows + row[n]) * 4) = sw;
   }
-  if (in_row) {
-    uint8_t* o = q + (row * cols + c0) / 2;
-    if constexpr (V == 8) *(uint32_t*)o = code;
-    else *(uint16_t*)o = (uint16_t)code;
-  }
-  uint32_t sb = in_row ? (uint32_t)(bad ? 255 : se + 127) << (8 * ((l / LB) & 3)) : 0u;
-#pragma unroll
-  for (int o = LB; o < LC; o <<= 1) sb |= (uint32_t)__shfl_xor((int)sb, o, 64);
-  if (l == 0 && row < rows) *(uint32_t*)(s + ((ch % nch) * rows + row) * 4) = sb;
 }
 
-template <class T>
+// N 16-byte pieces of the output a thread.
+template <class T, int N>
 __global__ __launch_bounds__(256) void dequantize_e2m1_kernel(const uint8_t* __restrict__ q,
                                                               const uint8_t* __restrict__ s, int rows, int cols,
                                                               T* __restrict__ out) {
   constexpr int V = 16 / (int)sizeof(T);
-  const long g = (long)blockIdx.x * 256 + threadIdx.x;  // 16-byte piece of the output
-  const int ppr = cols / V;
-  const long row = g / ppr;
-  if (row >= rows) return;
-  const int c0 = (int)(g % ppr) * V;
-  const uint8_t* p = q + (row * cols + c0) / 2;
-  const uint32_t code = V == 8 ? *(const uint32_t*)p : *(const uint16_t*)p;
-  const int b = c0 / 32;
-  const int sb = s[((long)(b / 4) * rows + row) * 4 + b % 4];
-  const float sc = sb == 255 ? __uint_as_float(0x7FC00000u)
-                             : (sb == 0 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)sb << 23));
-  float f[V];
+  const uint32_t ppr = (uint32_t)cols / V;
+  uint32_t code[N], sb[N];
+  long at[N];
 #pragma unroll
-  for (int c = 0; c < V; ++c) f[c] = e2m1_value((code >> (4 * c)) & 15u) * sc;
-  *(uint4*)(out + row * cols + c0) = pack16<T>(f);
+  for (int n = 0; n < N; ++n) {
+    const uint32_t g = (uint32_t)(blockIdx.x * N + n) * 256 + threadIdx.x;
+    const uint32_t row = g / ppr, c0 = (g - row * ppr) * V, b = c0 / 32;
+    at[n] = row < (uint32_t)rows ? (long)row * cols + c0 : -1;
+    if (at[n] >= 0) {
+      const uint8_t* p = q + at[n] / 2;
+      code[n] = V == 8 ? *(const uint32_t*)p : *(const uint16_t*)p;
+      sb[n] = s[((long)(b / 4) * rows + row) * 4 + b % 4];
+    }
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) {
+    if (at[n] < 0) continue;
+    const float sc = sb[n] == 255 ? __uint_as_float(0x7FC00000u)
+                                  : (sb[n] == 0 ? __uint_as_float(0x00400000u) : __uint_as_float(sb[n] << 23));
+    float f[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) f[c] = e2m1_value((code[n] >> (4 * c)) & 15u) * sc;
+    *(uint4*)(out + at[n]) = pack16<T>(f);
+  }
+}
+
+// Pieces a thread: four once that still leaves two workgroups a CU.
+template <class F>
+hipError_t with_pieces(long pieces, F&& f) {
+  if (pieces >= 4L * 256 * 512) return f(std::integral_constant<int, 4>{});
+  return f(std::integral_constant<int, 1>{});
 }
 
 }  // namespace
 
 hipError_t launch_quantize_e2m1(const void* in, bool bf16, int rows, int cols, uint8_t* q, uint8_t* s, hipStream_t st) {
-  const long chunks = (long)rows * ((cols + 127) / 128);
-  if (bf16)
-    quantize_e2m1_kernel<uint16_t><<<(unsigned)((chunks * 16 + 255) / 256), 256, 0, st>>>((const uint16_t*)in, rows,
-                                                                                         cols, q, s);
-  else
-    quantize_e2m1_kernel<float><<<(unsigned)((chunks * 32 + 255) / 256), 256, 0, st>>>((const float*)in, rows, cols, q,
-                                                                                      s);
-  return hipGetLastError();
+  const long pieces = (long)rows * ((cols + 127) / 128) * (bf16 ? 16 : 32);
+  return with_pieces(pieces, [&](auto N) {
+    const unsigned grid = (unsigned)((pieces + 256 * N - 1) / (256 * N));
+    if (bf16) quantize_e2m1_kernel<uint16_t, N><<<grid, 256, 0, st>>>((const uint16_t*)in, rows, cols, q, s);
+    else quantize_e2m1_kernel<float, N><<<grid, 256, 0, st>>>((const float*)in, rows, cols, q, s);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_dequantize_e2m1(const uint8_t* q, const uint8_t* s, bool bf16, int rows, int cols, void* out,
                                   hipStream_t st) {
   const long pieces = (long)rows * cols / (bf16 ? 8 : 4);
-  if (bf16)
-    dequantize_e2m1_kernel<uint16_t><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(q, s, rows, cols,
-                                                                                      (uint16_t*)out);
-  else
-    dequantize_e2m1_kernel<float><<<(unsigned)((pieces + 255) / 256), 256, 0, st>>>(q, s, rows, cols, (float*)out);
-  return hipGetLastError();
+  return with_pieces(pieces, [&](auto N) {
+    const unsigned grid = (unsigned)((pieces + 256 * N - 1) / (256 * N));
+    if (bf16) dequantize_e2m1_kernel<uint16_t, N><<<grid, 256, 0, st>>>(q, s, rows, cols, (uint16_t*)out);
+    else dequantize_e2m1_kernel<float, N><<<grid, 256, 0, st>>>(q, s, rows, cols, (float*)out);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace trg

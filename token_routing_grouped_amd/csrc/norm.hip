@@ -248,57 +248,73 @@ __global__ __launch_bounds__(WPR == 16 ? 1024 : 256) void rmsnorm_bwd_kernel(
   }
 }
 
-// dw[c] = sum over the workgroups' partials, in a fixed order: 16 groups of
-// rows, then the 16 group sums.  64 columns x 16 groups a workgroup.
+// dw[c] = sum over the workgroups' partials, in a fixed order: 64 groups of rows,
+// then the 64 group sums.  16 columns (a 64-byte line each) x 64 groups a
+// workgroup, so that 2048 columns are 128 workgroups with 8 loads in flight a
+// thread: 4 us instead of 11 with 64 columns x 16 groups (512 partials).
 template <class T>
 __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restrict__ part, int np, int d,
                                                           T* __restrict__ dw) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, g = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  __shared__ float red[64][17];
+  const int col = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int c = min(blockIdx.x * 16 + col, d - 1);  // d is a multiple of 4: the last workgroup may be short
   float a = 0.f;
-  if (c < d)
-    for (int p = g; p < np; p += 16) a += part[(long)p * d + c];
-  red[g][lane] = a;
+  for (int p0 = g; p0 < np; p0 += 64 * 8) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = part[(long)min(p0 + 64 * i, np - 1) * d + c];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) a += p0 + 64 * i < np ? v[i] : 0.f;
+  }
+  red[g][col] = a;
   __syncthreads();
-  if (g == 0 && c < d) {
+  if (threadIdx.x < 64) {  // lane: column lane % 16, a quarter of the groups each
+    const int q = threadIdx.x >> 4;
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += red[i][lane];
-    Elt<T>::st(dw + c, t);
+    for (int i = 0; i < 16; ++i) t += red[q * 16 + i][col];
+    t += __shfl_xor(t, 16, 64);
+    t += __shfl_xor(t, 32, 64);
+    if (q == 0 && blockIdx.x * 16 + col < d) Elt<T>::st(dw + c, t);
   }
 }
 
-// Rows' shape: waves a row and pieces a lane that hold d elements.
+// Rows' shape: waves a row and pieces a lane that hold d elements.  The backward
+// keeps three inputs, the weight and the gradient's sums of a lane's columns,
+// so more waves beat more pieces (at 16 x 8, the widest rows, it spills).
 struct RowShape {
   int wpr, np;
 };
 RowShape row_shape(int d, int esize) {
   const int pieces = d * esize / 16;  // at most 16 * 64 * 8 (checked by the caller)
-  const int wpr = pieces <= 64 * 4 ? 1 : (pieces <= 256 * 8 ? 4 : 16);
+  const int wpr = pieces <= 64 * 4 ? 1 : (pieces <= 256 * 4 ? 4 : 16);
   const int per = (pieces + wpr * 64 - 1) / (wpr * 64);
   return {wpr, per <= 1 ? 1 : per <= 2 ? 2 : per <= 4 ? 4 : 8};
 }
 
-// Workgroups of the backward's row pass: two a CU when there are rows enough.
+// Workgroups of the backward's row pass: two a CU when there are rows enough that
+// their partial weight gradients (d floats each, out and in) are little next to
+// the rows, else one.
 int bwd_groups(int rows, int rpb) {
-  const int full = (rows + rpb - 1) / rpb;
-  return full < 512 ? (full < 1 ? 1 : full) : 512;
+  const int full = (rows + rpb - 1) / rpb, most = rows >= 4096 ? 512 : 256;
+  return full < most ? (full < 1 ? 1 : full) : most;
 }
 
+// The shapes that row_shape gives.
 template <class F>
 hipError_t with_shape(RowShape r, F&& f) {
-#define TRG_NP(W)                                                       \
-  switch (r.np) {                                                       \
-    case 1: return f(std::integral_constant<int, W>{}, std::integral_constant<int, 1>{}); \
-    case 2: return f(std::integral_constant<int, W>{}, std::integral_constant<int, 2>{}); \
-    case 4: return f(std::integral_constant<int, W>{}, std::integral_constant<int, 4>{}); \
-    default: return f(std::integral_constant<int, W>{}, std::integral_constant<int, 8>{}); \
-  }
-  if (r.wpr == 1) { TRG_NP(1) }
-  if (r.wpr == 4) { TRG_NP(4) }
-  TRG_NP(16)
-#undef TRG_NP
+#define TRG_SHAPE(W, N) \
+  if (r.wpr == W && r.np == N) return f(std::integral_constant<int, W>{}, std::integral_constant<int, N>{})
+  TRG_SHAPE(1, 1);
+  TRG_SHAPE(1, 2);
+  TRG_SHAPE(1, 4);
+  TRG_SHAPE(4, 2);
+  TRG_SHAPE(4, 4);
+  TRG_SHAPE(16, 2);
+  TRG_SHAPE(16, 4);
+  TRG_SHAPE(16, 8);
+#undef TRG_SHAPE
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -343,9 +359,9 @@ hipError_t launch_rmsnorm_bwd(const void* dy, const void* ds, const void* s, con
   });
   if (e != hipSuccess) return e;
   if (bf16)
-    rmsnorm_dw_kernel<uint16_t><<<(d + 63) / 64, 1024, 0, st>>>((const float*)ws, np, d, (uint16_t*)dw);
+    rmsnorm_dw_kernel<uint16_t><<<(d + 15) / 16, 1024, 0, st>>>((const float*)ws, np, d, (uint16_t*)dw);
   else
-    rmsnorm_dw_kernel<float><<<(d + 63) / 64, 1024, 0, st>>>((const float*)ws, np, d, (float*)dw);
+    rmsnorm_dw_kernel<float><<<(d + 15) / 16, 1024, 0, st>>>((const float*)ws, np, d, (float*)dw);
   return hipGetLastError();
 }
 
