@@ -534,7 +534,8 @@ moe_status_t moe_rmsnorm_bwd(const void* dy, const void* ds, const void* s, cons
  * mx_quantize_e2m1: in [rows, cols] (dt MOE_F32 or MOE_BF16) to q and s.
  * mx_dequantize_e2m1: q and s to the values they stand for, in dt (exact in
  *   either, but for values under the type's smallest).
- * cols a multiple of 32; q 16-byte, s 4-byte aligned; rows * cols < 2^34.
+ * cols a multiple of 32; q 16-byte, s 4-byte aligned; rows * ceil(cols/128) <
+ * 2^26.
  */
 moe_status_t mx_quantize_e2m1(const void* in, int dt, int rows, int cols, uint8_t* q, uint8_t* s, void* stream);
 moe_status_t mx_dequantize_e2m1(const uint8_t* q, const uint8_t* s, int dt, int rows, int cols, void* out,
@@ -542,7 +543,8 @@ moe_status_t mx_dequantize_e2m1(const uint8_t* q, const uint8_t* s, int dt, int 
 /*
  * mx_linear_e2m1: y[t,:] = W x[t] for 0 <= T <= 64 tokens and a 4-bit matrix W
  * of n rows and K columns (q, s as mx_quantize_e2m1 writes them for [n,K]);
- * x [T,K], y [T,n] bf16, fp32 accumulation, one rounding.  K a multiple of 32.
+ * x [T,K], y [T,n] bf16, fp32 accumulation, one rounding.  K a multiple of 32,
+ * at most 65536; n * K / 2 < 2^31.
  */
 moe_status_t mx_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
                             void* stream);
@@ -561,7 +563,8 @@ moe_status_t mx_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, i
  *   dt: type of x, wr and y.  wt: type of w1, w3 [E,h,d] and w2 [E,d,h]: dt, or
  *   MOE_E2M1 with dt MOE_BF16: then each is packed as mx_quantize_e2m1 packs
  *   [E*h,d] and [E*d,h], w1s, w3s, w2s are their scales, and d and h must be
- *   multiples of 32.  d, h <= 65536.
+ *   multiples of 32.  d, h <= 65536, an expert's matrix under 2 GiB, and packed
+ *   matrices as large as mx_quantize_e2m1 takes them.
  *   n_live (nullable, 4-byte aligned): how many of the T tokens are there, read
  *   on the device (clamped to [0, T]), so that one captured call serves every
  *   smaller batch.  Rows of y, topk_idx and topk_w from *n_live on are left as

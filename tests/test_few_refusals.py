@@ -77,7 +77,8 @@ def test_e2m1_refusals():
     _says(lib.mx_quantize_e2m1(C, 2, 4, 64, C, C, None), UNSUPPORTED, "dt must be")
     _says(lib.mx_quantize_e2m1(C, 1, -1, 64, C, C, None), INVALID, "rows")
     _says(lib.mx_quantize_e2m1(C, 1, 4, 48, C, C, None), INVALID, "multiple of 32")
-    _says(lib.mx_quantize_e2m1(C, 1, 1 << 27, 32, C, C, None), UNSUPPORTED, "too large")
+    _says(lib.mx_quantize_e2m1(C, 1, 1 << 26, 32, C, C, None), UNSUPPORTED, "too large")
+    _says(lib.mx_dequantize_e2m1(C, C, 0, 1 << 20, 8192, C, None), UNSUPPORTED, "too large")
     _says(lib.mx_quantize_e2m1(C, 1, 4, 64, None, C, None), INVALID, "q is null")
     _says(lib.mx_quantize_e2m1(C, 1, 4, 64, C, None, None), INVALID, "s is null")
     _says(lib.mx_quantize_e2m1(C, 1, 4, 64, ctypes.c_void_p(72), C, None), ALIGN, "q is not")
@@ -90,6 +91,7 @@ def test_e2m1_refusals():
     _says(lib.mx_linear_e2m1(C, C, C, 4, 0, 64, C, None), INVALID, "n must be")
     _says(lib.mx_linear_e2m1(C, C, C, 4, 4, 40, C, None), INVALID, "multiple of 32")
     _says(lib.mx_linear_e2m1(C, C, C, 4, 4, 65568, C, None), UNSUPPORTED, "K must be")
+    _says(lib.mx_linear_e2m1(C, C, C, 4, 65536, 65536, C, None), UNSUPPORTED, "2 GiB")
     _says(lib.mx_linear_e2m1(None, C, C, 4, 4, 64, C, None), INVALID, "x is null")
     assert lib.mx_linear_e2m1(None, C, C, 0, 4, 64, None, None) == 0
 
@@ -121,6 +123,9 @@ def test_few_refusals():
     _says(_few(wt=4, dt=0), UNSUPPORTED, "need dt MOE_BF16")
     _says(_few(wt=4, d=72), INVALID, "% 32")
     _says(_few(wt=4, h=72), INVALID, "% 32")
+    _says(_few(d=65536, h=16384), UNSUPPORTED, "2 GiB")
+    _says(_few(dt=0, wt=0, d=32768, h=16384), UNSUPPORTED, "2 GiB")
+    _says(_few(wt=4, E=1024, d=65536, h=32768), UNSUPPORTED, "too large")
     _says(_few(wt=4), INVALID, "w1s is null")
     _says(_few(wt=4, w1s=64, w3s=66, w2s=64), ALIGN, "w3s is not")
     for n in ("x", "wr", "w1", "w3", "w2", "y"):

@@ -719,8 +719,8 @@ moe_status_t moe_rmsnorm_bwd(const void* dy, const void* ds, const void* s, cons
 static moe_status_t check_e2m1(const char* fn, long rows, long cols, const uint8_t* q, const uint8_t* s) {
   if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: rows must be >= 0", fn);
   if (cols <= 0 || cols % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: cols must be a positive multiple of 32", fn);
-  // one thread per 16 bytes of fp32 values, in whole 128-value chunks
-  if (rows * ((cols + 127) / 128) >= (1L << 27)) return fail(MOE_ERR_UNSUPPORTED, "%s: problem too large", fn);
+  // a launch has fewer than 2^32 threads: 32 a 128-value chunk (fp32)
+  if (rows * ((cols + 127) / 128) >= (1L << 26)) return fail(MOE_ERR_UNSUPPORTED, "%s: problem too large", fn);
   if (rows == 0) return MOE_OK;
   TRY(check_ptrs(fn, {{"q", q}}));
   if (s == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: s is null", fn);
@@ -762,6 +762,7 @@ moe_status_t mx_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, i
   if (n < 1) return fail(MOE_ERR_INVALID_ARG, "%s: n must be >= 1", fn);
   if (K > kFewWidth) return fail(MOE_ERR_UNSUPPORTED, "%s: K must be at most %d", fn, kFewWidth);
   TRY(check_e2m1(fn, n, K, q, s));
+  if ((long)n * K / 2 >= (1L << 31)) return fail(MOE_ERR_UNSUPPORTED, "%s: the matrix must be under 2 GiB", fn);
   if (T == 0) return ok();
   TRY(check_ptrs(fn, {{"x", x}, {"y", y}}));
   TRY(check_device());
@@ -798,6 +799,12 @@ moe_status_t moe_few_fwd(const moe_few_args* a, void* stream) {
     return fail(MOE_ERR_INVALID_ARG, "%s: MOE_E2M1 weights need d %% 32 == 0 and h %% 32 == 0", fn);
   TRY(check_row(fn, "d", a->d, a->dt));
   TRY(check_row(fn, "h", a->h, a->dt));
+  // 32-bit offsets inside an expert's matrix, and inside all scales of one kind
+  if ((long)a->d * a->h * (w4 ? 1 : 2 * esize(a->dt)) / 2 >= (1L << 31))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: an expert's matrix must be under 2 GiB", fn);
+  if (w4 && ((long)a->E * a->h * ((a->d + 127) / 128) >= (1L << 26) ||
+             (long)a->E * a->d * ((a->h + 127) / 128) >= (1L << 26)))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: problem too large", fn);
   if (a->T == 0) return ok();
   TRY(check_ptrs(fn, {{"x", a->x}, {"wr", a->wr}, {"w1", a->w1}, {"w3", a->w3}, {"w2", a->w2}, {"y", a->y}}));
   TRY(check_optional_aligned(fn, {{"topk_idx", a->topk_idx}, {"topk_w", a->topk_w}}));
