@@ -127,7 +127,8 @@ def test_few(T, d, E, k, h, wt):
     c.check(m.forward(c.x), m.topk_idx, m.topk_w)
 
 
-@pytest.mark.parametrize("T,d,E,k,h", [(1, 128, 8, 2, 256), (1, 32, 1, 1, 32), (2, 160, 5, 3, 96), (1, 2048, 8, 4, 1024),
+@pytest.mark.parametrize("T,d,E,k,h", [(1, 128, 8, 2, 256), (1, 32, 1, 1, 32), (2, 160, 5, 3, 96),
+                                       (1, 2048, 8, 4, 1024),
                                        (7, 288, 2, 2, 544), (16, 256, 4, 4, 96), (17, 544, 3, 2, 160),
                                        (16, 128, 384, 8, 64), (33, 1056, 6, 3, 288), (64, 256, 8, 4, 256),
                                        (64, 96, 130, 8, 32), (13, 160, 20, 4, 96), (9, 2080, 16, 3, 64),
@@ -297,6 +298,36 @@ def test_few_faulty_token_and_expert_stay_apart(tokens):
             if hit.all():
                 continue
             assert torch.equal(y[~hit], y0[~hit]) and not torch.isfinite(y[hit]).all(1).any()
+
+
+@pytest.mark.parametrize("wt,d,h", [("bf16", 72, 40), ("f32", 40, 24), ("e2m1", 288, 96)])
+@pytest.mark.parametrize("T", [2, 12, 20, 40])
+def test_few_infinity_in_a_rows_last_values_stays_one(T, wt, d, h):
+    """Rows that end inside a line: an infinite hidden value in the last place
+    times a zero weight elsewhere must not turn into NaN.  x's last value is
+    infinite and the matrices keep every sum a single infinity: W1 and W3 take
+    x's last value with weight 1 into the last hidden value and 0 elsewhere, W2
+    takes that into output 0; the other outputs read finite hidden values."""
+    c = Case(T, d, 4, 1, h, "bf16" if wt == "e2m1" else wt)
+    w1, w2 = torch.zeros(4, h, d), torch.zeros(4, d, h)
+    w1[:, :, 0] = 1.0   # every hidden value from x[0]
+    w2[:, :, 0] = 1.0   # every output from hidden 0
+    x = torch.zeros(T, d)
+    x[:, 0] = 1.0
+    x[T - 1, d - 1] = 3e38  # finite, and infinite once squared by the SwiGLU
+    w1[:, h - 1, d - 1] = 4.0
+    w2[:, :, h - 1] = 0.5
+    wr = torch.zeros(4, d)
+    wr[0, 0] = 1.0
+    put = lambda a: a.to(DEV).to(c.dt)
+    if wt == "e2m1":
+        q1, s1, _ = _pack(w1.numpy().astype(np.float64))
+        q2, s2, _ = _pack(w2.numpy().astype(np.float64))
+        m = _layer()(T, 1, put(wr), q1, q1, q2, w1s=s1, w3s=s1, w2s=s2)
+    else:
+        m = _layer()(T, 1, put(wr), put(w1), put(w1), put(w2))
+    y = m.forward(put(x))
+    assert torch.isfinite(y[:T - 1]).all() and (y[T - 1] == float("inf")).all()
 
 
 def test_few_faulty_logits():

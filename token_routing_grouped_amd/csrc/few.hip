@@ -27,10 +27,17 @@
 // instruction is free next to the weight stream.  fp32 weights use the fp32
 // matrix instruction and h stays fp32.
 //
-// Launches: router logits; routing (one workgroup); up projection with the
-// SwiGLU and gate epilogue; down projection, summing over the experts in its
-// accumulators (a column is a token, whichever experts it chose), so there is
-// no combine step and no partial result.  Every sum has a fixed order.
+// Launches, by the tokens (T) and entries (T k) of the call:
+//   at most 8 tokens, 64 entries   router logits; up projection, which routes in
+//                                  its prologue; down projection, summing over
+//                                  the experts in its accumulators (a column is
+//                                  a token, whichever experts it chose).  With
+//                                  at most 16 experts the up projection computes
+//                                  the logits as well: two launches.
+//   at most 16 tokens, 64 entries  the same, but the down projection writes a
+//                                  row an entry and a join adds a token's rows
+//   more                           logits; routing; up; down; join
+// Every sum has a fixed order.
 #include "common.h"
 #include "kernels.h"
 
@@ -220,8 +227,8 @@ TRG_DEV void w_mask(WStep& o, int c, int q, int rb) {
 }
 
 // The tokens' operand of one step for a lane's column: both pieces, KX 16-byte
-// parts each.  Where the weights are past the row's end this is the row's last
-// piece again, which meets zeros.
+// parts each.  Past the row's end it is the row's last piece again, until
+// x_mask puts zeros there: the weights are zeros too, but 0 * inf is not.
 template <int WT>
 struct XStep {
   uint4 v[2][Piece<WT>::kX];
@@ -229,7 +236,8 @@ struct XStep {
 // Piece i of the operand; xb: a uniform base, xo: the lane's column's row.
 template <int WT>
 TRG_DEV void x_piece(const char* xb, uint32_t xo, int c, int q, int i, int rb, uint4* x) {
-  const char* p = xb + (xo + (uint32_t)(min(c * 128 + q * 32 + 16 * i, rb - 16) / 16 * (Piece<WT>::kK * Piece<WT>::kXE)));
+  const int at = min(c * 128 + q * 32 + 16 * i, rb - 16) / 16 * (Piece<WT>::kK * Piece<WT>::kXE);
+  const char* p = xb + (xo + (uint32_t)at);
 #pragma unroll
   for (int j = 0; j < Piece<WT>::kX; ++j) x[j] = *(const uint4*)(p + j * 16);
 }
@@ -237,6 +245,13 @@ template <int WT>
 TRG_DEV void x_load(const char* xb, uint32_t xo, int c, int q, int rb, XStep<WT>& o) {
   x_piece<WT>(xb, xo, c, q, 0, rb, o.v[0]);
   x_piece<WT>(xb, xo, c, q, 1, rb, o.v[1]);
+}
+template <int WT>
+TRG_DEV void x_mask(uint4* x, int c, int q, int i, int rb) {
+  const bool in = c * 128 + q * 32 + 16 * i < rb;
+#pragma unroll
+  for (int j = 0; j < Piece<WT>::kX; ++j)
+    x[j] = make_uint4(in ? x[j].x : 0, in ? x[j].y : 0, in ? x[j].z : 0, in ? x[j].w : 0);
 }
 template <int WT>
 TRG_DEV f32x4_t mma_step(const WStep& w, const XStep<WT>& x, f32x4_t acc) {
@@ -256,8 +271,13 @@ TRG_DEV f32x4_t mma_step(const WStep& w, const XStep<WT>& x, f32x4_t acc) {
 // part of the operand a line at a time, with two (the hidden vector's halves)
 // a piece of it, 256 bytes a token and part.  Place s of token n is stored at s
 // ^ n, so that the 16 tokens' reads of one place fall into different banks.  No
-// barrier: the buffer is one wave's, and its LDS instructions run in order.
+// workgroup barrier: the buffer is one wave's, and its LDS instructions run in
+// order (wave_order keeps the compiler to it).
 constexpr int kStage = 8192;
+TRG_DEV void wave_order() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
 
 // In two steps, so that the weights' loads can go out in between.  xo: lane r's
 // row offset of column r, which repeats the last column where there is none;
@@ -343,13 +363,21 @@ TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const 
           uint4 x[XB][P][KX];
           if (n + b > 0) stage_load<P, XN>(st, xb, xpart, xo[n], c0, b, rb * 4);
           stage_store<P, XN>(st, xl);
+          wave_order();
 #pragma unroll
           for (int i = 0; i < XB; ++i)
 #pragma unroll
             for (int p = 0; p < P; ++p) staged_x<P>(xl, r, q, b + i, p, x[i][p]);
-          if (n + b == 0 && !whole) {  // the first use of the weights: their loads are waited for here
+          wave_order();
+          if (!whole) {
+            if (n + b == 0) {  // the first use of the weights: their loads are waited for here
 #pragma unroll
-            for (int m = 0; m < NM; ++m) w_mask<WT>(w[0][m], line[0], q, rb);
+              for (int m = 0; m < NM; ++m) w_mask<WT>(w[0][m], line[0], q, rb);
+            }
+#pragma unroll
+            for (int i = 0; i < XB; ++i)
+#pragma unroll
+              for (int p = 0; p < P; ++p) x_mask<WT>(x[i][p], line[0], q, b + i, rb);
           }
 #pragma unroll
           for (int i = 0; i < XB; ++i) {
@@ -372,13 +400,22 @@ TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const 
 #pragma unroll
             for (int i = 0; i < 2 * U; ++i)
 #pragma unroll
-              for (int p = 0; p < P; ++p) x_piece<WT>(xb + p * xpart, xo[n0 + n], line[i / 2], q, i & 1, rb, &x[n][i][p]);
+              for (int p = 0; p < P; ++p)
+                x_piece<WT>(xb + p * xpart, xo[n0 + n], line[i / 2], q, i & 1, rb, &x[n][i][p]);
         }
-        if (n0 == 0 && !whole) {
+        if (!whole) {
+          if (n0 == 0) {
 #pragma unroll
-          for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int m = 0; m < NM; ++m) w_mask<WT>(w[u][m], line[u], q, rb);
+              for (int m = 0; m < NM; ++m) w_mask<WT>(w[u][m], line[u], q, rb);
+          }
+#pragma unroll
+          for (int n = 0; n < NB_X; ++n)
+#pragma unroll
+            for (int i = 0; i < 2 * U; ++i)
+#pragma unroll
+              for (int p = 0; p < P; ++p) x_mask<WT>(&x[n][i][p], line[i / 2], q, i & 1, rb);
         }
 #pragma unroll
         for (int n = 0; n < NB_X; ++n)
@@ -413,12 +450,9 @@ TRG_DEV int live_tokens(const int* n_live, int T) { return n_live != nullptr ? m
 // tiles of 16 rows, its waves share the lines; blockIdx.y takes the part_lines
 // lines from blockIdx.y * part_lines and writes its own [T, n] of out.
 template <int WT, int NM, int NT, int U, int XN, int WAVES, class OUT>
-__global__ __launch_bounds__(WAVES * 64, NT > 1 && NM* NT > 3 ? 2 : 4) void few_linear_kernel(const char* __restrict__ x,
-                                                                 const void* __restrict__ w,
-                                                                 const uint8_t* __restrict__ ws, int T, int n, int rb,
-                                                                 int xb, int part_lines,
-                                                                 const int* __restrict__ n_live,
-                                                                 OUT* __restrict__ out) {
+__global__ __launch_bounds__(WAVES * 64, NT > 1 && NM* NT > 3 ? 2 : 4) void few_linear_kernel(
+    const char* __restrict__ x, const void* __restrict__ w, const uint8_t* __restrict__ ws, int T, int n, int rb,
+    int xb, int part_lines, const int* __restrict__ n_live, OUT* __restrict__ out) {
   // the waves' staging buffers, then (1 KB a wave) their accumulators
   __shared__ __attribute__((aligned(16))) char lds[WAVES * (WT == kE2M1 ? kStage : 1024)];
   float* red = (float*)lds;
@@ -563,11 +597,10 @@ constexpr int kRouteChunk = 8192;  // logits in LDS at a time
 // LDS, a wave routes a token at a time from there; then the chosen experts'
 // token masks are compacted, in expert order, into slots.
 template <int EPL>
-__global__ __launch_bounds__(1024) void few_route_kernel(const float* __restrict__ logits, int parts, int T, int E, int k,
-                                                         const int* __restrict__ n_live, int* __restrict__ idx_out,
-                                                         float* __restrict__ w_out, int* __restrict__ n_active,
-                                                         FewSlot* __restrict__ slots, float* __restrict__ gate,
-                                                         int* __restrict__ pos_out) {
+__global__ __launch_bounds__(1024) void few_route_kernel(
+    const float* __restrict__ logits, int parts, int T, int E, int k, const int* __restrict__ n_live,
+    int* __restrict__ idx_out, float* __restrict__ w_out, int* __restrict__ n_active, FewSlot* __restrict__ slots,
+    float* __restrict__ gate, int* __restrict__ pos_out) {
   __shared__ unsigned long long mask[1024];
   __shared__ float chunk[kRouteChunk];
   __shared__ int first[1024];
@@ -675,7 +708,8 @@ TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb
           } else {
             const uint16_t hi = f2bf(v);
             ((uint16_t*)hid)[at] = hi;
-            ((uint16_t*)hid)[hid_n + at] = f2bf(v - bf2f(hi));
+            const float lo = v - bf2f(hi);  // not a number where v is infinite: then hi says it all
+            ((uint16_t*)hid)[hid_n + at] = fabsf(bf2f(hi)) < INFINITY ? f2bf(lo) : (uint16_t)0;
           }
         }
       }
@@ -857,13 +891,20 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
   auto multiply = [&](Items& o) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      w_mask<WT>(o.w[u], o.c[u] + kr, q, rb);
       const bool on = (o.mask[u] >> ct) & 1;
       const uint32_t xo = (uint32_t)(o.off[u] + __popcll(o.mask[u] & ((1ull << ct) - 1))) * (uint32_t)(h * XE);
       XStep<WT> x[P];
       if (on) {
 #pragma unroll
         for (int p = 0; p < P; ++p) x_load<WT>(hid + p * hid_n * XE, xo, o.c[u] + kc, q, rb, x[p]);
+      }
+      if ((o.c[u] + KS) * 128 > rb) {  // the same for the whole wave
+        w_mask<WT>(o.w[u], o.c[u] + kr, q, rb);
+#pragma unroll
+        for (int p = 0; p < P; ++p) {
+          x_mask<WT>(x[p].v[0], o.c[u] + kc, q, 0, rb);
+          x_mask<WT>(x[p].v[1], o.c[u] + kc, q, 1, rb);
+        }
       }
       f32x4_t t = {0, 0, 0, 0};
 #pragma unroll
@@ -1013,8 +1054,9 @@ template <int WT, int NM, int NT, int U, int XN, int WAVES, class OUT>
 hipError_t linear_nt(const void* x, const void* w, const uint8_t* ws, int T, int n, int rb, int xb, int parts,
                      const int* n_live, OUT* out, hipStream_t st) {
   const int lines = (rb + 127) / 128, pl = (lines + parts - 1) / parts;
-  few_linear_kernel<WT, NM, NT, U, XN, WAVES, OUT><<<dim3((n + 16 * NM - 1) / (16 * NM), parts), WAVES * 64, 0, st>>>(
-      (const char*)x, w, ws, T, n, rb, xb, pl, n_live, out);
+  few_linear_kernel<WT, NM, NT, U, XN, WAVES, OUT>
+      <<<dim3((n + 16 * NM - 1) / (16 * NM), parts), WAVES * 64, 0, st>>>((const char*)x, w, ws, T, n, rb, xb, pl,
+                                                                          n_live, out);
   return hipGetLastError();
 }
 
@@ -1070,8 +1112,8 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   }
   if (!pro) {
 #define TRG_ROUTE(N)                                                                                                  \
-  few_route_kernel<N><<<1, 1024, 0, st>>>(logits, parts, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, n_active, slots, \
-                                          gate, pos)
+  few_route_kernel<N><<<1, 1024, 0, st>>>(logits, parts, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, n_active, \
+                                          slots, gate, pos)
     if (a.E <= 64) TRG_ROUTE(1);
     else if (a.E <= 128) TRG_ROUTE(2);
     else if (a.E <= 512) TRG_ROUTE(8);
@@ -1086,12 +1128,11 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   constexpr int UR = WT == kE2M1 ? 1 : 2;                             // row tiles a wave
   const long up_tiles = (long)slots_max * ((a.h + 15) / 16), down_tiles = (long)slots_max * ((a.d + 15) / 16);
   const int uw = pro ? kWaves : row_waves(rb1, up_tiles), dw = row_waves(rb2, down_tiles);
-#define TRG_UP(RM, U, EPL, PRO, ROUTER)                                                                                       \
-  few_up_kernel<WT, RM, U, EPL, PRO, ROUTER><<<(unsigned)slots_max * ((a.h + 16 * RM - 1) / (16 * RM)),                       \
-                                       uw * 64, lds_bytes<WT>(uw, 2), st>>>(                                          \
-                                             (const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.wr, a.T, a.E, a.k, a.h, rb1, \
-                                             logits, parts, a.n_live, a.topk_idx, a.topk_w, n_active, slots, gate, \
-                                             tokens_down(a.T, pro) ? nullptr : pos, hid, hid_n)
+#define TRG_UP(RM, U, EPL, PRO, ROUTER)                                                                             \
+  few_up_kernel<WT, RM, U, EPL, PRO, ROUTER>                                                                       \
+      <<<(unsigned)slots_max * ((a.h + 16 * RM - 1) / (16 * RM)), uw * 64, lds_bytes<WT>(uw, 2), st>>>(            \
+          (const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.wr, a.T, a.E, a.k, a.h, rb1, logits, parts, a.n_live,  \
+          a.topk_idx, a.topk_w, n_active, slots, gate, tokens_down(a.T, pro) ? nullptr : pos, hid, hid_n)
   if (!pro && (UR == 1 || up_tiles < 1024)) TRG_UP(1, U, 1, false, false);  // two a wave would leave CUs idle
   else if (!pro) TRG_UP(UR, U, 1, false, false);
   else if (router) TRG_UP(1, UP, 1, true, true);
