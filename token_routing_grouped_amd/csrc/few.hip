@@ -191,6 +191,18 @@ TRG_DEV WRow w_row(const WBase& b, int row, int rb) {
   return {(uint32_t)row * (uint32_t)rb, WT == kE2M1 ? (b.first + (uint32_t)row) * 4u : 0u};
 }
 
+// Row tile of the t-th of `tiles` workgroups (a permutation).  A cache line of
+// 4-bit rows' scales is 32 rows' of one chunk, G tiles'; workgroups go round the
+// 8 dies, so with tiles in order G of them would each fetch it.  So G
+// neighbouring tiles go to one die.  61 tokens, 128 experts, up projection: 50.2
+// -> 47.0 us.
+template <int WT, int G>
+TRG_DEV int near_tile(int t, int tiles) {
+  if constexpr (WT != kE2M1 || G <= 1) return t;
+  const int o = t % (8 * G), b = t - o;
+  return b + 8 * G <= tiles ? b + o % 8 * G + o / 8 : t;
+}
+
 // One step's share of a weight row: two 16-byte pieces and their scale bytes.
 struct WStep {
   uint4 v[2];
@@ -267,12 +279,13 @@ TRG_DEV f32x4_t mma_step(const WStep& w, const XStep<WT>& x, f32x4_t acc) {
 // eight times the same ones, and the address unit, not HBM, sets the pace (13
 // tokens, 24576 x 6144: 24.3 us, of which 15.6 are left without these loads;
 // staged 16.4).  So a wave copies them to its own kStage bytes of LDS, whole
-// cache lines an instruction, and its lanes read their pieces there: with one
-// part of the operand a line at a time, with two (the hidden vector's halves)
-// a piece of it, 256 bytes a token and part.  Place s of token n is stored at s
-// ^ n, so that the 16 tokens' reads of one place fall into different banks.  No
-// workgroup barrier: the buffer is one wave's, and its LDS instructions run in
-// order (wave_order keeps the compiler to it).
+// cache lines an instruction, and its lanes read their pieces there: XB = 2
+// pieces at a time (a line: 512 bytes of a token), or, where registers are short,
+// one (256 bytes a token, and room for both parts of the hidden vector).  A dense
+// product with one piece at a time: 19.0 instead of 16.7 us.  Place s of token n
+// is stored at s ^ n, so that the 16 tokens' reads of one place fall into
+// different banks.  No workgroup barrier: the buffer is one wave's, and its LDS
+// instructions run in order (wave_order keeps the compiler to it).
 constexpr int kStage = 8192;
 TRG_DEV void wave_order() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -282,18 +295,23 @@ TRG_DEV void wave_order() {
 // In two steps, so that the weights' loads can go out in between.  xo: lane r's
 // row offset of column r, which repeats the last column where there is none;
 // the first XN * (tokens an instruction) columns are copied.
-template <int P, int XN>
+template <int P, int XN, int XB>
 struct Stage {
-  static constexpr int LT = P == 1 ? 32 : 16;  // lanes (16-byte places) a token
+  static constexpr int LT = 16 * XB;           // lanes (16-byte places) a token
   static constexpr int TI = 64 / LT;           // tokens an instruction
   uint4 g[XN][P];
 };
-template <int P, int XN>
-TRG_DEV void stage_load(Stage<P, XN>& o, const char* xb, long xpart, uint32_t xo, int line, int piece, int row_bytes) {
-  constexpr int LT = Stage<P, XN>::LT, TI = Stage<P, XN>::TI;
+// Where in a token's row place s of a copy is.
+template <int XB>
+TRG_DEV int stage_at(int s, int line, int piece) {
+  return line * 512 + (XB == 2 ? s * 16 : (s >> 2) * 128 + piece * 64 + (s & 3) * 16);
+}
+template <int P, int XN, int XB>
+TRG_DEV void stage_load(Stage<P, XN, XB>& o, const char* xb, long xpart, uint32_t xo, int line, int piece,
+                        int row_bytes) {
+  constexpr int LT = Stage<P, XN, XB>::LT, TI = Stage<P, XN, XB>::TI;
   const int lane = threadIdx.x & 63, s = lane % LT;
-  const int in_line = P == 1 ? s * 16 : (s >> 2) * 128 + piece * 64 + (s & 3) * 16;
-  const uint32_t off = (uint32_t)min(line * 512 + in_line, row_bytes - 16);
+  const uint32_t off = (uint32_t)min(stage_at<XB>(s, line, piece), row_bytes - 16);
 #pragma unroll
   for (int t = 0; t < XN; ++t) {
     const uint32_t at = (uint32_t)__builtin_amdgcn_ds_bpermute((t * TI + lane / LT) * 4, (int)xo) + off;
@@ -301,9 +319,21 @@ TRG_DEV void stage_load(Stage<P, XN>& o, const char* xb, long xpart, uint32_t xo
     for (int p = 0; p < P; ++p) o.g[t][p] = *(const uint4*)(xb + p * xpart + at);
   }
 }
-template <int P, int XN>
-TRG_DEV void stage_store(const Stage<P, XN>& o, char* xl) {
-  constexpr int LT = Stage<P, XN>::LT, TI = Stage<P, XN>::TI;
+// Zeros past the row's end, where the row's last place was loaded again.
+template <int P, int XN, int XB>
+TRG_DEV void stage_mask(Stage<P, XN, XB>& o, int line, int piece, int row_bytes) {
+  const bool in = stage_at<XB>((threadIdx.x & 63) % Stage<P, XN, XB>::LT, line, piece) < row_bytes;
+#pragma unroll
+  for (int t = 0; t < XN; ++t)
+#pragma unroll
+    for (int p = 0; p < P; ++p) {
+      uint4& g = o.g[t][p];
+      g = make_uint4(in ? g.x : 0, in ? g.y : 0, in ? g.z : 0, in ? g.w : 0);
+    }
+}
+template <int P, int XN, int XB>
+TRG_DEV void stage_store(const Stage<P, XN, XB>& o, char* xl) {
+  constexpr int LT = Stage<P, XN, XB>::LT, TI = Stage<P, XN, XB>::TI;
   const int lane = threadIdx.x & 63, s = lane % LT;
 #pragma unroll
   for (int t = 0; t < XN; ++t) {
@@ -313,12 +343,12 @@ TRG_DEV void stage_store(const Stage<P, XN>& o, char* xl) {
   }
 }
 // Lane's four 16-byte parts of piece `piece` of part p.
-template <int P>
+template <int XB>
 TRG_DEV void staged_x(const char* xl, int r, int q, int piece, int p, uint4* x) {
-  constexpr int LT = P == 1 ? 32 : 16;
+  constexpr int LT = 16 * XB;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int s = P == 1 ? q * 8 + piece * 4 + j : q * 4 + j;
+    const int s = XB == 2 ? q * 8 + piece * 4 + j : q * 4 + j;
     x[j] = *(const uint4*)(xl + p * (kStage / 2) + r * (LT * 16) + (s ^ r) * 16);
   }
 }
@@ -333,62 +363,76 @@ TRG_DEV void staged_x(const char* xl, int r, int q, int piece, int p, uint4* x) 
 // Only the lanes of those columns load the operand (a few tokens are a few
 // lanes); the others' registers hold anything: columns do not mix, and theirs
 // are not stored.  xl: the wave's staging buffer, XN the copying instructions
-// (4-bit weights; cols and more columns fit).
-template <int WT, int NB, int NM, int NT, int U, int P, int XN>
+// (4-bit weights; cols and more columns fit).  PEEL: a body without masks for the
+// lines before a row's end (4-bit weights).  A dense product gains by it (24576 x
+// 6144, one / 13 / 64 tokens 16.4 / 17.4 / 39.9 -> 14.9 / 16.7 / 38.4 us); the
+// experts' short rows lose (61 tokens, 128 experts 95.6 -> 101.8).
+// One line of 4-bit rows; MASK: the row may end inside it.
+template <bool MASK, int NB, int NM, int NT, int P, int XN, int XB>
+TRG_DEV void line_e2m1(const WBase* wb, const WRow* wr, const char* xb, const uint32_t* xo, long xpart, int rb, int c,
+                       int r, int q, f32x4_t (*acc)[NT], char* xl) {
+  const bool tail = MASK && (c + 1) * 128 > rb;
+  WStep w[NM];
+  // the first copy's loads go out before the weights', so that it is in LDS when
+  // they arrive
+  Stage<P, XN, XB> st;
+  stage_load(st, xb, xpart, xo[0], c, 0, rb * 4);
+#pragma unroll
+  for (int m = 0; m < NM; ++m) w[m] = w_load<kE2M1>(wb[m % NB], wr[m], c, q, rb);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int b = 0; b < 2; b += XB) {
+      uint4 x[XB][P][4];
+      if (n + b > 0) stage_load(st, xb, xpart, xo[n], c, b, rb * 4);
+      if (tail) stage_mask(st, c, b, rb * 4);
+      stage_store(st, xl);
+      wave_order();
+#pragma unroll
+      for (int i = 0; i < XB; ++i)
+#pragma unroll
+        for (int p = 0; p < P; ++p) staged_x<XB>(xl, r, q, b + i, p, x[i][p]);
+      wave_order();
+      // the codes are waited for only here, after the copy: one token 15.8 -> 14.9
+      // us, 32 tokens 26.4 -> 25.1 (24576 x 6144)
+      __builtin_amdgcn_sched_barrier(0);
+      if (tail && n + b == 0) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m) w_mask<kE2M1>(w[m], c, q, rb);
+      }
+#pragma unroll
+      for (int i = 0; i < XB; ++i) {
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+          acc[m][n] = mma_parts<kE2M1, P>(w[m].v[b + i], e8m0((w[m].sb >> (8 * (b + i))) & 255u), x[i][0], x[i][P - 1],
+                                          acc[m][n]);
+        __builtin_amdgcn_sched_barrier(0);  // a piece's codes are decoded when it is used, not ahead
+      }
+    }
+}
+
+template <int WT, int NB, int NM, int NT, int U, int P, int XN, int XB = 2, bool PEEL = false>
 TRG_DEV void stream_tile(const WBase* wb, const WRow* wr, const char* xb, const uint32_t* xo, long xpart, int cols,
                          int rb, int c0, int c1, int step, int r, int q, f32x4_t (*acc)[NT], char* xl) {
-  constexpr int KX = Piece<WT>::kX;
-  static_assert(WT != kE2M1 || U == 1, "a staging buffer holds one line");
-  const int past = (rb + 127) >> 7;  // a line that is past every row's end
-  for (; c0 < c1; c0 += step * U) {
-    WStep w[U][NM];
-    int line[U];
-    // the first copy's loads go out before the weights', so that it is in LDS
-    // when they arrive
-    Stage<P, XN> st;
-    if constexpr (WT == kE2M1) stage_load<P, XN>(st, xb, xpart, xo[0], c0, 0, rb * 4);
+  if constexpr (WT == kE2M1) {
+    static_assert(U == 1, "a staging buffer holds one line");
+    if constexpr (PEEL)
+      for (; c0 < min(c1, rb >> 7); c0 += step)
+        line_e2m1<false, NB, NM, NT, P, XN, XB>(wb, wr, xb, xo, xpart, rb, c0, r, q, acc, xl);
+    for (; c0 < c1; c0 += step)
+      line_e2m1<true, NB, NM, NT, P, XN, XB>(wb, wr, xb, xo, xpart, rb, c0, r, q, acc, xl);
+  } else {
+    const int past = (rb + 127) >> 7;  // a line that is past every row's end
+    for (; c0 < c1; c0 += step * U) {
+      WStep w[U][NM];
+      int line[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      line[u] = c0 + u * step < c1 ? c0 + u * step : past;
+      for (int u = 0; u < U; ++u) {
+        line[u] = c0 + u * step < c1 ? c0 + u * step : past;
 #pragma unroll
-      for (int m = 0; m < NM; ++m) w[u][m] = w_load<WT>(wb[m % NB], wr[m], line[u], q, rb);
-    }
-    const bool whole = (line[U - 1] + 1) * 128 <= rb;  // lines rise, so all of them are
-    if constexpr (WT == kE2M1) {
-      constexpr int XB = P == 1 ? 2 : 1;  // pieces staged at once
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int b = 0; b < 2; b += XB) {
-          uint4 x[XB][P][KX];
-          if (n + b > 0) stage_load<P, XN>(st, xb, xpart, xo[n], c0, b, rb * 4);
-          stage_store<P, XN>(st, xl);
-          wave_order();
-#pragma unroll
-          for (int i = 0; i < XB; ++i)
-#pragma unroll
-            for (int p = 0; p < P; ++p) staged_x<P>(xl, r, q, b + i, p, x[i][p]);
-          wave_order();
-          if (!whole) {
-            if (n + b == 0) {  // the first use of the weights: their loads are waited for here
-#pragma unroll
-              for (int m = 0; m < NM; ++m) w_mask<WT>(w[0][m], line[0], q, rb);
-            }
-#pragma unroll
-            for (int i = 0; i < XB; ++i)
-#pragma unroll
-              for (int p = 0; p < P; ++p) x_mask<WT>(x[i][p], line[0], q, b + i, rb);
-          }
-#pragma unroll
-          for (int i = 0; i < XB; ++i) {
-#pragma unroll
-            for (int m = 0; m < NM; ++m)
-              acc[m][n] = mma_parts<WT, P>(w[0][m].v[b + i], e8m0((w[0][m].sb >> (8 * (b + i))) & 255u), x[i][0],
-                                           x[i][P - 1], acc[m][n]);
-            __builtin_amdgcn_sched_barrier(0);  // a piece's codes are decoded when it is used, not ahead
-          }
-        }
-    } else {
+        for (int m = 0; m < NM; ++m) w[u][m] = w_load<WT>(wb[m % NB], wr[m], line[u], q, rb);
+      }
+      const bool whole = (line[U - 1] + 1) * 128 <= rb;  // lines rise, so all of them are
       // the operand of all columns at once: one trip to the caches a batch
       constexpr int NB_X = NT * 2 * U * P <= 16 ? NT : 1;  // column tiles in registers: at most 64 of them
 #pragma unroll
@@ -472,7 +516,8 @@ __global__ __launch_bounds__(WAVES * 64, NT > 1 && NM* NT > 3 ? 2 : 4) void few_
   for (int m = 0; m < NM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0, 0, 0, 0};
-  stream_tile<WT, 1, NM, NT, U, 1, XN>(wb, wr, x, xo, 0, live, rb, c0 + wv, c1, WAVES, r, q, acc, lds + wv * kStage);
+  stream_tile<WT, 1, NM, NT, U, 1, XN, 2, true>(wb, wr, x, xo, 0, live, rb, c0 + wv, c1, WAVES, r, q, acc,
+                                                lds + wv * kStage);
 #pragma unroll
   for (int m = 0; m < NM; ++m)
 #pragma unroll
@@ -737,7 +782,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
   extern __shared__ __attribute__((aligned(16))) char lds[];  // lds_bytes<WT>(waves, 2)
   const int lane = threadIdx.x & 63, wv = wave_id();
   const int tiles = (h + 16 * RM - 1) / (16 * RM);
-  const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
+  const int slot = blockIdx.x / tiles, tile = near_tile<WT, 2 / RM>(blockIdx.x - slot * tiles, tiles);
   const int row0 = tile * 16 * RM;
   FewSlot sl;
   const float* gt;
@@ -856,7 +901,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
   const int lane = threadIdx.x & 63, wv = wave_id(), r = lane & 15, q = lane >> 4;
   const int live = live_tokens(n_live, T);
   const int na = *n_active;
-  const int row0 = blockIdx.x * RT;
+  const int row0 = near_tile<WT, 32 / RT>(blockIdx.x, gridDim.x) * RT;
   const int row = min(row0 + r % RT, d - 1), kr = r / RT;  // this lane's weight row and line group
   const int ct = r % CT, kc = r / CT;                      // this lane's column: token and line group
   const int nall = (rb + 127) >> 7, nit = (nall + KS - 1) / KS;
@@ -944,25 +989,35 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
 // join adds each token's k rows in order.  Those rows are R d floats, out and
 // in: 3 % of the weights' bytes with two tokens an expert at h = 1024 and 4
 // bits, 0.25 % in bf16 at h = 2048.
-template <int WT, int RM, int NT, int U, int XN>
+// H > 0 (at most H <= 8 tokens, h in halves): columns 0..H-1 are the tokens' hi
+// halves and H..2H-1 their lo halves, added at the end: half the matrix
+// instructions and operand reads of two passes over the columns.  4-bit weights,
+// 61 tokens, 128 experts: 32.0 -> 29.9 us; bf16, whose reads set the pace, no
+// different, so it keeps the one form.
+template <int WT, int RM, int NT, int U, int XN, int H>
 TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb, int rb, int cnt, int col0, int row0,
                        int d, int h, long pos0, int wk, int kw, char* lds, float* __restrict__ yp) {
   float* red = (float*)lds;
-  constexpr int P = WT == kF32 ? 1 : 2, XE = Piece<WT>::kXE;
+  constexpr int P = WT == kF32 || H > 0 ? 1 : 2, XE = Piece<WT>::kXE;
+  constexpr int CT = H > 0 ? H : 16;  // tokens a column tile
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   WRow wr[RM];
 #pragma unroll
   for (int m = 0; m < RM; ++m) wr[m] = w_row<WT>(wb[0], min(row0 + m * 16 + r, d - 1), rb);
   uint32_t xo[NT];
 #pragma unroll
-  for (int i = 0; i < NT; ++i) xo[i] = (uint32_t)(pos0 + min(col0 + i * 16 + r, cnt - 1)) * (uint32_t)(h * XE);
+  for (int i = 0; i < NT; ++i) {
+    const int c = col0 + i * CT + r % CT;
+    xo[i] = (uint32_t)(pos0 + min(c, cnt - 1)) * (uint32_t)(h * XE);
+    if (r >= CT) xo[i] += (uint32_t)hid_n * XE;
+  }
   f32x4_t acc[RM][NT];
 #pragma unroll
   for (int m = 0; m < RM; ++m)
 #pragma unroll
     for (int i = 0; i < NT; ++i) acc[m][i] = f32x4_t{0, 0, 0, 0};
-  stream_tile<WT, 1, RM, NT, U, P, XN>(wb, wr, hid, xo, hid_n * XE, cnt - col0, rb, kw, (rb + 127) >> 7, wk, r, q, acc,
-                                   lds + kw * kStage);
+  stream_tile<WT, 1, RM, NT, U, P, XN, 1>(wb, wr, hid, xo, hid_n * XE, H > 0 ? 2 * H : cnt - col0, rb, kw,
+                                       (rb + 127) >> 7, wk, r, q, acc, lds + kw * kStage);
 #pragma unroll
   for (int m = 0; m < RM; ++m)
 #pragma unroll
@@ -971,8 +1026,12 @@ TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb
       put_tile(red + kw * 256, lane, acc[m][i]);
       __syncthreads();
       for (int o = threadIdx.x; o < 256; o += wk * 64) {
-        const int lr = o & 15, col = o >> 4, c = col0 + i * 16 + col, row = row0 + m * 16 + lr;
-        if (c < cnt && row < d) yp[(pos0 + c) * d + row] = sum_tile(red, wk, lr, col);
+        const int lr = o & 15, col = o >> 4, c = col0 + i * CT + col, row = row0 + m * 16 + lr;
+        if (col < CT && c < cnt && row < d) {
+          float v = sum_tile(red, wk, lr, col);
+          if constexpr (H > 0) v += sum_tile(red, wk, lr, col + H);
+          yp[(pos0 + c) * d + row] = v;
+        }
       }
     }
 }
@@ -994,24 +1053,25 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_rows_kernel(const char* 
   if (slot >= na) return;
   const int cnt = __popcll(sl.mask);
   const WBase wb[1] = {w_base<WT>(w2, w2s, sl.e, E, d, rb)};
-#define TRG_TILE(RM, NT, U, XN, ROW0) \
-  down_tile<WT, RM, NT, U, XN>(hid, hid_n, wb, rb, cnt, c0, ROW0, d, h, sl.off, wk, wv, lds, yp)
+#define TRG_TILE(RM, NT, U, XN, H, ROW0) \
+  down_tile<WT, RM, NT, U, XN, H>(hid, hid_n, wb, rb, cnt, c0, ROW0, d, h, sl.off, wk, wv, lds, yp)
   int c0 = 0;
   if constexpr (WT == kE2M1) {
-    if (cnt <= 4) TRG_TILE(RM, 1, U, 1, row0);
+    if (cnt <= 2) TRG_TILE(RM, 1, U, 1, 2, row0);
+    else if (cnt <= 8) TRG_TILE(RM, 1, U, 4, 8, row0);
     else
       for (; c0 < cnt; c0 += 16) {
         if (c0 > 0) __syncthreads();
-        TRG_TILE(RM, 1, U, 4, row0);
+        TRG_TILE(RM, 1, U, 4, 0, row0);
       }
   } else if (cnt <= 16) {
-    TRG_TILE(RM, 1, U, 1, row0);
+    TRG_TILE(RM, 1, U, 1, 0, row0);
   } else {
     constexpr int RN = RM > 2 ? 2 : RM;
     for (int m = 0; m < RM; m += RN) {
       if (m > 0) __syncthreads();
-      if (cnt <= 32) TRG_TILE(RN, 2, 1, 1, row0 + 16 * m);
-      else TRG_TILE(RN, 4, 1, 1, row0 + 16 * m);
+      if (cnt <= 32) TRG_TILE(RN, 2, 1, 1, 0, row0 + 16 * m);
+      else TRG_TILE(RN, 4, 1, 1, 0, row0 + 16 * m);
     }
   }
 #undef TRG_TILE
