@@ -27,7 +27,8 @@
 // instruction is free next to the weight stream.  fp32 weights use the fp32
 // matrix instruction and h stays fp32.
 //
-// Launches, by the tokens (T) and entries (T k) of the call:
+// Launches, by the tokens (T) and entries (T k: a token's place among its k) of the
+// call:
 //   at most 8 tokens, 64 entries   router logits; up projection, which routes in
 //                                  its prologue; down projection, summing over
 //                                  the experts in its accumulators (a column is
@@ -50,20 +51,28 @@ enum { kF32 = 0, kBF16 = 1, kE2M1 = 2 };  // weight storage
 constexpr int kWaves = 8;          // waves of the product kernels' workgroups
 constexpr int kThreads = kWaves * 64;
 
-// One chosen expert: its index, the place of its first entry in the
-// expert-ordered entry list, and which tokens chose it.
+typedef unsigned long long mask_t;  // tokens, a bit each
+
+// One chosen expert (few_down_kernel's): its index, its first hidden row, and
+// which tokens chose it.
 struct FewSlot {
   int e, off;
-  unsigned long long mask;
+  mask_t mask;
+};
+// What token t's choice of expert e says, at [t E + e] (nothing where t did not
+// choose e): its weight, and its entry t k + j.
+struct FewEntry {
+  float w;
+  int row;
 };
 
-// Rows of the hidden buffer: an entry's own, or (routing in the up
-// projection's prologue) T for every slot.
+// Rows of the hidden buffer: an entry's own, or (few_down_kernel) T for every
+// slot.
 bool in_prologue(int T, int k);
-bool tokens_down(int T, bool pro);  // few_down_kernel, not few_down_rows_kernel
+bool tokens_down(int T, int k);  // few_down_kernel, not few_down_rows_kernel
 int hid_rows(int T, int E, int k) {
   const int R = T * k, S = R < E ? R : E;
-  return in_prologue(T, k) ? S * T : R;
+  return tokens_down(T, k) ? S * T : R;
 }
 // Partial sums that the router's logits come in (its E / 16 row tiles alone would
 // leave most of the chip idle): as many as leave each of a workgroup's 8 waves a
@@ -77,12 +86,12 @@ int logit_parts(int row_bytes) {
 }
 
 struct FewLayout {
-  size_t n_active, slots, gate, logits, hid, pos, yp, bytes;
+  size_t n_active, slots, masks, entries, logits, hid, yp, bytes;
 };
 
 FewLayout few_layout(int T, int d, int E, int k, int h) {
   const size_t R = (size_t)T * k, S = R < (size_t)E ? R : (size_t)E;
-  const bool pro = in_prologue(T, k);
+  const bool rows = !tokens_down(T, k);
   FewLayout l;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -90,14 +99,13 @@ FewLayout few_layout(int T, int d, int E, int k, int h) {
     at += (n + 255) / 256 * 256;
     return p;
   };
-  l.n_active = take(sizeof(int));
-  l.slots = take(S * sizeof(FewSlot));
-  l.gate = take(R * sizeof(float));
+  l.n_active = take(rows ? 0 : sizeof(int));
+  l.slots = take(rows ? 0 : S * sizeof(FewSlot));
+  l.masks = take(rows ? E * sizeof(mask_t) : 0);
+  l.entries = take(rows ? (size_t)T * E * sizeof(FewEntry) : 0);
   l.logits = take((size_t)logit_parts(d * 4) * T * E * sizeof(float));  // fp32 rows have the most lines
   l.hid = take((size_t)hid_rows(T, E, k) * h * sizeof(float));         // fp32, or the hi and lo bf16 halves
-  const bool rows = !tokens_down(T, pro);
-  l.pos = take(rows ? R * sizeof(int) : 0);
-  l.yp = take(rows ? (size_t)hid_rows(T, E, k) * d * sizeof(float) : 0);
+  l.yp = take(rows ? R * d * sizeof(float) : 0);
   l.bytes = at;
   return l;
 }
@@ -492,16 +500,20 @@ TRG_DEV int live_tokens(const int* n_live, int T) { return n_live != nullptr ? m
 // ---- a dense product, and the router's logits -----------------------------------
 // out[t, row] = <x[t], w[row]> for T <= NT * 16 columns.  A workgroup takes NM
 // tiles of 16 rows, its waves share the lines; blockIdx.y takes the part_lines
-// lines from blockIdx.y * part_lines and writes its own [T, n] of out.
+// lines from blockIdx.y * part_lines and writes its own [T, n] of out.  The first
+// one also clears the nz masks that the next launch sets.
 template <int WT, int NM, int NT, int U, int XN, int WAVES, class OUT>
 __global__ __launch_bounds__(WAVES * 64, NT > 1 && NM* NT > 3 ? 2 : 4) void few_linear_kernel(
     const char* __restrict__ x, const void* __restrict__ w, const uint8_t* __restrict__ ws, int T, int n, int rb,
-    int xb, int part_lines, const int* __restrict__ n_live, OUT* __restrict__ out) {
+    int xb, int part_lines, const int* __restrict__ n_live, OUT* __restrict__ out, mask_t* __restrict__ masks,
+    int nz) {
   // the waves' staging buffers, then (1 KB a wave) their accumulators
   __shared__ __attribute__((aligned(16))) char lds[WAVES * (WT == kE2M1 ? kStage : 1024)];
   float* red = (float*)lds;
   const int lane = threadIdx.x & 63, wv = wave_id(), r = lane & 15, q = lane >> 4;
   const int live = live_tokens(n_live, T);
+  if (blockIdx.x + blockIdx.y == 0)
+    for (int i = threadIdx.x; i < nz; i += WAVES * 64) masks[i] = 0;
   const int row0 = blockIdx.x * (16 * NM);
   const int c0 = blockIdx.y * part_lines, c1 = min((rb + 127) >> 7, c0 + part_lines);
   const WBase wb[1] = {w_base<WT>(w, ws, 0, 1, n, rb)};
@@ -554,15 +566,19 @@ TRG_DEV float wave_sum_dpp(float v) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sum_dpp<0x143>(sum_dpp<0x142>(v))), 63));
 }
 
-// One wave routes token t from its logits (v[i] of lane l: expert l + 64 i): the
+// One wave routes a token from its logits (v[i] of lane l: expert l + 64 i): the
 // k largest, ties to the lower expert, a NaN never before a number (moe_route's
 // rules), and their softmax values.  A logit becomes a 32-bit key that orders
 // like it (0 is below every key), so a round is one wave maximum and the first
-// lane of the first register that holds it.  sel, selw: this token's k places.
+// lane of the first register that holds it.
 template <int EPL>
-TRG_DEV void route_token(float* v, int E, int k, int t, int lane, uint16_t* sel, float* selw,
-                         unsigned long long* mask) {
-  float p[EPL];
+struct Routed {
+  int mine;               // lane j: the j-th choice
+  int place[EPL];         // places of this lane's experts, -1: not chosen
+  float p[EPL], s;        // softmax p / s
+};
+template <int EPL>
+TRG_DEV void route_token(float* v, int E, int k, int lane, Routed<EPL>& o) {
   uint32_t key[EPL], top = 0;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
@@ -577,13 +593,13 @@ TRG_DEV void route_token(float* v, int E, int k, int t, int lane, uint16_t* sel,
   float s = 0.f;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    p[i] = lane + 64 * i < E ? expf(v[i] - m) : 0.f;
-    s += p[i];
+    o.p[i] = lane + 64 * i < E ? expf(v[i] - m) : 0.f;
+    s += o.p[i];
   }
-  s = wave_sum_dpp(s);
-  int place[EPL], mine = 0;  // places of this lane's experts; lane j: the j-th choice
+  o.s = wave_sum_dpp(s);
+  o.mine = 0;
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) place[i] = -1;
+  for (int i = 0; i < EPL; ++i) o.place[i] = -1;
   for (int j = 0; j < k; ++j) {
     // no branches: a round is a chain of dependent instructions as it is
     int e = 0;
@@ -592,24 +608,17 @@ TRG_DEV void route_token(float* v, int E, int k, int t, int lane, uint16_t* sel,
       const unsigned long long at = __ballot(key[i] == top);
       e = at != 0 ? 64 * i + __ffsll(at) - 1 : e;
     }
-    mine = lane == j ? e : mine;
+    o.mine = lane == j ? e : o.mine;
     uint32_t next = 0;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const bool hit = lane + 64 * i == e;
       key[i] = hit ? 0u : key[i];
-      place[i] = hit ? j : place[i];
+      o.place[i] = hit ? j : o.place[i];
       next = max(next, key[i]);
     }
     top = wave_max_u32(next);
   }
-  if (lane < k) {
-    sel[lane] = (uint16_t)mine;
-    atomicOr(&mask[mine], 1ull << t);  // integer: the order does not matter
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i)
-    if (place[i] >= 0) selw[place[i]] = p[i] / s;
 }
 
 // out[j] = the router's partial logits at at[j] (of plane = T E values), added in
@@ -635,65 +644,62 @@ TRG_DEV void add_logits(const float* __restrict__ logits, int parts, uint32_t pl
   }
 }
 
-constexpr int kRouteChunk = 8192;  // logits in LDS at a time
-
 // Routing in a launch of its own (more than kProTokens tokens or kProEntries
-// entries): one workgroup adds the partial logits of as many tokens as fit into
-// LDS, a wave routes a token at a time from there; then the chosen experts'
-// token masks are compacted, in expert order, into slots.
+// entries): a wave, and a workgroup, a token.  An expert's mask collects its tokens
+// by an integer OR, which has one result in any order; the products find the
+// chosen experts in the masks themselves (nth_expert), so that nothing has to wait
+// for all tokens.  One workgroup routing all of them and listing the experts took
+// 10.0 us with 61 tokens and 128 experts, 18.2 with 24 and 384.
 template <int EPL>
-__global__ __launch_bounds__(1024) void few_route_kernel(
-    const float* __restrict__ logits, int parts, int T, int E, int k, const int* __restrict__ n_live,
-    int* __restrict__ idx_out, float* __restrict__ w_out, int* __restrict__ n_active, FewSlot* __restrict__ slots,
-    float* __restrict__ gate, int* __restrict__ pos_out) {
-  __shared__ unsigned long long mask[1024];
-  __shared__ float chunk[kRouteChunk];
-  __shared__ int first[1024];
-  __shared__ int tmp[32];
-  __shared__ uint16_t sel16[64 * 32];
-  __shared__ float selw[64 * 32];
-  const int lane = threadIdx.x & 63, wv = wave_id();
-  mask[threadIdx.x] = 0;
-  const int live = live_tokens(n_live, T);
-  const int per = kRouteChunk / E;  // tokens a chunk: at least 8
-  for (int t0 = 0; t0 < live; t0 += per) {
-    const int nt = min(per, live - t0), n = nt * E;
-    uint32_t at[kRouteChunk / 1024];
-    float sum[kRouteChunk / 1024];
+__global__ __launch_bounds__(64) void few_route_kernel(const float* __restrict__ logits, int parts, int T, int E, int k,
+                                                       const int* __restrict__ n_live, int* __restrict__ idx_out,
+                                                       float* __restrict__ w_out, mask_t* __restrict__ masks,
+                                                       FewEntry* __restrict__ entries) {
+  const int lane = threadIdx.x, t = blockIdx.x;
+  uint32_t at[EPL];
+  float v[EPL];
 #pragma unroll
-    for (int j = 0; j < kRouteChunk / 1024; ++j)
-      at[j] = (uint32_t)(t0 * E + min((int)threadIdx.x + 1024 * j, n - 1));
-    add_logits<kRouteChunk / 1024>(logits, parts, (uint32_t)T * (uint32_t)E, at, sum);
-    __syncthreads();  // the chunk before has been read
+  for (int i = 0; i < EPL; ++i) at[i] = (uint32_t)(t * E + min(lane + 64 * i, E - 1));
+  if (t >= live_tokens(n_live, T)) return;
+  add_logits<EPL>(logits, parts, (uint32_t)T * (uint32_t)E, at, v);
+  Routed<EPL> o;
+  route_token<EPL>(v, E, k, lane, o);
+  if (lane < k) {
+    atomicOr(&masks[o.mine], 1ull << t);
+    if (idx_out != nullptr) idx_out[t * k + lane] = o.mine;
+  }
 #pragma unroll
-    for (int j = 0; j < kRouteChunk / 1024; ++j)
-      if ((int)threadIdx.x + 1024 * j < n) chunk[threadIdx.x + 1024 * j] = sum[j];
-    __syncthreads();
-    for (int t = wv; t < nt; t += 16) {
-      float v[EPL];
+  for (int i = 0; i < EPL; ++i)
+    if (o.place[i] >= 0) {
+      const int row = t * k + o.place[i];
+      entries[at[i]] = FewEntry{o.p[i] / o.s, row};
+      if (w_out != nullptr) w_out[row] = o.p[i] / o.s;
+    }
+}
+
+// The n-th expert, from 0, that has tokens, and its tokens' mask; -1: there are
+// no more.  The same in every lane.
+TRG_DEV int nth_expert(const mask_t* __restrict__ masks, int E, int n, int lane, mask_t* mask) {
+  constexpr int B = 4;  // loads in flight
+  for (int e0 = 0; e0 < E; e0 += 64 * B) {
+    mask_t m[B];
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) v[i] = chunk[t * E + min(lane + 64 * i, E - 1)];
-      route_token<EPL>(v, E, k, t0 + t, lane, sel16 + (t0 + t) * 32, selw + (t0 + t) * 32, mask);
+    for (int i = 0; i < B; ++i) m[i] = masks[min(e0 + 64 * i + lane, E - 1)];
+#pragma unroll
+    for (int i = 0; i < B; ++i) {
+      const mask_t on = __ballot(m[i] != 0 && e0 + 64 * i + lane < E);
+      const int c = __popcll(on);
+      if (n < c) {
+        const mask_t at = __ballot((on >> lane & 1) && __popcll(on & ((1ull << lane) - 1)) == n);
+        const int l = __ffsll(at) - 1;
+        *mask = (mask_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(m[i] >> 32), l) << 32 |
+                (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)m[i], l);
+        return e0 + 64 * i + l;
+      }
+      n -= c;
     }
   }
-  __syncthreads();
-  // experts with tokens, in order: (slots, entries) before each, in one scan
-  const unsigned long long mk = mask[threadIdx.x];
-  const int cnt = __popcll(mk);
-  int total;
-  const int before = block_excl_scan_1024((cnt > 0 ? 1 << 16 : 0) | cnt, tmp, &total);  // at most 2048 entries
-  first[threadIdx.x] = before & 0xFFFF;
-  if (cnt > 0) slots[before >> 16] = FewSlot{(int)threadIdx.x, before & 0xFFFF, mk};
-  if (threadIdx.x == 0) *n_active = total >> 16;
-  __syncthreads();
-  for (int i = threadIdx.x; i < live * k; i += 1024) {
-    const int t = i / k, j = i - t * k, e = sel16[t * 32 + j];
-    const int pos = first[e] + __popcll(mask[e] & ((1ull << t) - 1));
-    gate[pos] = selw[t * 32 + j];
-    pos_out[i] = pos;
-    if (idx_out != nullptr) idx_out[i] = e;
-    if (w_out != nullptr) w_out[i] = selw[t * 32 + j];
-  }
+  return -1;
 }
 
 // ---- up projection ------------------------------------------------------------------
@@ -708,13 +714,20 @@ TRG_DEV int nth_token(unsigned long long mask, int lane, int c) {
   return __builtin_amdgcn_ds_bpermute(c * 4, list);
 }
 
-// RM * 16 rows of h for a slot's columns: both matrices' rows, shared by the
+// Lane c: column c's choice, for the tokens of expert e's mask (not empty); lanes
+// without a column have the last one's.
+TRG_DEV FewEntry column_entry(const FewEntry* __restrict__ entries, int E, int e, mask_t mask, int lane) {
+  const int cnt = __popcll(mask), t = nth_token(mask, lane, min(lane, cnt - 1));  // every lane takes part
+  return entries[t * E + e];
+}
+
+// RM * 16 rows of h for an expert's columns: both matrices' rows, shared by the
 // workgroup's wk waves along k (this one is kw), then h = gate * silu(g) * u.
-// lds: 2 KB a wave (kStage with 4-bit weights).
+// ent: lane c has column c's.  lds: 2 KB a wave (kStage with 4-bit weights).
 template <int WT, int RM, int NT, int U, int XN>
-TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb, unsigned long long mask,
-                     const float* gate, int cnt, int col0, int row0, int h, char* hid, long hid_n, long pos0, int wk,
-                     int kw, char* lds) {
+TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb, mask_t mask,
+                     FewEntry ent, int cnt, int col0, int row0, int h, char* hid, long hid_n, int wk, int kw,
+                     char* lds) {
   float* red = (float*)lds;
   const int lane = threadIdx.x & 63, r = lane & 15, q = lane >> 4;
   WRow wr[2 * RM];
@@ -744,10 +757,12 @@ TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb
       __syncthreads();
       for (int o = threadIdx.x; o < 256; o += wk * 64) {
         const int lr = o & 15, col = o >> 4, c = col0 + i * 16 + col, row = row0 + m * 16 + lr;
+        const float gate = __int_as_float(__builtin_amdgcn_ds_bpermute(c * 4, __float_as_int(ent.w)));
+        const int hrow = __builtin_amdgcn_ds_bpermute(c * 4, ent.row);
         if (c < cnt && row < h) {
           const float g = sum_tile(red, wk, lr, col), u = sum_tile(red + wk * 256, wk, lr, col);
-          const float v = gate[c] * (g / (1.0f + expf(-g)) * u);
-          const long at = (pos0 + c) * h + row;
+          const float v = gate * (g / (1.0f + expf(-g)) * u);
+          const long at = (long)hrow * h + row;
           if constexpr (WT == kF32) {
             ((float*)hid)[at] = v;
           } else {
@@ -766,31 +781,32 @@ constexpr int kProEntries = 64;         // a lane an entry
 constexpr int kProRouter = 65536;       // bytes of router weights
 
 // PRO: every workgroup routes the (few) tokens in its prologue, a wave a token or
-// two, instead of waiting for a launch that does it once; the slots' first
-// workgroups leave them, and (pos_out) where the join finds their rows.  ROUTER:
-// it computes their logits too (at most 16 experts and kProRouter bytes of
-// router weights, which every workgroup reads).  Slots are then in the order of
-// their first (token, place), and slot s has hid rows s * T.
+// two, instead of waiting for a launch that does it once.  What the down
+// projection needs to know is left by the first workgroup (masks, entries), or
+// for few_down_kernel (slots not null) by each slot's first; slots are in the order
+// of their first (token, place), and slot s then has hid rows s * T.  ROUTER: it
+// computes the logits too (at most 16 experts and kProRouter bytes of router
+// weights, which every workgroup reads).
 template <int WT, int RM, int U, int EPL, bool PRO, bool ROUTER>
 __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     const char* __restrict__ x, int xb, const void* __restrict__ w1, const uint8_t* __restrict__ w1s,
     const void* __restrict__ w3, const uint8_t* __restrict__ w3s, const void* __restrict__ wr, int T, int E, int k,
     int h, int rb, const float* __restrict__ logits, int parts, const int* __restrict__ n_live,
     int* __restrict__ idx_out, float* __restrict__ w_out, int* __restrict__ n_active, FewSlot* __restrict__ slots,
-    float* __restrict__ gate, int* __restrict__ pos_out, char* __restrict__ hid, long hid_n) {
+    mask_t* __restrict__ masks, FewEntry* __restrict__ entries_out, char* __restrict__ hid, long hid_n) {
   const int wk = blockDim.x >> 6;  // all its waves share a row tile
   extern __shared__ __attribute__((aligned(16))) char lds[];  // lds_bytes<WT>(waves, 2)
   const int lane = threadIdx.x & 63, wv = wave_id();
   const int tiles = (h + 16 * RM - 1) / (16 * RM);
   const int slot = blockIdx.x / tiles, tile = near_tile<WT, 2 / RM>(blockIdx.x - slot * tiles, tiles);
   const int row0 = tile * 16 * RM;
-  FewSlot sl;
-  const float* gt;
+  int ex;          // the expert
+  mask_t toks;     // its tokens
+  FewEntry ent;    // lane c: column c's
   if constexpr (PRO) {
-    __shared__ unsigned long long mask[EPL * 64];
+    __shared__ mask_t mask[EPL * 64];
     __shared__ uint16_t sel[kProEntries];
     __shared__ float selw[kProEntries];
-    __shared__ float mygate[kProTokens];
     const int live = live_tokens(n_live, T), entries = live * k;
     for (int e = threadIdx.x; e < EPL * 64; e += kThreads) mask[e] = 0;  // launched with kThreads
     float* red = (float*)lds;
@@ -817,41 +833,51 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
         for (int i = 0; i < EPL; ++i) at[i] = (uint32_t)(tk * E + min(lane + 64 * i, E - 1));
         add_logits<EPL>(logits, parts, (uint32_t)T * (uint32_t)E, at, v);
       }
-      route_token<EPL>(v, E, k, tk, lane, sel + tk * k, selw + tk * k, mask);
+      Routed<EPL> o;
+      route_token<EPL>(v, E, k, lane, o);
+      if (lane < k) {
+        sel[tk * k + lane] = (uint16_t)o.mine;
+        atomicOr(&mask[o.mine], 1ull << tk);  // integer: the order does not matter
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i)
+        if (o.place[i] >= 0) selw[tk * k + o.place[i]] = o.p[i] / o.s;
     }
     __syncthreads();
     // every wave: lane = entry (token lane / k, place lane % k)
     const int e = lane < entries ? sel[lane] : 0, t = lane / k;
-    const unsigned long long mk = lane < entries ? mask[e] : 0;
-    const unsigned long long lead = __ballot(lane < entries && (mk & ((1ull << t) - 1)) == 0);
+    const mask_t mk = lane < entries ? mask[e] : 0;
+    const mask_t lead = __ballot(lane < entries && (mk & ((1ull << t) - 1)) == 0);
     const int na = __popcll(lead);
-    if (blockIdx.x == 0 && wv == 0) {
-      if (lane == 0) *n_active = na;
-      if (lane < entries && idx_out != nullptr) idx_out[lane] = e;
-      if (lane < entries && w_out != nullptr) w_out[lane] = selw[lane];
+    if (blockIdx.x == 0) {
+      if (wv == 0 && lane < entries) {
+        if (idx_out != nullptr) idx_out[lane] = e;
+        if (w_out != nullptr) w_out[lane] = selw[lane];
+      }
+      if (slots != nullptr) {
+        if (threadIdx.x == 0) *n_active = na;
+      } else {
+        if (wv == 0 && lane < entries) entries_out[t * E + e] = FewEntry{selw[lane], lane};
+        for (int i = threadIdx.x; i < E; i += kThreads) masks[i] = mask[i];
+      }
     }
     if (slot >= na) return;  // the whole workgroup
     const int at = nth_token(lead, lane, slot);  // the entry that leads this slot
-    sl.e = __builtin_amdgcn_readfirstlane(__shfl(e, at, 64));
-    sl.mask = mask[sl.e];
-    sl.off = slot * T;
-    if (wv == 0 && lane < entries && e == sl.e) {
-      const int rank = __popcll(sl.mask & ((1ull << t) - 1));
-      mygate[rank] = selw[lane];
-      if (tile == 0 && pos_out != nullptr) pos_out[lane] = sl.off + rank;
-    }
-    if (tile == 0 && threadIdx.x == 0) slots[slot] = sl;
-    gt = mygate;  // read after the products' barrier
+    ex = __builtin_amdgcn_readfirstlane(__shfl(e, at, 64));
+    toks = mask[ex];
+    // its entries are in its tokens' order
+    const int mine = nth_token(__ballot(lane < entries && e == ex), lane, lane);
+    ent = FewEntry{selw[mine], slots != nullptr ? slot * T + lane : mine};
+    if (slots != nullptr && tile == 0 && threadIdx.x == 0) slots[slot] = FewSlot{ex, slot * T, toks};
   } else {
-    const int na = *n_active;
-    sl = slots[slot];  // in bounds; meaningful if slot < na
-    if (slot >= na) return;
-    gt = gate + sl.off;
+    ex = nth_expert(masks, E, slot, lane, &toks);
+    if (ex < 0) return;  // the whole workgroup
+    ent = column_entry(entries_out, E, ex, toks, lane);
   }
-  const int cnt = __popcll(sl.mask);
-  const WBase wb[2] = {w_base<WT>(w1, w1s, sl.e, E, h, rb), w_base<WT>(w3, w3s, sl.e, E, h, rb)};
+  const int cnt = __popcll(toks);
+  const WBase wb[2] = {w_base<WT>(w1, w1s, ex, E, h, rb), w_base<WT>(w3, w3s, ex, E, h, rb)};
 #define TRG_TILE(RM, NT, U, XN, ROW0) \
-  up_tile<WT, RM, NT, U, XN>(x, xb, wb, rb, sl.mask, gt, cnt, c0, ROW0, h, hid, hid_n, sl.off, wk, wv, lds)
+  up_tile<WT, RM, NT, U, XN>(x, xb, wb, rb, toks, ent, cnt, c0, ROW0, h, hid, hid_n, wk, wv, lds)
   int c0 = 0;
   if constexpr (PRO) {
     if (WT == kE2M1 && cnt > 2) TRG_TILE(RM, 1, U, 8, row0);
@@ -984,8 +1010,9 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
 }
 
 // ---- down projection, more tokens ------------------------------------------------------
-// As the up projection: workgroup (slot, row tiles of d), columns the slot's own
-// tokens, lines shared by wk waves; every entry's row goes out in fp32 and the
+// As the up projection: workgroup (expert, row tiles of d), columns the expert's own
+// tokens, lines shared by wk waves; ent: lane c has column c's entry, the hidden
+// row it reads and the row it writes; every entry's row goes out in fp32 and the
 // join adds each token's k rows in order.  Those rows are R d floats, out and
 // in: 3 % of the weights' bytes with two tokens an expert at h = 1024 and 4
 // bits, 0.25 % in bf16 at h = 2048.
@@ -995,8 +1022,8 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
 // 61 tokens, 128 experts: 32.0 -> 29.9 us; bf16, whose reads set the pace, no
 // different, so it keeps the one form.
 template <int WT, int RM, int NT, int U, int XN, int H>
-TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb, int rb, int cnt, int col0, int row0,
-                       int d, int h, long pos0, int wk, int kw, char* lds, float* __restrict__ yp) {
+TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb, int rb, int ent, int cnt, int col0,
+                       int row0, int d, int h, int wk, int kw, char* lds, float* __restrict__ yp) {
   float* red = (float*)lds;
   constexpr int P = WT == kF32 || H > 0 ? 1 : 2, XE = Piece<WT>::kXE;
   constexpr int CT = H > 0 ? H : 16;  // tokens a column tile
@@ -1008,7 +1035,7 @@ TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb
 #pragma unroll
   for (int i = 0; i < NT; ++i) {
     const int c = col0 + i * CT + r % CT;
-    xo[i] = (uint32_t)(pos0 + min(c, cnt - 1)) * (uint32_t)(h * XE);
+    xo[i] = (uint32_t)__builtin_amdgcn_ds_bpermute(min(c, cnt - 1) * 4, ent) * (uint32_t)(h * XE);
     if (r >= CT) xo[i] += (uint32_t)hid_n * XE;
   }
   f32x4_t acc[RM][NT];
@@ -1027,10 +1054,11 @@ TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb
       __syncthreads();
       for (int o = threadIdx.x; o < 256; o += wk * 64) {
         const int lr = o & 15, col = o >> 4, c = col0 + i * CT + col, row = row0 + m * 16 + lr;
+        const int yrow = __builtin_amdgcn_ds_bpermute(c * 4, ent);
         if (col < CT && c < cnt && row < d) {
           float v = sum_tile(red, wk, lr, col);
           if constexpr (H > 0) v += sum_tile(red, wk, lr, col + H);
-          yp[(pos0 + c) * d + row] = v;
+          yp[(long)yrow * d + row] = v;
         }
       }
     }
@@ -1040,21 +1068,21 @@ template <int WT, int RM, int U>
 __global__ __launch_bounds__(kThreads, 4) void few_down_rows_kernel(const char* __restrict__ hid, long hid_n,
                                                                     const void* __restrict__ w2,
                                                                     const uint8_t* __restrict__ w2s, int E, int d,
-                                                                    int h, int rb, const int* __restrict__ n_active,
-                                                                    const FewSlot* __restrict__ slots,
+                                                                    int h, int rb, const mask_t* __restrict__ masks,
+                                                                    const FewEntry* __restrict__ entries,
                                                                     float* __restrict__ yp) {
   extern __shared__ __attribute__((aligned(16))) char lds[];  // lds_bytes<WT>(waves, 1)
-  const int wv = wave_id(), wk = blockDim.x >> 6;
+  const int wv = wave_id(), wk = blockDim.x >> 6, lane = threadIdx.x & 63;
   const int tiles = (d + 16 * RM - 1) / (16 * RM);
   const int slot = blockIdx.x / tiles, tile = blockIdx.x - slot * tiles;
   const int row0 = tile * 16 * RM;
-  const int na = *n_active;
-  const FewSlot sl = slots[slot];  // in bounds; meaningful if slot < na
-  if (slot >= na) return;
-  const int cnt = __popcll(sl.mask);
-  const WBase wb[1] = {w_base<WT>(w2, w2s, sl.e, E, d, rb)};
+  mask_t toks;
+  const int ex = nth_expert(masks, E, slot, lane, &toks);
+  if (ex < 0) return;
+  const int cnt = __popcll(toks), ent = column_entry(entries, E, ex, toks, lane).row;
+  const WBase wb[1] = {w_base<WT>(w2, w2s, ex, E, d, rb)};
 #define TRG_TILE(RM, NT, U, XN, H, ROW0) \
-  down_tile<WT, RM, NT, U, XN, H>(hid, hid_n, wb, rb, cnt, c0, ROW0, d, h, sl.off, wk, wv, lds, yp)
+  down_tile<WT, RM, NT, U, XN, H>(hid, hid_n, wb, rb, ent, cnt, c0, ROW0, d, h, wk, wv, lds, yp)
   int c0 = 0;
   if constexpr (WT == kE2M1) {
     if (cnt <= 2) TRG_TILE(RM, 1, U, 1, 2, row0);
@@ -1079,21 +1107,17 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_rows_kernel(const char* 
 
 // y[t] = sum over its k entries' rows, in the order of its choices.
 template <class OUT>
-__global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__ yp, const int* __restrict__ pos, int T,
-                                                       int d, int k, const int* __restrict__ n_live,
-                                                       OUT* __restrict__ y) {
+__global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__ yp, int T, int d, int k,
+                                                       const int* __restrict__ n_live, OUT* __restrict__ y) {
   const int i = (blockIdx.x * 256 + threadIdx.x) * 4;  // d is a multiple of 4
   const int t = blockIdx.y;
   if (i >= d || t >= live_tokens(n_live, T)) return;
   float4 a = make_float4(0, 0, 0, 0);
   constexpr int B = 8;  // rows in flight; past the last one it is loaded again and not added
   for (int j0 = 0; j0 < k; j0 += B) {
-    int p[B];
     float4 b[B];
 #pragma unroll
-    for (int j = 0; j < B; ++j) p[j] = pos[t * k + min(j0 + j, k - 1)];
-#pragma unroll
-    for (int j = 0; j < B; ++j) b[j] = *(const float4*)(yp + (long)p[j] * d + i);
+    for (int j = 0; j < B; ++j) b[j] = *(const float4*)(yp + (long)(t * k + min(j0 + j, k - 1)) * d + i);
 #pragma unroll
     for (int j = 0; j < B; ++j)
       if (j0 + j < k) {
@@ -1112,11 +1136,11 @@ __global__ __launch_bounds__(256) void few_join_kernel(const float* __restrict__
 
 template <int WT, int NM, int NT, int U, int XN, int WAVES, class OUT>
 hipError_t linear_nt(const void* x, const void* w, const uint8_t* ws, int T, int n, int rb, int xb, int parts,
-                     const int* n_live, OUT* out, hipStream_t st) {
+                     const int* n_live, OUT* out, hipStream_t st, mask_t* masks = nullptr, int nz = 0) {
   const int lines = (rb + 127) / 128, pl = (lines + parts - 1) / parts;
   few_linear_kernel<WT, NM, NT, U, XN, WAVES, OUT>
       <<<dim3((n + 16 * NM - 1) / (16 * NM), parts), WAVES * 64, 0, st>>>((const char*)x, w, ws, T, n, rb, xb, pl,
-                                                                          n_live, out);
+                                                                          n_live, out, masks, nz);
   return hipGetLastError();
 }
 
@@ -1139,7 +1163,7 @@ size_t lds_bytes(int waves, int tiles) {
 
 // The down projection over tokens writes y itself, in one launch; its tiles of 4
 // or 8 rows need T <= 8.
-bool tokens_down(int T, bool pro) { return pro && T <= 8; }
+bool tokens_down(int T, int k) { return in_prologue(T, k) && T <= 8; }
 
 bool in_prologue(int T, int k) { return T <= kProTokens && T * k <= kProEntries; }
 
@@ -1148,14 +1172,14 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   constexpr int XE = WT == kF32 ? 4 : 2;
   const FewLayout l = few_layout(a.T, a.d, a.E, a.k, a.h);
   char* ws = (char*)a.ws;
+  const bool pro = in_prologue(a.T, a.k), tokens = tokens_down(a.T, a.k);
   int* n_active = (int*)(ws + l.n_active);
-  FewSlot* slots = (FewSlot*)(ws + l.slots);
-  float* gate = (float*)(ws + l.gate);
+  FewSlot* slots = tokens ? (FewSlot*)(ws + l.slots) : nullptr;
+  mask_t* masks = (mask_t*)(ws + l.masks);
+  FewEntry* entries = (FewEntry*)(ws + l.entries);
   float* logits = (float*)(ws + l.logits);
   char* hid = ws + l.hid;
-  int* pos = (int*)(ws + l.pos);
   float* yp = (float*)(ws + l.yp);
-  const bool pro = in_prologue(a.T, a.k);
   const int R = a.T * a.k, slots_max = R < a.E ? R : a.E;
   const long hid_n = (long)hid_rows(a.T, a.E, a.k) * a.h;
   const int xb = a.d * XE;
@@ -1165,15 +1189,15 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   if (!router) {
     constexpr int RT = WT == kF32 ? kF32 : kBF16;
 #define TRG_LOGITS(NT) \
-  linear_nt<RT, 1, NT, 1, 1, kWaves, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, parts, a.n_live, logits, st)
+  linear_nt<RT, 1, NT, 1, 1, kWaves, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, parts, a.n_live, logits, st, \
+                                                masks, pro ? 0 : a.E)
     e = a.T <= 16 ? TRG_LOGITS(1) : a.T <= 32 ? TRG_LOGITS(2) : TRG_LOGITS(4);
 #undef TRG_LOGITS
     if (e != hipSuccess) return e;
   }
   if (!pro) {
 #define TRG_ROUTE(N)                                                                                                  \
-  few_route_kernel<N><<<1, 1024, 0, st>>>(logits, parts, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, n_active, \
-                                          slots, gate, pos)
+  few_route_kernel<N><<<a.T, 64, 0, st>>>(logits, parts, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, masks, entries)
     if (a.E <= 64) TRG_ROUTE(1);
     else if (a.E <= 128) TRG_ROUTE(2);
     else if (a.E <= 512) TRG_ROUTE(8);
@@ -1192,7 +1216,7 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   few_up_kernel<WT, RM, U, EPL, PRO, ROUTER>                                                                       \
       <<<(unsigned)slots_max * ((a.h + 16 * RM - 1) / (16 * RM)), uw * 64, lds_bytes<WT>(uw, 2), st>>>(            \
           (const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.wr, a.T, a.E, a.k, a.h, rb1, logits, parts, a.n_live,  \
-          a.topk_idx, a.topk_w, n_active, slots, gate, tokens_down(a.T, pro) ? nullptr : pos, hid, hid_n)
+          a.topk_idx, a.topk_w, n_active, slots, masks, entries, hid, hid_n)
   if (!pro && (UR == 1 || up_tiles < 1024)) TRG_UP(1, U, 1, false, false);  // two a wave would leave CUs idle
   else if (!pro) TRG_UP(UR, U, 1, false, false);
   else if (router) TRG_UP(1, UP, 1, true, true);
@@ -1206,7 +1230,7 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   few_down_kernel<WT, U, KS><<<(a.d + 16 / KS - 1) / (16 / KS), kThreads, 0, st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, \
                                                                                    a.h, rb2, n_active, slots,       \
                                                                                    slots_max, a.T, a.n_live, a.y)
-  if (tokens_down(a.T, pro)) {
+  if (tokens) {
     if (a.T <= 4) TRG_DOWN(4);
     else TRG_DOWN(2);
     return hipGetLastError();
@@ -1218,8 +1242,8 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   // 36.1; 128 experts, 61 tokens in 4 bits (4 a wave) 100, no more than 1 % apart.
 #define TRG_ROWS(RM, U)                                                                                             \
   few_down_rows_kernel<WT, RM, U><<<(unsigned)slots_max * ((a.d + 16 * RM - 1) / (16 * RM)), 64 * dw,               \
-                                    lds_bytes<WT>(dw, 1), st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, n_active, \
-                                                                slots, yp)
+                                    lds_bytes<WT>(dw, 1), st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, masks, \
+                                                                entries, yp)
   if (down_tiles < 4096) TRG_ROWS(2, 1);
   else TRG_ROWS(4, 1);
 #undef TRG_ROWS
@@ -1227,9 +1251,9 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   if (e != hipSuccess) return e;
   const dim3 jg((a.d / 4 + 255) / 256, a.T);
   if constexpr (WT == kF32)
-    few_join_kernel<float><<<jg, 256, 0, st>>>(yp, pos, a.T, a.d, a.k, a.n_live, (float*)a.y);
+    few_join_kernel<float><<<jg, 256, 0, st>>>(yp, a.T, a.d, a.k, a.n_live, (float*)a.y);
   else
-    few_join_kernel<uint16_t><<<jg, 256, 0, st>>>(yp, pos, a.T, a.d, a.k, a.n_live, (uint16_t*)a.y);
+    few_join_kernel<uint16_t><<<jg, 256, 0, st>>>(yp, a.T, a.d, a.k, a.n_live, (uint16_t*)a.y);
   return hipGetLastError();
 }
 
