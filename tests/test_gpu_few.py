@@ -140,6 +140,33 @@ def test_few_4bit(T, d, E, k, h):
     c.check(m.forward(c.x), m.topk_idx, m.topk_w)
 
 
+# few tokens on both sides of the rule for routing in the up projection (512
+# workgroups of 16 rows), and masks of more experts than one batch of loads
+@pytest.mark.parametrize("T,d,E,k,h", [(1, 64, 16, 8, 1024), (1, 64, 16, 8, 1056), (8, 64, 8, 2, 1024),
+                                       (8, 64, 8, 2, 1056), (1, 96, 40, 32, 256), (1, 96, 40, 32, 288),
+                                       (2, 64, 1024, 32, 160), (8, 64, 513, 8, 160), (64, 64, 1024, 2, 32),
+                                       (33, 64, 257, 1, 64)])
+@pytest.mark.parametrize("wt", ["bf16", "f32", "e2m1"])
+def test_few_routed_in_either_place(T, d, E, k, h, wt):
+    say(f"few T={T} d={d} E={E} k={k} h={h} {wt}")
+    c = Case(T, d, E, k, h, wt)
+    m = c.layer()
+    c.check(m.forward(c.x), m.topk_idx, m.topk_w)
+
+
+@pytest.mark.parametrize("live", [0, 1, 3, 5])
+def test_few_live_count_routed_in_its_own_launch(live):
+    """More rows than are live, at 1024 workgroups and few tokens."""
+    c = Case(5, 64, 200, 8, 416, "bf16")
+    n = torch.tensor([live], dtype=torch.int32, device=DEV)
+    m = c.layer()
+    full = m.forward(c.x).clone()
+    m.y.fill_(7)
+    m.topk_idx.fill_(-7)
+    m.forward(c.x, n_live=n)
+    assert torch.equal(m.y[:live], full[:live]) and (m.y[live:] == 7).all() and (m.topk_idx[live:] == -7).all()
+
+
 @pytest.mark.parametrize("wt", ["bf16", "e2m1"])
 def test_few_smaller_batches_of_one_object(wt):
     """Every batch from 0 to the object's T through the same buffers; rows

@@ -27,17 +27,16 @@
 // instruction is free next to the weight stream.  fp32 weights use the fp32
 // matrix instruction and h stays fp32.
 //
-// Launches, by the tokens (T) and entries (T k: a token's place among its k) of the
-// call:
-//   at most 8 tokens, 64 entries   router logits; up projection, which routes in
+// Launches (in_prologue has the rule):
+//   a token or a few, few experts  router logits; up projection, which routes in
 //                                  its prologue; down projection, summing over
 //                                  the experts in its accumulators (a column is
 //                                  a token, whichever experts it chose).  With
 //                                  at most 16 experts the up projection computes
 //                                  the logits as well: two launches.
-//   at most 16 tokens, 64 entries  the same, but the down projection writes a
-//                                  row an entry and a join adds a token's rows
-//   more                           logits; routing; up; down; join
+//   more                           logits; routing; up; down, a row an entry (a
+//                                  token's place among its k); join, which adds a
+//                                  token's rows
 // Every sum has a fixed order.
 #include "common.h"
 #include "kernels.h"
@@ -66,14 +65,26 @@ struct FewEntry {
   int row;
 };
 
+// The most experts that T tokens can choose.
+int slots_of(int T, int E, int k) { return T * k < E ? T * k : E; }
+
+constexpr int kProTokens = kWaves;  // tokens that the up projection routes itself: a wave each
+constexpr int kProEntries = 64;     // and their entries: a lane each
+// Routing in the up projection's prologue, and few_down_kernel: the launches of
+// the routing and the join are saved (3 to 6 us), but every workgroup routes, so
+// only where the chip takes all of them at once (256 CUs, two of 8 waves each).
+// Measured, prologue / own launch, us, d = 2048, bf16 and 4 bits, with 512
+// workgroups: one token, 128 experts, h = 2048, k = 4 30.1 / 34.2, 18.2 / 21.3; 2
+// tokens, 384 experts, h = 512, k = 8 31.8 / 36.9, 22.6 / 24.1; 8 tokens, 8
+// experts, h = 1024, k = 4 32.1 / 33.3, 20.5 / 21.6.  With 1024: one token, 384
+// experts, h = 2048, k = 8 57.5 / 54.0, 32.3 / 29.2; 8 tokens, 8 experts, h = 2048,
+// k = 2 57.2 / 55.2, 30.6 / 25.4.
+bool in_prologue(int T, int E, int k, int h) {
+  return T <= kProTokens && T * k <= kProEntries && slots_of(T, E, k) * ((h + 15) / 16) <= 512;
+}
 // Rows of the hidden buffer: an entry's own, or (few_down_kernel) T for every
 // slot.
-bool in_prologue(int T, int k);
-bool tokens_down(int T, int k);  // few_down_kernel, not few_down_rows_kernel
-int hid_rows(int T, int E, int k) {
-  const int R = T * k, S = R < E ? R : E;
-  return tokens_down(T, k) ? S * T : R;
-}
+int hid_rows(int T, int E, int k, int h) { return in_prologue(T, E, k, h) ? slots_of(T, E, k) * T : T * k; }
 // Partial sums that the router's logits come in (its E / 16 row tiles alone would
 // leave most of the chip idle): as many as leave each of a workgroup's 8 waves a
 // line.  Whoever adds them reads them all, so no more than that.  One part of 16
@@ -90,8 +101,8 @@ struct FewLayout {
 };
 
 FewLayout few_layout(int T, int d, int E, int k, int h) {
-  const size_t R = (size_t)T * k, S = R < (size_t)E ? R : (size_t)E;
-  const bool rows = !tokens_down(T, k);
+  const size_t R = (size_t)T * k, S = slots_of(T, E, k);
+  const bool rows = !in_prologue(T, E, k, h);
   FewLayout l;
   size_t at = 0;
   auto take = [&](size_t n) {
@@ -104,7 +115,7 @@ FewLayout few_layout(int T, int d, int E, int k, int h) {
   l.masks = take(rows ? E * sizeof(mask_t) : 0);
   l.entries = take(rows ? (size_t)T * E * sizeof(FewEntry) : 0);
   l.logits = take((size_t)logit_parts(d * 4) * T * E * sizeof(float));  // fp32 rows have the most lines
-  l.hid = take((size_t)hid_rows(T, E, k) * h * sizeof(float));         // fp32, or the hi and lo bf16 halves
+  l.hid = take((size_t)hid_rows(T, E, k, h) * h * sizeof(float));         // fp32, or the hi and lo bf16 halves
   l.yp = take(rows ? R * d * sizeof(float) : 0);
   l.bytes = at;
   return l;
@@ -644,8 +655,7 @@ TRG_DEV void add_logits(const float* __restrict__ logits, int parts, uint32_t pl
   }
 }
 
-// Routing in a launch of its own (more than kProTokens tokens or kProEntries
-// entries): a wave, and a workgroup, a token.  An expert's mask collects its tokens
+// Routing in a launch of its own: a wave, and a workgroup, a token.  An expert's mask collects its tokens
 // by an integer OR, which has one result in any order; the products find the
 // chosen experts in the masks themselves (nth_expert), so that nothing has to wait
 // for all tokens.  One workgroup routing all of them and listing the experts took
@@ -776,24 +786,21 @@ TRG_DEV void up_tile(const char* __restrict__ x, int xb, const WBase* wb, int rb
     }
 }
 
-constexpr int kProTokens = 2 * kWaves;  // tokens and entries that the up projection routes itself
-constexpr int kProEntries = 64;         // a lane an entry
-constexpr int kProRouter = 65536;       // bytes of router weights
+constexpr int kProRouter = 65536;  // bytes of router weights that a prologue reads
 
-// PRO: every workgroup routes the (few) tokens in its prologue, a wave a token or
-// two, instead of waiting for a launch that does it once.  What the down
-// projection needs to know is left by the first workgroup (masks, entries), or
-// for few_down_kernel (slots not null) by each slot's first; slots are in the order
-// of their first (token, place), and slot s then has hid rows s * T.  ROUTER: it
-// computes the logits too (at most 16 experts and kProRouter bytes of router
-// weights, which every workgroup reads).
+// PRO: every workgroup routes the (few) tokens in its prologue, a wave a token,
+// instead of waiting for a launch that does it once.  Each slot's first workgroup
+// leaves it for the down projection; slots are in the order of their first (token,
+// place), and slot s has hid rows s * T.  ROUTER: it computes the logits too (at
+// most 16 experts and kProRouter bytes of router weights, which every workgroup
+// reads).
 template <int WT, int RM, int U, int EPL, bool PRO, bool ROUTER>
 __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     const char* __restrict__ x, int xb, const void* __restrict__ w1, const uint8_t* __restrict__ w1s,
     const void* __restrict__ w3, const uint8_t* __restrict__ w3s, const void* __restrict__ wr, int T, int E, int k,
     int h, int rb, const float* __restrict__ logits, int parts, const int* __restrict__ n_live,
     int* __restrict__ idx_out, float* __restrict__ w_out, int* __restrict__ n_active, FewSlot* __restrict__ slots,
-    mask_t* __restrict__ masks, FewEntry* __restrict__ entries_out, char* __restrict__ hid, long hid_n) {
+    const mask_t* __restrict__ masks, const FewEntry* __restrict__ entries, char* __restrict__ hid, long hid_n) {
   const int wk = blockDim.x >> 6;  // all its waves share a row tile
   extern __shared__ __attribute__((aligned(16))) char lds[];  // lds_bytes<WT>(waves, 2)
   const int lane = threadIdx.x & 63, wv = wave_id();
@@ -807,7 +814,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     __shared__ mask_t mask[EPL * 64];
     __shared__ uint16_t sel[kProEntries];
     __shared__ float selw[kProEntries];
-    const int live = live_tokens(n_live, T), entries = live * k;
+    const int live = live_tokens(n_live, T), ne = live * k;
     for (int e = threadIdx.x; e < EPL * 64; e += kThreads) mask[e] = 0;  // launched with kThreads
     float* red = (float*)lds;
     if constexpr (ROUTER) {
@@ -822,57 +829,48 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
       put_tile(red + wv * 256, lane, acc[0][0]);
     }
     __syncthreads();
-#pragma unroll 1
-    for (int tk = wv; tk < live; tk += kWaves) {
+    if (wv < live) {
       float v[EPL];
       if constexpr (ROUTER) {
-        v[0] = sum_tile(red, kWaves, lane & 15, tk);
+        v[0] = sum_tile(red, kWaves, lane & 15, wv);
       } else {
         uint32_t at[EPL];
 #pragma unroll
-        for (int i = 0; i < EPL; ++i) at[i] = (uint32_t)(tk * E + min(lane + 64 * i, E - 1));
+        for (int i = 0; i < EPL; ++i) at[i] = (uint32_t)(wv * E + min(lane + 64 * i, E - 1));
         add_logits<EPL>(logits, parts, (uint32_t)T * (uint32_t)E, at, v);
       }
       Routed<EPL> o;
       route_token<EPL>(v, E, k, lane, o);
       if (lane < k) {
-        sel[tk * k + lane] = (uint16_t)o.mine;
-        atomicOr(&mask[o.mine], 1ull << tk);  // integer: the order does not matter
+        sel[wv * k + lane] = (uint16_t)o.mine;
+        atomicOr(&mask[o.mine], 1ull << wv);  // integer: the order does not matter
       }
 #pragma unroll
       for (int i = 0; i < EPL; ++i)
-        if (o.place[i] >= 0) selw[tk * k + o.place[i]] = o.p[i] / o.s;
+        if (o.place[i] >= 0) selw[wv * k + o.place[i]] = o.p[i] / o.s;
     }
     __syncthreads();
     // every wave: lane = entry (token lane / k, place lane % k)
-    const int e = lane < entries ? sel[lane] : 0, t = lane / k;
-    const mask_t mk = lane < entries ? mask[e] : 0;
-    const mask_t lead = __ballot(lane < entries && (mk & ((1ull << t) - 1)) == 0);
+    const int e = lane < ne ? sel[lane] : 0, t = lane / k;
+    const mask_t mk = lane < ne ? mask[e] : 0;
+    const mask_t lead = __ballot(lane < ne && (mk & ((1ull << t) - 1)) == 0);
     const int na = __popcll(lead);
-    if (blockIdx.x == 0) {
-      if (wv == 0 && lane < entries) {
-        if (idx_out != nullptr) idx_out[lane] = e;
-        if (w_out != nullptr) w_out[lane] = selw[lane];
-      }
-      if (slots != nullptr) {
-        if (threadIdx.x == 0) *n_active = na;
-      } else {
-        if (wv == 0 && lane < entries) entries_out[t * E + e] = FewEntry{selw[lane], lane};
-        for (int i = threadIdx.x; i < E; i += kThreads) masks[i] = mask[i];
-      }
+    if (blockIdx.x == 0 && wv == 0) {
+      if (lane == 0) *n_active = na;
+      if (lane < ne && idx_out != nullptr) idx_out[lane] = e;
+      if (lane < ne && w_out != nullptr) w_out[lane] = selw[lane];
     }
     if (slot >= na) return;  // the whole workgroup
     const int at = nth_token(lead, lane, slot);  // the entry that leads this slot
     ex = __builtin_amdgcn_readfirstlane(__shfl(e, at, 64));
     toks = mask[ex];
     // its entries are in its tokens' order
-    const int mine = nth_token(__ballot(lane < entries && e == ex), lane, lane);
-    ent = FewEntry{selw[mine], slots != nullptr ? slot * T + lane : mine};
-    if (slots != nullptr && tile == 0 && threadIdx.x == 0) slots[slot] = FewSlot{ex, slot * T, toks};
+    ent = FewEntry{selw[nth_token(__ballot(lane < ne && e == ex), lane, lane)], slot * T + lane};
+    if (tile == 0 && threadIdx.x == 0) slots[slot] = FewSlot{ex, slot * T, toks};
   } else {
     ex = nth_expert(masks, E, slot, lane, &toks);
     if (ex < 0) return;  // the whole workgroup
-    ent = column_entry(entries_out, E, ex, toks, lane);
+    ent = column_entry(entries, E, ex, toks, lane);
   }
   const int cnt = __popcll(toks);
   const WBase wb[2] = {w_base<WT>(w1, w1s, ex, E, h, rb), w_base<WT>(w3, w3s, ex, E, h, rb)};
@@ -880,7 +878,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
   up_tile<WT, RM, NT, U, XN>(x, xb, wb, rb, toks, ent, cnt, c0, ROW0, h, hid, hid_n, wk, wv, lds)
   int c0 = 0;
   if constexpr (PRO) {
-    if (WT == kE2M1 && cnt > 2) TRG_TILE(RM, 1, U, 8, row0);
+    if (WT == kE2M1 && cnt > 2) TRG_TILE(RM, 1, U, 4, row0);
     else TRG_TILE(RM, 1, U, 1, row0);
   } else if constexpr (WT == kE2M1) {
     // 4-bit rows are read again for every 16 tokens (from L2): the accumulators
@@ -904,7 +902,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
 #undef TRG_TILE
 }
 
-// ---- down projection, at most 8 tokens -----------------------------------------------
+// ---- down projection after a prologue's routing: at most 8 tokens ----------------------
 // A workgroup takes 16 / KS rows of d and all chosen experts: item f is KS
 // lines of a row, from line f % nit * KS of slot f / nit.  A column is a token;
 // an expert's item meets only the columns of its own tokens.  T <= 16 / KS: the
@@ -1009,7 +1007,7 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
   }
 }
 
-// ---- down projection, more tokens ------------------------------------------------------
+// ---- down projection, a row an entry --------------------------------------------------
 // As the up projection: workgroup (expert, row tiles of d), columns the expert's own
 // tokens, lines shared by wk waves; ent: lane c has column c's entry, the hidden
 // row it reads and the row it writes; every entry's row goes out in fp32 and the
@@ -1161,27 +1159,21 @@ size_t lds_bytes(int waves, int tiles) {
   return (size_t)waves * (WT == kE2M1 ? kStage : tiles * 1024);
 }
 
-// The down projection over tokens writes y itself, in one launch; its tiles of 4
-// or 8 rows need T <= 8.
-bool tokens_down(int T, int k) { return in_prologue(T, k) && T <= 8; }
-
-bool in_prologue(int T, int k) { return T <= kProTokens && T * k <= kProEntries; }
-
 template <int WT>
 hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   constexpr int XE = WT == kF32 ? 4 : 2;
   const FewLayout l = few_layout(a.T, a.d, a.E, a.k, a.h);
   char* ws = (char*)a.ws;
-  const bool pro = in_prologue(a.T, a.k), tokens = tokens_down(a.T, a.k);
+  const bool pro = in_prologue(a.T, a.E, a.k, a.h);
   int* n_active = (int*)(ws + l.n_active);
-  FewSlot* slots = tokens ? (FewSlot*)(ws + l.slots) : nullptr;
+  FewSlot* slots = (FewSlot*)(ws + l.slots);
   mask_t* masks = (mask_t*)(ws + l.masks);
   FewEntry* entries = (FewEntry*)(ws + l.entries);
   float* logits = (float*)(ws + l.logits);
   char* hid = ws + l.hid;
   float* yp = (float*)(ws + l.yp);
-  const int R = a.T * a.k, slots_max = R < a.E ? R : a.E;
-  const long hid_n = (long)hid_rows(a.T, a.E, a.k) * a.h;
+  const int slots_max = slots_of(a.T, a.E, a.k);
+  const long hid_n = (long)hid_rows(a.T, a.E, a.k, a.h) * a.h;
   const int xb = a.d * XE;
   const bool router = pro && a.E <= 16 && a.E * xb <= kProRouter;
   const int parts = logit_parts(xb);
@@ -1230,7 +1222,7 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   few_down_kernel<WT, U, KS><<<(a.d + 16 / KS - 1) / (16 / KS), kThreads, 0, st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, \
                                                                                    a.h, rb2, n_active, slots,       \
                                                                                    slots_max, a.T, a.n_live, a.y)
-  if (tokens) {
+  if (pro) {
     if (a.T <= 4) TRG_DOWN(4);
     else TRG_DOWN(2);
     return hipGetLastError();
