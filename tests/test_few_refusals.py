@@ -170,3 +170,25 @@ def test_host_tensors_and_wrong_shapes_are_refused():
         _abi.mx_linear_e2m1(x, w, w, torch.zeros(3, 8, dtype=bf))
     with pytest.raises(_abi.MoeError, match="w1 must be"):
         _abi.few_args(2, torch.zeros(8, 64, dtype=bf), x, x, x, w)
+
+
+def test_norms_refuse_more_rows_than_a_launch_has_threads_for():
+    """64 threads a row up to 4 KiB, 256 up to 16 KiB, 1024 above: 2^32 in all."""
+    lib = _lib()
+    for T, d, dt in ((1 << 26, 8, 1), (1 << 26, 1024, 0), (1 << 24, 2056, 1), (1 << 22, 16384, 1),
+                     (2 ** 31 - 1, 64, 1)):
+        _says(lib.moe_rmsnorm_fwd(C, None, C, T, d, 1e-6, dt, None, C, None, None, None, None), UNSUPPORTED,
+              "too large")
+        _says(lib.moe_rmsnorm_bwd(C, None, C, C, C, T, d, dt, C, C, C, 1 << 40, None), UNSUPPORTED, "too large")
+
+
+def test_decode_layer_of_no_tokens_is_refused():
+    from token_routing_grouped_amd import _abi
+    from token_routing_grouped_amd.layer import MoEDecodeGPU
+
+    w = torch.zeros(4, 64, 64)
+    for T in (0, -3):
+        with pytest.raises(_abi.MoeError, match="at least 1"):
+            MoEDecodeGPU(T, 2, torch.zeros(4, 64), w, w, w)
+    with pytest.raises(_abi.MoeError, match="T must be"):
+        MoEDecodeGPU(65, 2, torch.zeros(4, 64), w, w, w)

@@ -282,6 +282,27 @@ def test_few_captured_once_for_every_batch():
             assert torch.equal(m.topk_idx[:t], eager_y.topk_idx[:t])
 
 
+@pytest.mark.parametrize("T,E,wt", [(6, 8, "bf16"), (1, 40, "e2m1"), (20, 300, "e2m1")])
+def test_few_captured_and_replayed(T, E, wt):
+    """Each way through (two launches, three, five): replays with other tokens
+    equal eager calls bit for bit, whatever ran in between."""
+    c = Case(T, 256, E, 2, 64, wt)
+    m, e = c.layer(), c.layer()
+    x = c.x.clone()
+    m.forward(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        m.forward(x)
+    for i in range(4):
+        x.copy_(torch.from_numpy(np.random.default_rng(i).standard_normal((T, 256)).astype(np.float32)).to(DEV))
+        e.forward(x)
+        m.y.fill_(5)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(m.y, e.y) and torch.equal(m.topk_idx, e.topk_idx) and torch.equal(m.topk_w, e.topk_w)
+
+
 def test_few_two_streams_at_once():
     """Two objects with the same weights on two streams, interleaved."""
     a = Case(3, 520, 16, 4, 256, "bf16")

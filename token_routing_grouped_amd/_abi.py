@@ -534,7 +534,8 @@ def moe_rmsnorm_fwd(x, w, eps, y, res=None, s=None, q=None, qs=None, rstd=None):
     T, d = _matrix(x, "x")
     n, dt, dev = T * d, x.dtype, _device(x)
     _check(lib().moe_rmsnorm_fwd(_arg(x, dt, n, "x", dev), _arg(res, dt, n, "res", dev), _arg(w, dt, d, "w", dev), T,
-                                 d, eps, _dt(x), _arg(s, dt, n, "s", dev), _arg(y, dt, n, "y", dev), _arg(q, torch.uint8, n, "q", dev),
+                                 d, eps, _dt(x), _arg(s, dt, n, "s", dev), _arg(y, dt, n, "y", dev),
+                                 _arg(q, torch.uint8, n, "q", dev),
                                  _arg(qs, torch.uint8, mx_scale_bytes(T, d), "qs", dev),
                                  _arg(rstd, torch.float32, T, "rstd", dev), _stream(dev)), "moe_rmsnorm_fwd")
 

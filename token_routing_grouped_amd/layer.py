@@ -353,6 +353,8 @@ class MoEDecodeGPU:
     """
 
     def __init__(self, T: int, k: int, wr, w1, w3, w2, w1s=None, w3s=None, w2s=None, norm_w=None, eps: float = 1e-6):
+        if T < 1:
+            raise _abi.MoeError(f"T must be at least 1, got {T}")
         E, d = wr.shape
         dev = wr.device
         self.T, self.d, self.E, self.k, self.h = T, d, E, k, w1.shape[1]
