@@ -1147,10 +1147,11 @@ hipError_t linear_nt(const void* x, const void* w, const uint8_t* ws, int T, int
 // loads in flight), short ones leave a wave too little to do, and with many
 // tiles the chip is full without them.  Measured, us a pass with 8 / 4 / 2 / 1
 // waves: 24 tokens, 384 experts, rows of 12 and 4 KB 1843 / 1926 / 2018 / 2029; 61
-// tokens, 128 experts, rows of 4 and 2 KB 260 / 268 / 276 / 270, of 1 KB and 512
-// bytes (4 bits) 141 / 108 / 101 / 104; 16 tokens, 8 experts, 4 bits 26.7 / 26.6 /
-// 29.8 / 37.5.
-int row_waves(int rb, long tiles) { return rb >= 4096 ? 8 : (rb <= 1024 && tiles >= 4096 ? 2 : 4); }
+// tokens, 128 experts, rows of 4 and 2 KB 260 / 268 / 276 / 270.  4 bits, waves of
+// the up and of the down projection: 61 tokens, 128 experts, rows of 1 KB and 512
+// bytes 4, 4: 99.3; 2, 4: 94.5; 2, 2: 90.5; 2, 1: 88.6; 1, 2: 93.0; 64 tokens, 8
+// experts 4, 4: 39.5; 4, 2: 40.5; 2, 2: 42.0.
+int row_waves(int rb, long tiles) { return rb >= 4096 ? 8 : rb > 1024 || tiles < 4096 ? 4 : rb > 512 ? 2 : 1; }
 
 // LDS of a product's workgroup: the waves' accumulators of `tiles` matrices, or
 // their staging buffers.
