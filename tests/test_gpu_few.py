@@ -154,6 +154,20 @@ def test_few_routed_in_either_place(T, d, E, k, h, wt):
     c.check(m.forward(c.x), m.topk_idx, m.topk_w)
 
 
+# every expert has all the tokens: each number of column tiles, with one and more
+# row tiles a wave in either projection
+@pytest.mark.parametrize("E,d,h", [(2, 136, 72), (32, 64, 512), (32, 2048, 32)])
+@pytest.mark.parametrize("T", [16, 17, 32, 33, 48, 49])
+@pytest.mark.parametrize("wt", ["bf16", "f32", "e2m1"])
+def test_few_every_expert_has_every_token(wt, T, E, d, h):
+    if wt == "e2m1":
+        d, h = d // 32 * 32, h // 32 * 32
+    say(f"few T={T} d={d} E=k={E} h={h} {wt}")
+    c = Case(T, d, E, E, h, wt)
+    m = c.layer()
+    c.check(m.forward(c.x), m.topk_idx, m.topk_w)
+
+
 @pytest.mark.parametrize("live", [0, 1, 3, 5])
 def test_few_live_count_routed_in_its_own_launch(live):
     """More rows than are live, at 1024 workgroups and few tokens."""
