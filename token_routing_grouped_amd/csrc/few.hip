@@ -705,7 +705,7 @@ TRG_DEV int nth_expert(const mask_t* __restrict__ masks, int E, int n, int lane,
       const mask_t on = __ballot(m[i] != 0 && e0 + 64 * i + lane < E);
       const int c = __popcll(on);
       if (n < c) {
-        const mask_t at = __ballot((on >> lane & 1) && __popcll(on & ((1ull << lane) - 1)) == n);
+        const mask_t at = __ballot((on >> lane & 1) && (int)__popcll(on & ((1ull << lane) - 1)) == n);
         const int l = __ffsll(at) - 1;
         *mask = (mask_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(m[i] >> 32), l) << 32 |
                 (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)m[i], l);
