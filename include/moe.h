@@ -502,8 +502,8 @@ moe_status_t moe_grouped_gemm_recompute_gu_mx(const moe_mx_fwd_args* args, void*
  *   rstd (nullable): [T] f32, for the backward.
  * w [d] dt.  eps finite and >= 0.  s may be x or res, and y may be x or res if
  * s is neither the same buffer; nothing else may overlap.  T = 0 writes
- * nothing.  d * element size at most 128 KiB, and T rows of 64 threads (256 from
- * 4 KiB on, 1024 from 16 KiB on) fewer than 2^32 threads.
+ * nothing.  d * element size at most 128 KiB, and fewer than 2^32 threads: 256
+ * for each four rows begun, or each row over 4 KiB; 1024 for each row over 16 KiB.
  */
 moe_status_t moe_rmsnorm_fwd(const void* x, const void* res, const void* w, int T, int d, float eps, int dt, void* s,
                              void* y, uint8_t* q, uint8_t* qs, float* rstd, void* stream);

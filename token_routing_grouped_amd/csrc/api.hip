@@ -666,9 +666,10 @@ static moe_status_t check_norm_dims(const char* fn, int T, int d, int dt) {
   // a row is held in registers: 16 waves of 64 lanes, eight 16-byte pieces each
   if ((long)d * esize(dt) > 16L * 64 * 8 * 16)
     return fail(MOE_ERR_UNSUPPORTED, "%s: d * element size must be at most 128 KiB", fn);
-  // a launch has fewer than 2^32 threads: 64 a row, or 1024 where a row is over 16 KiB, 256 over 4 KiB
+  // a launch has fewer than 2^32 threads: 1024 a row over 16 KiB, 256 a row over 4 KiB, else 256 for each four
+  // rows begun
   const long bytes = (long)d * esize(dt);
-  if ((long)T * (bytes > 16384 ? 1024 : bytes > 4096 ? 256 : 64) >= (1L << 32))
+  if ((bytes > 16384 ? (long)T * 1024 : bytes > 4096 ? (long)T * 256 : ((long)T + 3) / 4 * 256) >= (1L << 32))
     return fail(MOE_ERR_UNSUPPORTED, "%s: problem too large", fn);
   return MOE_OK;
 }
