@@ -535,8 +535,8 @@ moe_status_t moe_rmsnorm_bwd(const void* dy, const void* ds, const void* s, cons
  * mx_quantize_e2m1: in [rows, cols] (dt MOE_F32 or MOE_BF16) to q and s.
  * mx_dequantize_e2m1: q and s to the values they stand for, in dt (exact in
  *   either, but for values under the type's smallest).
- * cols a multiple of 32; q 16-byte, s 4-byte aligned; rows * ceil(cols/128) <
- * 2^26.
+ * cols a multiple of 32, at most 2^31 - 128; q 16-byte, s 4-byte aligned; rows *
+ * ceil(cols/128) < 2^26.
  */
 moe_status_t mx_quantize_e2m1(const void* in, int dt, int rows, int cols, uint8_t* q, uint8_t* s, void* stream);
 moe_status_t mx_dequantize_e2m1(const uint8_t* q, const uint8_t* s, int dt, int rows, int cols, void* out,

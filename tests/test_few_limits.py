@@ -45,3 +45,17 @@ def test_norm_rows_end_where_a_launch_has_2_32_threads(d, dt, last):
     for T in (last + 1, last + 2, last + 3, last + 4):
         _says(fwd(T), UNSUPPORTED, "too large")
         _says(bwd(T), UNSUPPORTED, "too large")
+
+
+def test_e2m1_columns_end_where_rounding_up_to_a_chunk_passes_31_bits():
+    """cols + 127 is taken in 32 bits.  (Accepted sizes are then refused for
+    their missing buffers, or have no rows.)"""
+    lib = _lib()
+    last = 2 ** 31 - 128
+    for rows in (1, 2, 3):
+        _says(lib.mx_quantize_e2m1(C, 1, rows, last, None, C, None), INVALID, "q is null")
+        _says(lib.mx_dequantize_e2m1(None, C, 0, rows, last, C, None), INVALID, "q is null")
+    for cols in (last + 32, last + 64, last + 96):
+        for rows in (0, 1, 2, 3):
+            _says(lib.mx_quantize_e2m1(C, 1, rows, cols, None, C, None), UNSUPPORTED, "cols must be at most")
+            _says(lib.mx_dequantize_e2m1(None, C, 0, rows, cols, C, None), UNSUPPORTED, "cols must be at most")

@@ -724,6 +724,8 @@ moe_status_t moe_rmsnorm_bwd(const void* dy, const void* ds, const void* s, cons
 static moe_status_t check_e2m1(const char* fn, long rows, long cols, const uint8_t* q, const uint8_t* s) {
   if (rows < 0) return fail(MOE_ERR_INVALID_ARG, "%s: rows must be >= 0", fn);
   if (cols <= 0 || cols % 32 != 0) return fail(MOE_ERR_INVALID_ARG, "%s: cols must be a positive multiple of 32", fn);
+  // the launches and kernels round columns up to whole chunks in 32 bits
+  if (cols > INT32_MAX - 127) return fail(MOE_ERR_UNSUPPORTED, "%s: cols must be at most 2^31 - 128", fn);
   // a launch has fewer than 2^32 threads: 32 a 128-value chunk (fp32)
   if (rows * ((cols + 127) / 128) >= (1L << 26)) return fail(MOE_ERR_UNSUPPORTED, "%s: problem too large", fn);
   if (rows == 0) return MOE_OK;
