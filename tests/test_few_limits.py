@@ -59,3 +59,11 @@ def test_e2m1_columns_end_where_rounding_up_to_a_chunk_passes_31_bits():
         for rows in (0, 1, 2, 3):
             _says(lib.mx_quantize_e2m1(C, 1, rows, cols, None, C, None), UNSUPPORTED, "cols must be at most")
             _says(lib.mx_dequantize_e2m1(None, C, 0, rows, cols, C, None), UNSUPPORTED, "cols must be at most")
+
+
+def test_norm_takes_every_finite_eps():
+    lib = _lib()
+    for eps in (0.0, 1e-45, 1e30, 2e30, 3.4028234e38):
+        assert lib.moe_rmsnorm_fwd(None, None, None, 0, 64, eps, 1, None, None, None, None, None, None) == 0
+    for eps in (-1e-45, float("inf"), float("nan")):
+        _says(lib.moe_rmsnorm_fwd(None, None, None, 0, 64, eps, 1, None, None, None, None, None, None), INVALID, "eps")

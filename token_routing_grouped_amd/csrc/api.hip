@@ -2,6 +2,7 @@
 // checks, error reporting, and the launches.  Every entry point only enqueues
 // work on the caller's stream; none copies device data to the host or
 // synchronises (the routing metadata never leaves the GPU).
+#include <float.h>
 #include <stdarg.h>
 #include <stdio.h>
 #include <string.h>
@@ -678,7 +679,7 @@ moe_status_t moe_rmsnorm_fwd(const void* x, const void* res, const void* w, int 
                              void* y, uint8_t* q, uint8_t* qs, float* rstd, void* stream) {
   const char* fn = "moe_rmsnorm_fwd";
   TRY(check_norm_dims(fn, T, d, dt));
-  if (!(eps >= 0.0f) || eps > 1e30f) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  if (!(eps >= 0.0f) || eps > FLT_MAX) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
   if (T == 0) return ok();
   if ((q == nullptr) != (qs == nullptr)) return fail(MOE_ERR_INVALID_ARG, "%s: q and qs go together", fn);
   if (y == nullptr && q == nullptr) return fail(MOE_ERR_INVALID_ARG, "%s: nothing to write (y and q are null)", fn);
