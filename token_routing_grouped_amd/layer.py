@@ -397,10 +397,12 @@ class MoEDecodeGPU:
 class MoEBlockGPU:
     """The layer with its norm, for training: s = x + res, y = layer(rmsnorm(s)).
 
-    layer: a MoELayerGPU, whose weights stay the caller's.  forward() returns y
-    and leaves the residual stream in self.s; backward() takes y's gradient and
-    the one that reaches s from further on, and returns the gradient of x and
-    res (the same tensor); the norm weight's is in self.dnorm_w.
+    layer: a MoELayerGPU of any mode, whose weights stay the caller's.  forward()
+    returns y and leaves the residual stream in self.s (forced_idx: the layer's
+    own); backward() takes y's gradient and the one that reaches s from further
+    on, and returns the gradient of x and res (the same tensor); the norm
+    weight's is in self.dnorm_w.  The layer takes the normed rows in its own
+    type, in MXFP8 too: it routes and quantises them itself.
     """
 
     def __init__(self, layer: MoELayerGPU, eps: float = 1e-6):
@@ -411,9 +413,9 @@ class MoEBlockGPU:
         self.rstd = e(T, dt=torch.float32)
         self.ws_norm = _abi.workspace(_abi.moe_rmsnorm_bwd_workspace_size(T, d), dev)
 
-    def forward(self, x, norm_w, wr, w1, w3, w2, res=None):
+    def forward(self, x, norm_w, wr, w1, w3, w2, res=None, forced_idx=None):
         _abi.moe_rmsnorm_fwd(x, norm_w, self.eps, self.xn, res=res, s=self.s, rstd=self.rstd)
-        return self.layer.forward(self.xn, wr, w1, w3, w2)
+        return self.layer.forward(self.xn, wr, w1, w3, w2, forced_idx)
 
     def backward(self, dy, norm_w, wr, w1, w3, w2, ds=None):
         dxn = self.layer.backward(dy, self.xn, wr, w1, w3, w2)
