@@ -497,8 +497,12 @@ moe_status_t moe_grouped_gemm_recompute_gu_mx(const moe_mx_fwd_args* args, void*
  *   q, qs (nullable, together; d a multiple of 32): y's MXFP8 copy, rowwise,
  *       in mx_quantize's encoding and layout (q [T,d]; qs ceil(d/128) * T * 4
  *       bytes, 4-byte aligned, places past the last block 0), taken from the
- *       fp32 values; a NaN keeps the NaN code.  It feeds the scaled grouped
- *       GEMMs as xq / xs.
+ *       fp32 values; a NaN keeps the NaN code.  As xq / xs of the scaled
+ *       grouped GEMMs these are rows in the order of the experts' segments, so
+ *       it stands there only where that is the tokens' order: one expert with
+ *       all the rows (E = 1, R = T; a dense FFN), forward.  For routed rows,
+ *       and for the columnwise copies of the backward, mx_quantize gathers
+ *       from y.
  *   rstd (nullable): [T] f32, for the backward.
  * w [d] dt.  eps finite and >= 0.  s may be x or res, and y may be x or res if
  * s is neither the same buffer; nothing else may overlap.  T = 0 writes
