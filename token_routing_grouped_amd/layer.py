@@ -376,7 +376,8 @@ class MoEDecodeGPU:
         """y [t,d] of x [t,d], t <= T, in self.y (with topk_idx, topk_w and,
         with norm_w, the residual stream x + res in self.s).  n_live: a device
         int32 with the number of tokens that are there; rows of y, topk_idx
-        and topk_w behind them are left as they were."""
+        and topk_w behind them are left as they were.  The norm takes all t
+        rows, so self.s is written for all of them; res may be self.s."""
         t = x.shape[0]
         if t > self.T:
             raise _abi.MoeError(f"{t} tokens, but the buffers are for {self.T}")
