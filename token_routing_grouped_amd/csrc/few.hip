@@ -1184,12 +1184,36 @@ size_t lds_bytes(int waves, int tiles) {
   return (size_t)waves * (WT == kE2M1 ? kStage : tiles * 1024);
 }
 
+// Which of its launches' variants a call takes.
+FewPlan few_plan_of(int T, int d, int E, int k, int h, int wt) {
+  const int xe = wt == kF32 ? 4 : 2, xb = d * xe;
+  // bytes of a weight row
+  const int rb1 = wt == kE2M1 ? d / 2 : xb, rb2 = wt == kE2M1 ? h / 2 : h * xe;
+  const long slots = slots_of(T, E, k), up_tiles = slots * ((h + 15) / 16), down_tiles = slots * ((d + 15) / 16);
+  FewPlan p;
+  p.pro = in_prologue(T, E, k, h);
+  p.router = p.pro && E <= 16 && E * xb <= kProRouter;
+  p.logit_tiles = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  p.epl = p.router ? 1 : E <= 64 && !p.pro ? 1 : E <= 128 ? 2 : E <= 512 ? 8 : 16;
+  // two row tiles a wave would leave CUs idle where there are few; 4-bit rows' staging and accumulators leave
+  // no registers for a second one
+  p.up_rows = p.pro || wt == kE2M1 || up_tiles < 1024 ? 1 : 2;
+  p.up_waves = p.pro ? kWaves : row_waves(rb1, up_tiles);
+  // Four row tiles a wave read the operand once for 64 rows; with few tiles that
+  // leaves CUs idle.  Measured with 1 / 2 / 4 a wave, 8 experts: 64 tokens 65.7 /
+  // 60.8 / 65.0 us in bf16 and 46.5 / 44.2 / 49.0 in 4 bits, 16 tokens 36.7 / 35.6 /
+  // 36.1; 128 experts, 61 tokens in 4 bits (4 a wave) 100, no more than 1 % apart.
+  p.down_rows = down_tiles < 4096 ? 2 : 4;
+  p.down_waves = row_waves(rb2, down_tiles);
+  return p;
+}
+
 template <int WT>
 hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   constexpr int XE = WT == kF32 ? 4 : 2;
   const FewLayout l = few_layout(a.T, a.d, a.E, a.k, a.h);
+  const FewPlan p = few_plan_of(a.T, a.d, a.E, a.k, a.h, WT);
   char* ws = (char*)a.ws;
-  const bool pro = in_prologue(a.T, a.E, a.k, a.h);
   int* n_active = (int*)(ws + l.n_active);
   FewSlot* slots = (FewSlot*)(ws + l.slots);
   mask_t* masks = (mask_t*)(ws + l.masks);
@@ -1200,24 +1224,23 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   const int slots_max = slots_of(a.T, a.E, a.k);
   const long hid_n = (long)hid_rows(a.T, a.E, a.k, a.h) * a.h;
   const int xb = a.d * XE;
-  const bool router = pro && a.E <= 16 && a.E * xb <= kProRouter;
   const int parts = logit_parts(xb);
   hipError_t e = hipSuccess;
-  if (!router) {
+  if (!p.router) {
     constexpr int RT = WT == kF32 ? kF32 : kBF16;
 #define TRG_LOGITS(NT) \
   linear_nt<RT, 1, NT, 1, 1, kWaves, float>(a.x, a.wr, nullptr, a.T, a.E, xb, xb, parts, a.n_live, logits, st, \
-                                                masks, pro ? 0 : a.E)
-    e = a.T <= 16 ? TRG_LOGITS(1) : a.T <= 32 ? TRG_LOGITS(2) : TRG_LOGITS(4);
+                                                masks, p.pro ? 0 : a.E)
+    e = p.logit_tiles == 1 ? TRG_LOGITS(1) : p.logit_tiles == 2 ? TRG_LOGITS(2) : TRG_LOGITS(4);
 #undef TRG_LOGITS
     if (e != hipSuccess) return e;
   }
-  if (!pro) {
+  if (!p.pro) {
 #define TRG_ROUTE(N)                                                                                                  \
   few_route_kernel<N><<<a.T, 64, 0, st>>>(logits, parts, a.T, a.E, a.k, a.n_live, a.topk_idx, a.topk_w, masks, entries)
-    if (a.E <= 64) TRG_ROUTE(1);
-    else if (a.E <= 128) TRG_ROUTE(2);
-    else if (a.E <= 512) TRG_ROUTE(8);
+    if (p.epl == 1) TRG_ROUTE(1);
+    else if (p.epl == 2) TRG_ROUTE(2);
+    else if (p.epl == 8) TRG_ROUTE(8);
     else TRG_ROUTE(16);
 #undef TRG_ROUTE
     e = hipGetLastError();
@@ -1226,19 +1249,18 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   // bytes of a weight row
   const int rb1 = WT == kE2M1 ? a.d / 2 : a.d * XE, rb2 = WT == kE2M1 ? a.h / 2 : a.h * XE;
   constexpr int U = WT == kE2M1 ? 1 : 2, UP = WT == kE2M1 ? 1 : 4;  // lines at a time
-  constexpr int UR = WT == kE2M1 ? 1 : 2;                             // row tiles a wave
-  const long up_tiles = (long)slots_max * ((a.h + 15) / 16), down_tiles = (long)slots_max * ((a.d + 15) / 16);
-  const int uw = pro ? kWaves : row_waves(rb1, up_tiles), dw = row_waves(rb2, down_tiles);
+  constexpr int UR = WT == kE2M1 ? 1 : 2;                             // row tiles a wave, at most
+  const int uw = p.up_waves, dw = p.down_waves;
 #define TRG_UP(RM, U, EPL, PRO, ROUTER)                                                                             \
   few_up_kernel<WT, RM, U, EPL, PRO, ROUTER>                                                                       \
       <<<(unsigned)slots_max * ((a.h + 16 * RM - 1) / (16 * RM)), uw * 64, lds_bytes<WT>(uw, 2), st>>>(            \
           (const char*)a.x, xb, a.w1, a.w1s, a.w3, a.w3s, a.wr, a.T, a.E, a.k, a.h, rb1, logits, parts, a.n_live,  \
           a.topk_idx, a.topk_w, n_active, slots, masks, entries, hid, hid_n)
-  if (!pro && (UR == 1 || up_tiles < 1024)) TRG_UP(1, U, 1, false, false);  // two a wave would leave CUs idle
-  else if (!pro) TRG_UP(UR, U, 1, false, false);
-  else if (router) TRG_UP(1, UP, 1, true, true);
-  else if (a.E <= 128) TRG_UP(1, UP, 2, true, false);
-  else if (a.E <= 512) TRG_UP(1, UP, 8, true, false);
+  if (!p.pro && p.up_rows == 1) TRG_UP(1, U, 1, false, false);
+  else if (!p.pro) TRG_UP(UR, U, 1, false, false);
+  else if (p.router) TRG_UP(1, UP, 1, true, true);
+  else if (p.epl == 2) TRG_UP(1, UP, 2, true, false);
+  else if (p.epl == 8) TRG_UP(1, UP, 8, true, false);
   else TRG_UP(1, UP, 16, true, false);
 #undef TRG_UP
   e = hipGetLastError();
@@ -1247,21 +1269,17 @@ hipError_t few_any(const moe_few_args& a, hipStream_t st) {
   few_down_kernel<WT, U, KS><<<(a.d + 16 / KS - 1) / (16 / KS), kThreads, 0, st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, \
                                                                                    a.h, rb2, n_active, slots,       \
                                                                                    slots_max, a.T, a.n_live, a.y)
-  if (pro) {
+  if (p.pro) {
     if (a.T <= 4) TRG_DOWN(4);
     else TRG_DOWN(2);
     return hipGetLastError();
   }
 #undef TRG_DOWN
-  // Four row tiles a wave read the operand once for 64 rows; with few tiles that
-  // leaves CUs idle.  Measured with 1 / 2 / 4 a wave, 8 experts: 64 tokens 65.7 /
-  // 60.8 / 65.0 us in bf16 and 46.5 / 44.2 / 49.0 in 4 bits, 16 tokens 36.7 / 35.6 /
-  // 36.1; 128 experts, 61 tokens in 4 bits (4 a wave) 100, no more than 1 % apart.
 #define TRG_ROWS(RM, U)                                                                                             \
   few_down_rows_kernel<WT, RM, U><<<(unsigned)slots_max * ((a.d + 16 * RM - 1) / (16 * RM)), 64 * dw,               \
                                     lds_bytes<WT>(dw, 1), st>>>(hid, hid_n, a.w2, a.w2s, a.E, a.d, a.h, rb2, masks, \
                                                                 entries, yp)
-  if (down_tiles < 4096) TRG_ROWS(2, 1);
+  if (p.down_rows == 2) TRG_ROWS(2, 1);
   else TRG_ROWS(4, 1);
 #undef TRG_ROWS
   e = hipGetLastError();
@@ -1292,14 +1310,17 @@ hipError_t launch_few_fwd(const moe_few_args& a, hipStream_t st) {
   return few_any<kF32>(a, st);
 }
 
-hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
-                              hipStream_t st) {
-  // Row tiles a wave: more read the tokens' operand fewer times, fewer leave less
-  // of the chip idle at the end.  The model: a workgroup costs its row tiles plus
-  // the staging of its column tiles, a CU does ceil(workgroups / 256) of them.
-  // Measured, 24576 x 6144 (1536 tiles), with 1 / 2 / 3 / 4 row tiles: 13 tokens
-  // 22.4 / 17.1 / 16.5 / 20.2 us, 32 tokens 34.7 / 29.7 / 26.2 / 30.6, 64 tokens
-  // 60.8 / 47.2 / 37.8 / 57.6; 6144 x 2048, 64 tokens 9.9 / 8.1 / 9.5 / 12.9.
+FewPlan few_plan(int T, int d, int E, int k, int h, int wt) {
+  return few_plan_of(T, d, E, k, h, wt == MOE_E2M1 ? kE2M1 : wt == MOE_BF16 ? kBF16 : kF32);
+}
+
+// Row tiles a wave: more read the tokens' operand fewer times, fewer leave less
+// of the chip idle at the end.  The model: a workgroup costs its row tiles plus
+// the staging of its column tiles, a CU does ceil(workgroups / 256) of them.
+// Measured, 24576 x 6144 (1536 tiles), with 1 / 2 / 3 / 4 row tiles: 13 tokens
+// 22.4 / 17.1 / 16.5 / 20.2 us, 32 tokens 34.7 / 29.7 / 26.2 / 30.6, 64 tokens
+// 60.8 / 47.2 / 37.8 / 57.6; 6144 x 2048, 64 tokens 9.9 / 8.1 / 9.5 / 12.9.
+int linear_row_tiles(int T, int n) {
   const long tiles = (n + 15) / 16;
   const int nt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
   int nm = 1;
@@ -1311,6 +1332,12 @@ hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s,
       nm = m;
     }
   }
+  return nm;
+}
+
+hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
+                              hipStream_t st) {
+  const int nt = T <= 16 ? 1 : T <= 32 ? 2 : 4, nm = linear_row_tiles(T, n);
 #define TRG_LINEAR(NM, NT, XN) \
   linear_nt<kE2M1, NM, NT, 1, XN, kWaves, uint16_t>(x, q, s, T, n, K / 2, K * 2, 1, nullptr, (uint16_t*)y, st)
 #define TRG_NT(NM)                                                                                           \

@@ -53,6 +53,14 @@ hipError_t launch_rmsnorm_bwd(const void* dy, const void* ds, const void* s, con
 // the layer for a few tokens, and 4-bit weights
 size_t few_ws_bytes(int T, int d, int E, int k, int h);        // of a call with T tokens
 size_t few_ws_bytes_up_to(int T, int d, int E, int k, int h);  // of every call with 0 to T tokens
+// Which variants of its launches a call takes: routing in the up projection's prologue, and the logits there
+// too; column tiles of the logits' launch; experts a lane of the routing; row tiles a wave and waves a row tile of
+// the up projection, and (not after a prologue) of the down projection.  wt: MOE_F32, MOE_BF16 or MOE_E2M1.
+struct FewPlan {
+  int pro, router, logit_tiles, epl, up_rows, up_waves, down_rows, down_waves;
+};
+FewPlan few_plan(int T, int d, int E, int k, int h, int wt);
+int linear_row_tiles(int T, int n);  // row tiles a wave of launch_linear_e2m1
 hipError_t launch_few_fwd(const moe_few_args& a, hipStream_t st);
 hipError_t launch_quantize_e2m1(const void* in, bool bf16, int rows, int cols, uint8_t* q, uint8_t* s, hipStream_t st);
 hipError_t launch_dequantize_e2m1(const uint8_t* q, const uint8_t* s, bool bf16, int rows, int cols, void* out,
