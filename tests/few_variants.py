@@ -105,6 +105,6 @@ PRO = [(wt, T, d, E, k, h) for wt in WT for T, d, E, k, h in
        [(1, 160, 130, 4, 160), (7, 288, 300, 8, 96), (3, 96, 600, 5, 96), (8, 160, 1000, 8, 96), (4, 160, 512, 8, 224),
         (5, 288, 513, 6, 224), (8, 160, 16, 3, 160), (3, 160, 9, 4, 96), (3, 2080, 16, 4, 96), (6, 160, 40, 5, 96), (2, 96, 128, 12, 288)]]
 
-# n for 1, 2, 3 and 4 row tiles a wave (none a multiple of 16 of them) by T
+# n for 1, 2, 3 and 4 (to 32 tokens) row tiles a wave, none a multiple of 16 of them
 LINEAR_T = (1, 4, 5, 13, 17, 32, 33, 64)
 LINEAR_N = (4090, 4117, 6140, 8209, 10007, 12310, 16391, 20491, 24571, 40933)

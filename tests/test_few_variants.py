@@ -79,4 +79,10 @@ def test_every_row_and_column_tile_count_of_the_dense_product_has_a_shape():
             if n % (16 * m):
                 rows.setdefault(cols, set()).add(m)
     reach = {T: {fv.linear_row_tiles(T, n) for n in range(1, 70000, 16)} for T in (1, 13, 17, 64)}
-    assert rows == {4: reach[1], 16: reach[13], 32: reach[17], 64: reach[64]} and all(len(v) == 4 for v in rows.values())
+    assert rows == {4: reach[1], 16: reach[13], 32: reach[17], 64: reach[64]}
+    assert rows[4] == rows[16] == rows[32] == {1, 2, 3, 4}
+
+
+def test_no_four_row_tiles_with_four_column_tiles():
+    """Their accumulators and operands do not fit into the registers."""
+    assert {fv.linear_row_tiles(T, n) for T in (33, 48, 64) for n in range(16, 1 << 18, 16)} == {1, 2, 3}

@@ -1316,16 +1316,23 @@ FewPlan few_plan(int T, int d, int E, int k, int h, int wt) {
 
 // Row tiles a wave: more read the tokens' operand fewer times, fewer leave less
 // of the chip idle at the end.  The model: a workgroup costs its row tiles plus
-// the staging of its column tiles, a CU does ceil(workgroups / 256) of them.
-// Measured, 24576 x 6144 (1536 tiles), with 1 / 2 / 3 / 4 row tiles: 13 tokens
-// 22.4 / 17.1 / 16.5 / 20.2 us, 32 tokens 34.7 / 29.7 / 26.2 / 30.6, 64 tokens
-// 60.8 / 47.2 / 37.8 / 57.6; 6144 x 2048, 64 tokens 9.9 / 8.1 / 9.5 / 12.9.
+// the staging of its column tiles, a CU does ceil(workgroups / 256) of them.  It
+// orders the counts by their rounds and is no estimate of the times.  Four row
+// tiles are left out above 32 tokens: with four column tiles their accumulators
+// spill 42 registers.  Measured in us, K = 6144, with 1 / 2 / 3 / 4 row tiles:
+//   n       13 tokens                 32                        64
+//   24576   22.3 / 18.7 / 17.4 / 25.7 37.1 / 35.6 / 27.5 / 32.6 75.8 / 51.4 / 44.3 / 79.3
+//   28672   31.4 / 26.4 / 25.8 / 27.5 50.6 / 45.4 / 42.3 / 34.6 96.6 / 69.8 / 61.5 / 84.3
+//   32768   37.3 / 31.0 / 29.9 / 31.6 59.7 / 49.5 / 45.3 / 38.2 111 / 73.6 / 64.9 / 87.4
+//   40960   47.0 / 39.1 / 37.0 / 47.5 75.5 / 61.5 / 59.4 / 53.9 140 / 90.8 / 85.6 / 129
+// and 6144 x 2048, 64 tokens 11.8 / 8.6 / 10.0 / 15.9.  The rule takes the fastest
+// of them but for 13 tokens with n = 28672 and 32768 (four, 7 % slower than three).
 int linear_row_tiles(int T, int n) {
   const long tiles = (n + 15) / 16;
   const int nt = T <= 16 ? 1 : T <= 32 ? 2 : 4;
   int nm = 1;
   long best = 0;
-  for (int m = 1; m <= 4; ++m) {
+  for (int m = 1; m <= (nt == 4 ? 3 : 4); ++m) {
     const long cost = ((tiles + m - 1) / m + 255) / 256 * (m + nt);
     if (m == 1 || cost < best) {
       best = cost;
@@ -1340,13 +1347,13 @@ hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s,
   const int nt = T <= 16 ? 1 : T <= 32 ? 2 : 4, nm = linear_row_tiles(T, n);
 #define TRG_LINEAR(NM, NT, XN) \
   linear_nt<kE2M1, NM, NT, 1, XN, kWaves, uint16_t>(x, q, s, T, n, K / 2, K * 2, 1, nullptr, (uint16_t*)y, st)
-#define TRG_NT(NM)                                                                                           \
-  return T <= 4 ? TRG_LINEAR(NM, 1, 2) : nt == 1 ? TRG_LINEAR(NM, 1, 8) : nt == 2 ? TRG_LINEAR(NM, 2, 8) \
-                                                                                  : TRG_LINEAR(NM, 4, 8)
-  if (nm == 1) TRG_NT(1);
-  if (nm == 2) TRG_NT(2);
-  if (nm == 3) TRG_NT(3);
-  TRG_NT(4);
+#define TRG_NT(NM) \
+  if (nm == NM) return T <= 4 ? TRG_LINEAR(NM, 1, 2) : nt == 1 ? TRG_LINEAR(NM, 1, 8) : TRG_LINEAR(NM, 2, 8)
+  if (nt == 4) return nm == 1 ? TRG_LINEAR(1, 4, 8) : nm == 2 ? TRG_LINEAR(2, 4, 8) : TRG_LINEAR(3, 4, 8);
+  TRG_NT(1);
+  TRG_NT(2);
+  TRG_NT(3);
+  return T <= 4 ? TRG_LINEAR(4, 1, 2) : nt == 1 ? TRG_LINEAR(4, 1, 8) : TRG_LINEAR(4, 2, 8);
 #undef TRG_LINEAR
 #undef TRG_NT
 }
