@@ -237,3 +237,35 @@ def test_quantize_four_pieces_a_thread(rows, cols, dt):
         got = out[r0:r1].cpu()
         assert torch.equal(got.isnan(), want.isnan())
         assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(want))
+
+
+@pytest.mark.parametrize("wt,T,E", [("bf16", 3, 12), ("e2m1", 3, 40), ("f32", 20, 12), ("e2m1", 20, 40)])
+def test_layer_without_the_routing_outputs(wt, T, E):
+    """topk_idx and topk_w are optional; y is the same without them."""
+    c = Layer(wt, T, 288, E, 3, 160)
+    want = c.m.forward(c.x).clone()
+    y = torch.full_like(want, 7)
+    _abi().moe_few_fwd(c.m._args, c.x, y)
+    assert torch.equal(y, want)
+
+
+@pytest.mark.parametrize("T,E", [(3, 12), (3, 40), (20, 40), (64, 6)])
+def test_faulty_4bit_expert_reaches_only_its_tokens(T, E):
+    """A scale byte of 255 (NaN) or 254 (infinite sums) in one expert's matrices."""
+    c = Layer("e2m1", T, 288, E, 2, 160)
+    y0 = c.m.forward(c.x).clone()
+    idx = c.m.topk_idx.clone()
+    e = int(idx[0, 0])
+    hit = (idx == e).any(1)
+    assert hit.any() and not hit.all()
+    for i in range(3):
+        for byte in (255, 254):
+            s = c.w[i][1]
+            old = s[0, e, 7].clone()
+            s[0, e, 7, 1] = byte  # block 1 of the expert's row 7
+            y = c.m.forward(c.x).clone()
+            s[0, e, 7] = old
+            assert torch.equal(y[~hit], y0[~hit])
+            if byte == 255:
+                assert not torch.isfinite(y[hit]).all(1).any()
+    assert torch.equal(c.m.forward(c.x), y0)
