@@ -24,8 +24,10 @@
 // fp32 accumulation throughout.  The hidden vector h (gate included) is kept
 // for the second product as two bf16 halves, hi = bf16(h) and lo = bf16(h -
 // hi): 16 mantissa bits, so its rounding is far below y's own; a second matrix
-// instruction is free next to the weight stream.  fp32 weights use the fp32
-// matrix instruction and h stays fp32.
+// instruction is free next to the weight stream.  Measured, 24 tokens, 384
+// experts: 0.3 % of the bf16 outputs round to the neighbour of what an fp32 h
+// gives, and the error against 64 bits is the same, 1.6615e-3 of y's norm with
+// either.  fp32 weights use the fp32 matrix instruction and h stays fp32.
 //
 // Launches (in_prologue has the rule):
 //   a token or a few, few experts  router logits; up projection, which routes in
@@ -514,9 +516,11 @@ TRG_DEV int live_tokens(const int* n_live, int T) { return n_live != nullptr ? m
 // lines from blockIdx.y * part_lines and writes its own [T, n] of out.  The first
 // one also clears the nz masks that the next launch sets.
 // 4 bits, 24576 x 6144 (80 MB, HBM-bound; decoding and the operand's way through
-// LDS take their share of the issue slots): one token 14.3 us, 5.5 TB/s, 13
-// tokens 16.9, 4.8, 64 tokens 38.  Logits of 61 tokens, 128 experts, d = 2048:
-// 5.2 us, latency.
+// LDS take their share of the issue slots): one token 14.5 us, 5.5 TB/s, 13
+// tokens 17 to 19 (by the card), 4.3 to 4.8 TB/s.  Above 16 tokens each of the 8
+// waves stages its own line for every column tile, and a staged byte serves only
+// that wave's rows: 32 tokens 27.5 us, 64 tokens 44, for 13 of bytes.  Logits of 61
+// tokens, 128 experts, d = 2048: 5.2 us, latency.
 template <int WT, int NM, int NT, int U, int XN, int WAVES, class OUT>
 __global__ __launch_bounds__(WAVES * 64, NT > 1 && NM* NT > 3 ? 2 : 4) void few_linear_kernel(
     const char* __restrict__ x, const void* __restrict__ w, const uint8_t* __restrict__ ws, int T, int n, int rb,
@@ -801,8 +805,11 @@ constexpr int kProRouter = 65536;  // bytes of router weights that a prologue re
 // reads).
 // Measured: bf16, 24 tokens, d = 6144, 384 experts, h = 2048 1228 us, 6.2 TB/s,
 // HBM's read rate; 4 bits, 61 tokens, d = 2048, 128 experts, h = 1024 47.7 us, 5.1
-// TB/s: rows of 1 KB are four loads a wave.  One token, 4 experts of 8, bf16 12.8
-// us for 5.3 us of bytes: the router and the choice come before the first load.
+// TB/s: rows of 1 KB are four loads a wave.  One token, 4 experts of 8, bf16 12.7
+// to 13.4 us for 5.3 us of bytes: the router and the choice come before the first
+// load.  64 tokens, 8 experts (32 an expert): bf16 24.7 us, 2.8 TB/s, the tokens'
+// operand as many bytes through the caches as the weights; 4 bits 16.6 us for 2.9
+// of bytes, the codes read and decoded again for every 16 tokens.
 template <int WT, int RM, int U, int EPL, bool PRO, bool ROUTER>
 __global__ __launch_bounds__(kThreads, 4) void few_up_kernel(
     const char* __restrict__ x, int xb, const void* __restrict__ w1, const uint8_t* __restrict__ w1s,
@@ -1035,9 +1042,10 @@ __global__ __launch_bounds__(kThreads, 4) void few_down_kernel(const char* __res
 // instructions and operand reads of two passes over the columns.  4-bit weights,
 // 61 tokens, 128 experts: 32.0 -> 29.9 us; bf16, whose reads set the pace, no
 // different, so it keeps the one form.
-// Measured: bf16, 24 tokens, 384 experts, d = 6144, h = 2048 620 us, 6.2 TB/s; 4
-// bits, 61 tokens, 128 experts, d = 2048, h = 1024 29.3 us, 4.1 TB/s: a row is 512
-// bytes, so a workgroup's life is one trip to memory.
+// Measured: bf16, 24 tokens, 384 experts, d = 6144, h = 2048 621 us, 6.2 TB/s; 4
+// bits, 61 tokens, 128 experts, d = 2048, h = 1024 29.4 us, 4.1 TB/s (4.5 with the
+// hidden vector): a row is 512 bytes, so a workgroup's life is one trip to memory.
+// 64 tokens, 8 experts: bf16 18.3 us, 4 bits 14.4, for the up projection's reasons.
 template <int WT, int RM, int NT, int U, int XN, int H>
 TRG_DEV void down_tile(const char* __restrict__ hid, long hid_n, const WBase* wb, int rb, int ent, int cnt, int col0,
                        int row0, int d, int h, int wk, int kw, char* lds, float* __restrict__ yp) {
@@ -1194,15 +1202,18 @@ FewPlan few_plan_of(int T, int d, int E, int k, int h, int wt) {
   p.pro = in_prologue(T, E, k, h);
   p.router = p.pro && E <= 16 && E * xb <= kProRouter;
   p.logit_tiles = T <= 16 ? 1 : T <= 32 ? 2 : 4;
+  // 129 to 256 experts take the next width's 8 a lane: 4 would save 0.2 to 1.3 us of 18 to 81 (256 experts, 1 to
+  // 40 tokens)
   p.epl = p.router ? 1 : E <= 64 && !p.pro ? 1 : E <= 128 ? 2 : E <= 512 ? 8 : 16;
   // two row tiles a wave would leave CUs idle where there are few; 4-bit rows' staging and accumulators leave
   // no registers for a second one
   p.up_rows = p.pro || wt == kE2M1 || up_tiles < 1024 ? 1 : 2;
   p.up_waves = p.pro ? kWaves : row_waves(rb1, up_tiles);
   // Four row tiles a wave read the operand once for 64 rows; with few tiles that
-  // leaves CUs idle.  Measured with 1 / 2 / 4 a wave, 8 experts: 64 tokens 65.7 /
-  // 60.8 / 65.0 us in bf16 and 46.5 / 44.2 / 49.0 in 4 bits, 16 tokens 36.7 / 35.6 /
-  // 36.1; 128 experts, 61 tokens in 4 bits (4 a wave) 100, no more than 1 % apart.
+  // leaves CUs idle.  Measured, us a call with 1 / 2 / 4 a wave, 8 experts (2 taken):
+  // 64 tokens 58.4 / 51.3 / 54.5 in bf16 and 41.0 / 39.1 / 40.5 in 4 bits, 16 tokens
+  // 37.1 / 36.2 / 36.6 and 21.5 / 22.8 / 23.6; 128 experts, 61 tokens (4 taken) 287 /
+  // 260 / 262 and 98.9 / 92.5 / 88.4.
   p.down_rows = down_tiles < 4096 ? 2 : 4;
   p.down_waves = row_waves(rb2, down_tiles);
   return p;

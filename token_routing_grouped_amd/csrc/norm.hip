@@ -46,7 +46,7 @@ TRG_DEV float row_sum(float v, float* red, int wave_in_row) {
 
 // E8M0 exponent and E4M3 codes: s = clamp(floor(log2 amax) - 8, -127, 127)
 // from the exponent bits; elements are divided by 2^s (an exact multiplication
-// by 2^-s; s never exceeds 119, so 2^-s is normal or, at s = -127, 2^127),
+// by 2^-s; s is at most 120, so 2^-s is normal or, at s = -127, 2^127),
 // clamped to +-448 and rounded to nearest even.  NaN keeps the NaN code: the
 // clamp alone would turn it into a number.
 TRG_DEV int norm_scale_exp(float amax) {
@@ -286,7 +286,11 @@ __global__ __launch_bounds__(1024) void rmsnorm_dw_kernel(const float* __restric
 
 // Rows' shape: waves a row and pieces a lane that hold d elements.  The backward
 // keeps three inputs, the weight and the gradient's sums of a lane's columns,
-// so more waves beat more pieces (at 16 x 8, the widest rows, it spills).
+// so more waves beat more pieces.  With 16 waves a lane has 128 registers, and the
+// backward's rows over 32 KiB in bf16 do not fit: 4 pieces spill 97, 8 spill 398
+// (fp32: 4 and 186).  Measured, backward with ds, 64 MiB a matrix: bf16 d = 16384 63
+// us, 4.2 TB/s; 16392 (16 x 4) 220, 1.2; 65536 (16 x 8) 440, 0.6; fp32 16384 67, 4.0;
+// 32768 165, 1.6.  The forward has no such step: 4.2 to 5.1 TB/s at all of them.
 struct RowShape {
   int wpr, np;
 };
