@@ -593,6 +593,77 @@ typedef struct {
 size_t moe_few_workspace_size(int T, int d, int E, int k, int h);
 moe_status_t moe_few_fwd(const moe_few_args* args, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Dense products beside the experts, and their gradients.  x [T,K], w [n,K]
+ * (output-major, as the experts' weights), y, z, res, dy [T,n], bias [n].
+ * ---------------------------------------------------------------------------
+ * moe_linear_fwd: z = x w^T + bias,  y = act(z) + res, in fp32 and rounded once
+ *   per output.  bias, res and z (what the backward needs of an activation) may
+ *   be null.  y may be res; nothing else may overlap an output.
+ *   MOE_ACT_GELU is z Phi(z) with the error function, MOE_ACT_SILU z sigmoid(z).
+ * moe_linear_bwd: from dy (res's gradient is dy itself) and the stored z (null
+ *   with MOE_ACT_NONE),
+ *     dz = dy act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum_t dz
+ *   relu's slope at 0 is 0.  With an activation dz is rounded to dt once before
+ *   the two products (dbias is summed from the unrounded values); sums are fp32,
+ *   in a fixed order.  dx, dw and dbias may each be null (not computed); w is
+ *   needed for dx, x for dw.  T = 0 gives dw = 0 and dbias = 0.
+ * n and K at most 2^20; (T/128 + 1) * (max(n,K)/128 + 1) < 2^27.
+ * ws: moe_linear_workspace_size / moe_linear_bwd_workspace_size bytes for these
+ * sizes exactly (a smaller T may need more); calls that may run concurrently
+ * need separate workspaces.
+ */
+enum { MOE_ACT_NONE = 0, MOE_ACT_RELU = 1, MOE_ACT_GELU = 2, MOE_ACT_SILU = 3 };
+size_t moe_linear_workspace_size(int T, int n, int K, int dt);
+moe_status_t moe_linear_fwd(const void* x, const void* w, const void* bias, const void* res, int T, int n, int K,
+                            int act, int dt, void* z, void* y, void* ws, size_t ws_bytes, void* stream);
+size_t moe_linear_bwd_workspace_size(int T, int n, int K, int dt);
+moe_status_t moe_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int T, int n, int K, int act,
+                            int dt, void* dx, void* dw, void* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * ---------------------------------------------------------------------------
+ * Orthogonalised weight update (the JUPITER article's optimizer step, whose
+ * Newton-Schulz iteration runs on the GPU) for a batch of B matrices
+ * [rows, cols], e.g. the experts' dw1 [E,h,d].
+ * ---------------------------------------------------------------------------
+ * moe_orthogonalize: every matrix by itself,
+ *     X = g / (|g|_F + eps);  `steps` times  X <- a X + (b A + c A^2) X,
+ *     A = X X^T (X^T X where rows > cols),  (a, b, c) = (3.4445, -4.7750, 2.0315)
+ *   which moves the singular values towards 1; out [B,rows,cols] dt.  dt MOE_BF16:
+ *   the iterates are kept in fp16 (11 bits), sums in fp32; dt MOE_F32: in pairs
+ *   of fp16 (22 bits).  A singular value below about 2^-11 (2^-22) of |g|_F is
+ *   thus lost in the others' rounding.  A zero matrix gives zeros; one that
+ *   holds an infinity or NaN gives NaNs, and no other is touched.  |g|_F is
+ *   summed in 64 bits.  out may be g.
+ * moe_muon_step: momentum, orthogonalisation and the weights' step,
+ *     buf_out = momentum buf + g
+ *     u = g + momentum buf_out (nesterov != 0) or buf_out
+ *     w_out = w (1 - s decay) - s step orthogonalize(u)
+ *   w, w_out and g are dt, buf and buf_out fp32.  master, master_out (nullable,
+ *   together): the weights in fp32; then w_out is master_out rounded, and w is
+ *   not read.  s = *lr_scale, read on the device (1 if null), so that one
+ *   captured step serves a schedule.  w_out, buf_out and master_out may each be
+ *   its own input; nothing else may overlap.
+ * rows, cols at most 2^20; steps 1 to 32; eps finite and >= 0.
+ * ws: moe_orthogonalize_workspace_size(B, rows, cols, dt) bytes for these sizes
+ * exactly; calls that may run concurrently need separate workspaces.
+ */
+typedef struct {
+  int B, rows, cols, dt, steps, nesterov;
+  float eps, momentum, step, decay;
+  const void* w; const void* g; const float* buf; const float* master;
+  const float* lr_scale;
+  void* w_out; float* buf_out; float* master_out;
+  void* ws; size_t ws_bytes;
+} moe_muon_args;
+
+size_t moe_orthogonalize_workspace_size(int B, int rows, int cols, int dt);
+moe_status_t moe_orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, void* out,
+                               void* ws, size_t ws_bytes, void* stream);
+moe_status_t moe_muon_step(const moe_muon_args* args, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

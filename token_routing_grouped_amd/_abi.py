@@ -70,6 +70,13 @@ _SIGS = {
     "mx_linear_e2m1": ([_P, _P, _P, _I, _I, _I, _P, _P], _I),
     "moe_few_workspace_size": ([_I, _I, _I, _I, _I], _Z),
     "moe_few_fwd": ([_P, _P], _I),
+    "moe_linear_workspace_size": ([_I, _I, _I, _I], _Z),
+    "moe_linear_fwd": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _Z, _P], _I),
+    "moe_linear_bwd_workspace_size": ([_I, _I, _I, _I], _Z),
+    "moe_linear_bwd": ([_P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _P, _P, _Z, _P], _I),
+    "moe_orthogonalize_workspace_size": ([_I, _I, _I, _I], _Z),
+    "moe_orthogonalize": ([_P, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _Z, _P], _I),
+    "moe_muon_step": ([_P, _P], _I),
 }
 
 
@@ -95,6 +102,14 @@ class FewArgs(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int) for n in ("T", "d", "E", "k", "h", "dt", "wt")] + \
         [(n, ctypes.c_void_p) for n in ("x", "wr", "w1", "w3", "w2", "w1s", "w3s", "w2s", "n_live", "y", "topk_idx",
                                         "topk_w", "ws")] + [("ws_bytes", ctypes.c_size_t)]
+
+
+class MuonArgs(ctypes.Structure):
+    """moe_muon_args (include/moe.h)."""
+    _fields_ = [(n, ctypes.c_int) for n in ("B", "rows", "cols", "dt", "steps", "nesterov")] + \
+        [(n, ctypes.c_float) for n in ("eps", "momentum", "step", "decay")] + \
+        [(n, ctypes.c_void_p) for n in ("w", "g", "buf", "master", "lr_scale", "w_out", "buf_out", "master_out", "ws")] + \
+        [("ws_bytes", ctypes.c_size_t)]
 
 
 EXPORTED = tuple(_SIGS)
@@ -625,3 +640,102 @@ def moe_few_fwd(a, x, y, topk_idx=None, topk_w=None, n_live=None):
     a.topk_w = _arg(topk_w, torch.float32, T * a.k, "topk_w", dev)
     a.n_live = _arg(n_live, torch.int32, 1, "n_live", dev)
     _check(lib().moe_few_fwd(ctypes.byref(a), _stream(dev)), "moe_few_fwd")
+
+
+# ---------------------------------------------------------------------------
+# dense products beside the experts, the orthogonalised weight update
+# ---------------------------------------------------------------------------
+
+ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3}
+
+
+def _size(nbytes: int) -> int:
+    """A workspace's size; 0 says that the sizes are refused."""
+    if nbytes == 0:
+        raise MoeError(lib().moe_last_error_string().decode())
+    return int(nbytes)
+
+
+def _dtype(dtype) -> int:
+    if dtype not in _DT:
+        raise MoeError(f"unsupported dtype {dtype}")
+    return _DT[dtype]
+
+
+def _act(act) -> int:
+    if act not in ACTS:
+        raise MoeError(f"act must be one of {', '.join(ACTS)}, got {act!r}")
+    return ACTS[act]
+
+
+def moe_linear_workspace_size(T: int, n: int, K: int, dtype) -> int:
+    return _size(lib().moe_linear_workspace_size(T, n, K, _dtype(dtype)))
+
+
+def moe_linear_bwd_workspace_size(T: int, n: int, K: int, dtype) -> int:
+    return _size(lib().moe_linear_bwd_workspace_size(T, n, K, _dtype(dtype)))
+
+
+def moe_linear_fwd(x, w, y, ws, bias=None, res=None, act="none", z=None):
+    """y [T, n] = act(x w^T + bias) + res for x [T, K], w [n, K]; z (if given)
+    receives what the activation is taken of."""
+    (T, K), (n, Kw) = _matrix(x, "x"), _matrix(w, "w")
+    if Kw != K:
+        raise MoeError(f"w must have {K} columns, got {Kw}")
+    dt, dev = x.dtype, _device(x)
+    _check(lib().moe_linear_fwd(_arg(x, dt, T * K, "x", dev), _arg(w, dt, n * K, "w", dev),
+                                _arg(bias, dt, n, "bias", dev), _arg(res, dt, T * n, "res", dev), T, n, K, _act(act),
+                                _dt(x), _arg(z, dt, T * n, "z", dev), _arg(y, dt, T * n, "y", dev), _ws_arg(ws, dev),
+                                ws.numel(), _stream(dev)), "moe_linear_fwd")
+
+
+def moe_linear_bwd(dy, x, w, ws, act="none", z=None, dx=None, dw=None, dbias=None):
+    """Gradients of moe_linear_fwd from dy [T, n] and its z: dx, dw, dbias where
+    given (res's is dy itself)."""
+    (T, K), (n, Kw) = _matrix(x, "x"), _matrix(w, "w")
+    if Kw != K:
+        raise MoeError(f"w must have {K} columns, got {Kw}")
+    dt, dev = x.dtype, _device(x)
+    _check(lib().moe_linear_bwd(_arg(dy, dt, T * n, "dy", dev), _arg(x, dt, T * K, "x", dev),
+                                _arg(w, dt, n * K, "w", dev), _arg(z, dt, T * n, "z", dev), T, n, K, _act(act), _dt(x),
+                                _arg(dx, dt, T * K, "dx", dev), _arg(dw, dt, n * K, "dw", dev),
+                                _arg(dbias, dt, n, "dbias", dev), _ws_arg(ws, dev), ws.numel(), _stream(dev)),
+           "moe_linear_bwd")
+
+
+def _batch(t, name):
+    if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
+        raise MoeError(f"{name} must be a matrix or a batch of matrices")
+    return t.shape if t.dim() == 3 else (1, *t.shape)
+
+
+def moe_orthogonalize_workspace_size(B: int, rows: int, cols: int, dtype) -> int:
+    return _size(lib().moe_orthogonalize_workspace_size(B, rows, cols, _dtype(dtype)))
+
+
+def moe_orthogonalize(g, out, ws, steps=5, eps=1e-7):
+    """out = each matrix of g [B, rows, cols] (or [rows, cols]) with its singular
+    values moved towards 1 by `steps` Newton-Schulz steps."""
+    B, rows, cols = _batch(g, "g")
+    n, dt, dev = B * rows * cols, g.dtype, _device(g)
+    _check(lib().moe_orthogonalize(_arg(g, dt, n, "g", dev), B, rows, cols, _dt(g), steps, eps,
+                                   _arg(out, dt, n, "out", dev), _ws_arg(ws, dev), ws.numel(), _stream(dev)),
+           "moe_orthogonalize")
+
+
+def moe_muon_step(w, g, buf, ws, step, decay=0.0, momentum=0.95, nesterov=True, steps=5, eps=1e-7, master=None,
+                  lr_scale=None, w_out=None, buf_out=None, master_out=None):
+    """One update of the matrices w [B, rows, cols] from their gradient g, the
+    fp32 momentum buf and (if given) fp32 master weights, in place unless *_out
+    say otherwise."""
+    B, rows, cols = _batch(w, "w")
+    n, dt, f32, dev = B * rows * cols, w.dtype, torch.float32, _device(w)
+    a = MuonArgs(B=B, rows=rows, cols=cols, dt=_dt(w), steps=steps, nesterov=1 if nesterov else 0, eps=eps,
+                 momentum=momentum, step=step, decay=decay)
+    a.w, a.g, a.buf = _arg(w, dt, n, "w", dev), _arg(g, dt, n, "g", dev), _arg(buf, f32, n, "buf", dev)
+    a.master, a.lr_scale = _arg(master, f32, n, "master", dev), _arg(lr_scale, f32, 1, "lr_scale", dev)
+    a.w_out = a.w if w_out is None else _arg(w_out, dt, n, "w_out", dev)
+    a.buf_out = a.buf if buf_out is None else _arg(buf_out, f32, n, "buf_out", dev)
+    a.master_out = a.master if master_out is None else _arg(master_out, f32, n, "master_out", dev)
+    a.ws, a.ws_bytes = _ws_arg(ws, dev), ws.numel()
+    _check(lib().moe_muon_step(ctypes.byref(a), _stream(dev)), "moe_muon_step")

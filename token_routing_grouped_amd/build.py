@@ -20,7 +20,7 @@ LIB_NAME = "libtrg_moe.so"
 LIB_PATH = os.path.join(PKG, LIB_NAME)
 
 SOURCES = ["api.hip", "route.hip", "permute.hip", "router.hip", "gemm_bf16.hip", "ggemm.hip", "ggemm_mx.hip", "mx.hip", "gemm_f32.hip", "balance.hip",
-           "norm.hip", "mx4.hip", "few.hip"]
+           "norm.hip", "mx4.hip", "few.hip", "dense.hip", "muon.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 FLAGS = [

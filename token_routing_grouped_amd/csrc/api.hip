@@ -832,4 +832,145 @@ moe_status_t moe_few_fwd(const moe_few_args* a, void* stream) {
   return hip_status(fn, trg::launch_few_fwd(*a, (hipStream_t)stream));
 }
 
+// ---- dense products and the weight update -----------------------------------
+// Row widths and matrix sides: 256 rows of a tile stay under 2^31 bytes.
+constexpr int kDenseSide = 1 << 20;
+
+static moe_status_t check_workspace(const char* fn, const void* ws, size_t have, size_t need) {
+  if (need == 0) return MOE_OK;
+  if (ws == nullptr || have < need)
+    return fail(MOE_ERR_WORKSPACE, "%s: workspace needs %zu bytes, got %zu", fn, need, have);
+  if (!aligned16(ws)) return fail(MOE_ERR_ALIGNMENT, "%s: ws is not 16-byte aligned", fn);
+  return MOE_OK;
+}
+
+static moe_status_t check_linear(const char* fn, int T, int n, int K, int dt) {
+  TRY(check_dt(fn, dt));
+  if (T < 0) return fail(MOE_ERR_INVALID_ARG, "%s: T must be >= 0", fn);
+  TRY(check_row(fn, "n", n, dt));
+  TRY(check_row(fn, "K", K, dt));
+  if (n > kDenseSide || K > kDenseSide)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: n and K must be at most %d", fn, kDenseSide);
+  // output tiles (in up to 16 parts each) and the join's threads are counted in 32 bits
+  const long side = n > K ? n : K;
+  if (((long)T / 128 + 1) * (side / 128 + 1) >= (1L << 27))
+    return fail(MOE_ERR_UNSUPPORTED, "%s: problem too large", fn);
+  return MOE_OK;
+}
+
+static moe_status_t check_act(const char* fn, int act) {
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SILU) return fail(MOE_ERR_INVALID_ARG, "%s: act must be a MOE_ACT_* value", fn);
+  return MOE_OK;
+}
+
+size_t moe_linear_workspace_size(int T, int n, int K, int dt) {
+  if (check_linear("moe_linear_workspace_size", T, n, K, dt) != MOE_OK) return 0;
+  return trg::linear_ws_bytes(T, n, K, dt) + 16;
+}
+
+moe_status_t moe_linear_fwd(const void* x, const void* w, const void* bias, const void* res, int T, int n, int K,
+                            int act, int dt, void* z, void* y, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_linear_fwd";
+  TRY(check_linear(fn, T, n, K, dt));
+  TRY(check_act(fn, act));
+  if (T == 0) return ok();
+  TRY(check_ptrs(fn, {{"x", x}, {"w", w}, {"y", y}}));
+  TRY(check_optional_aligned(fn, {{"bias", bias}, {"res", res}, {"z", z}}));
+  if (y == x || y == w || z == y) return fail(MOE_ERR_INVALID_ARG, "%s: y, x, w and z must be different buffers", fn);
+  TRY(check_workspace(fn, ws, ws_bytes, trg::linear_ws_bytes(T, n, K, dt)));
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_linear_fwd(x, w, bias, res, T, n, K, act, dt, z, y, ws, (hipStream_t)stream));
+}
+
+size_t moe_linear_bwd_workspace_size(int T, int n, int K, int dt) {
+  if (check_linear("moe_linear_bwd_workspace_size", T, n, K, dt) != MOE_OK) return 0;
+  return trg::linear_bwd_ws_bytes(T, n, K, dt) + 16;
+}
+
+moe_status_t moe_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int T, int n, int K, int act,
+                            int dt, void* dx, void* dw, void* dbias, void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_linear_bwd";
+  TRY(check_linear(fn, T, n, K, dt));
+  TRY(check_act(fn, act));
+  if (dx == nullptr && dw == nullptr && dbias == nullptr)
+    return fail(MOE_ERR_INVALID_ARG, "%s: nothing to write (dx, dw and dbias are null)", fn);
+  if (T > 0) {
+    TRY(check_ptrs(fn, {{"dy", dy}}));
+    if (dx != nullptr) TRY(check_ptrs(fn, {{"w", w}}));
+    if (dw != nullptr) TRY(check_ptrs(fn, {{"x", x}}));
+    if (act != MOE_ACT_NONE) TRY(check_ptrs(fn, {{"z", z}}));
+    if (dx != nullptr && (dx == dy || dx == w || dx == x || dx == z))
+      return fail(MOE_ERR_INVALID_ARG, "%s: dx must be a buffer of its own", fn);
+    if (dw != nullptr && (dw == dy || dw == w || dw == x || dw == z || dw == dx))
+      return fail(MOE_ERR_INVALID_ARG, "%s: dw must be a buffer of its own", fn);
+  }
+  TRY(check_optional_aligned(fn, {{"dx", dx}, {"dw", dw}, {"dbias", dbias}}));
+  TRY(check_workspace(fn, ws, ws_bytes, trg::linear_bwd_ws_bytes(T, n, K, dt)));
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_linear_bwd(dy, x, w, z, T, n, K, act, dt, dx, dw, dbias, ws, (hipStream_t)stream));
+}
+
+static moe_status_t check_matrices(const char* fn, int B, int rows, int cols, int dt) {
+  TRY(check_dt(fn, dt));
+  if (B < 0) return fail(MOE_ERR_INVALID_ARG, "%s: B must be >= 0", fn);
+  if (rows < 1) return fail(MOE_ERR_INVALID_ARG, "%s: rows must be positive", fn);
+  TRY(check_row(fn, "cols", cols, dt));
+  if (rows > kDenseSide || cols > kDenseSide)
+    return fail(MOE_ERR_UNSUPPORTED, "%s: rows and cols must be at most %d", fn, kDenseSide);
+  return MOE_OK;
+}
+
+static moe_status_t check_iteration(const char* fn, int steps, float eps) {
+  if (steps < 1 || steps > 32) return fail(MOE_ERR_INVALID_ARG, "%s: steps must be in [1, 32]", fn);
+  if (!(eps >= 0.0f) || eps > FLT_MAX) return fail(MOE_ERR_INVALID_ARG, "%s: eps must be finite and >= 0", fn);
+  return MOE_OK;
+}
+
+size_t moe_orthogonalize_workspace_size(int B, int rows, int cols, int dt) {
+  if (check_matrices("moe_orthogonalize_workspace_size", B, rows, cols, dt) != MOE_OK) return 0;
+  return trg::orthogonalize_ws_bytes(B, rows, cols, dt) + 16;
+}
+
+moe_status_t moe_orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, void* out,
+                               void* ws, size_t ws_bytes, void* stream) {
+  const char* fn = "moe_orthogonalize";
+  TRY(check_matrices(fn, B, rows, cols, dt));
+  TRY(check_iteration(fn, steps, eps));
+  if (B == 0) return ok();
+  TRY(check_ptrs(fn, {{"g", g}, {"out", out}}));
+  TRY(check_workspace(fn, ws, ws_bytes, trg::orthogonalize_ws_bytes(B, rows, cols, dt)));
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_orthogonalize(g, B, rows, cols, dt, steps, eps, out, ws, (hipStream_t)stream));
+}
+
+moe_status_t moe_muon_step(const moe_muon_args* a, void* stream) {
+  const char* fn = "moe_muon_step";
+  if (!a) return fail(MOE_ERR_INVALID_ARG, "%s: args is null", fn);
+  TRY(check_matrices(fn, a->B, a->rows, a->cols, a->dt));
+  TRY(check_iteration(fn, a->steps, a->eps));
+  for (auto& p : {std::make_pair("step", a->step), std::make_pair("decay", a->decay),
+                  std::make_pair("momentum", a->momentum)})
+    if (!(p.second >= -FLT_MAX && p.second <= FLT_MAX))
+      return fail(MOE_ERR_INVALID_ARG, "%s: %s must be finite", fn, p.first);
+  if ((a->master == nullptr) != (a->master_out == nullptr))
+    return fail(MOE_ERR_INVALID_ARG, "%s: master and master_out go together", fn);
+  if (a->B == 0) return ok();
+  TRY(check_ptrs(fn, {{"w", a->w}, {"g", a->g}, {"buf", a->buf}, {"w_out", a->w_out}, {"buf_out", a->buf_out}}));
+  TRY(check_optional_aligned(fn, {{"master", a->master}, {"master_out", a->master_out}}));
+  if ((uintptr_t)a->lr_scale & 3) return fail(MOE_ERR_ALIGNMENT, "%s: lr_scale is not 4-byte aligned", fn);
+  const void* outs[] = {a->w_out, a->buf_out, a->master_out};
+  const void* ins[] = {a->w, a->buf, a->master};
+  for (int i = 0; i < 3; ++i)
+    for (int j = 0; j < 3; ++j)
+      if (outs[i] != nullptr && ((i != j && (outs[i] == outs[j] || outs[i] == ins[j])) || outs[i] == a->g))
+        return fail(MOE_ERR_INVALID_ARG, "%s: an output may be its own input and no other buffer", fn);
+  TRY(check_workspace(fn, a->ws, a->ws_bytes, trg::orthogonalize_ws_bytes(a->B, a->rows, a->cols, a->dt)));
+  TRY(check_device());
+  trg::ProfScope ps(fn, (hipStream_t)stream);
+  return hip_status(fn, trg::launch_muon_step(*a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -68,6 +68,18 @@ hipError_t launch_dequantize_e2m1(const uint8_t* q, const uint8_t* s, bool bf16,
 hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
                               hipStream_t st);
 
+// dense products with an epilogue, and the orthogonalised weight update.  act: MOE_ACT_*
+size_t linear_ws_bytes(int T, int n, int K, int dt);
+hipError_t launch_linear_fwd(const void* x, const void* w, const void* bias, const void* res, int T, int n, int K,
+                             int act, int dt, void* z, void* y, void* ws, hipStream_t s);
+size_t linear_bwd_ws_bytes(int T, int n, int K, int dt);
+hipError_t launch_linear_bwd(const void* dy, const void* x, const void* w, const void* z, int T, int n, int K, int act,
+                             int dt, void* dx, void* dw, void* db, void* ws, hipStream_t s);
+size_t orthogonalize_ws_bytes(int B, int rows, int cols, int dt);
+hipError_t launch_orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, void* out,
+                                void* ws, hipStream_t s);
+hipError_t launch_muon_step(const moe_muon_args& a, hipStream_t s);
+
 // grouped GEMMs
 size_t ggemm_ws_bytes(int E, int R, int d, int h);
 hipError_t launch_ggemm_fwd(const void* xp, const void* w1, const void* w3, const void* w2, const int* offsets,

@@ -1,0 +1,360 @@
+// Orthogonalised updates (Newton-Schulz products, as the Muon optimiser uses
+// them) for batches of matrices: the experts' weight gradients.
+//   X_0 = G / (|G|_F + eps);  A = X X^T (X^T X for tall ones: the smaller side)
+//   X <- a X + (b A + c A^2) X,  (a, b, c) = (3.4445, -4.7750, 2.0315)
+// The odd quintic takes singular values in (0, 1] towards 1 (it stays under
+// 1.21 on [0, 1.21]), so every iterate is bounded and fits fp16 after scaling by
+// 2^8: fp16 has the matrix rate of bf16 and three more mantissa bits, which the
+// quintic's slope at 0 (3.4 a step, 485 over five) makes worth having.  fp32
+// matrices are kept as two fp16 planes (22 bits) and multiplied as split sums.
+//
+// A step is three products of dense_impl.h: A (symmetric: tiles on and above
+// the diagonal), b A + c A^2 (symmetric, A in the epilogue) and a X + B X (X in
+// the epilogue).  A wide matrix reads X as rows in the first and as columns (the
+// transpose read) in the last, a tall one the other way round, so no
+// transposed copy is made.  Before them one pass forms the momentum and the
+// sum of squares (in 64 bits: the square of any fp32 value fits) and one
+// scales into fp16; the last product's epilogue writes the result, or moves
+// the weights.
+#include "dense_impl.h"
+
+namespace trg {
+namespace dn {
+
+constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
+constexpr float kS = 256.0f;  // scale of the stored X, A and B
+constexpr int kSumBlocks = 256;  // partial sums of squares a matrix, at most
+
+TRG_DEV f16x8_t ld_h8(const _Float16* p) { return *(const f16x8_t*)p; }
+
+// Stored = hi + lo / 2^11 where there are two planes.
+TRG_DEV void put_planes(_Float16* out, long plane, bool two, const float (&v)[8]) {
+  f16x8_t hi;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) hi[i] = (_Float16)v[i];
+  *(f16x8_t*)out = hi;
+  if (two) {
+    f16x8_t lo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) lo[i] = (_Float16)((v[i] - (float)hi[i]) * 2048.0f);
+    *(f16x8_t*)(out + plane) = lo;
+  }
+}
+// v = alpha v + beta stored
+TRG_DEV void mix_planes(const _Float16* in, long plane, bool two, float alpha, float beta, float (&v)[8]) {
+  const f16x8_t hi = ld_h8(in);
+  if (two) {
+    const f16x8_t lo = ld_h8(in + plane);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = alpha * v[i] + beta * ((float)hi[i] + (float)lo[i] * (1.0f / 2048.0f));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = alpha * v[i] + beta * (float)hi[i];
+  }
+}
+
+// out = alpha v + beta in, in planes (in may be absent).
+struct EpiIter {
+  _Float16* out;
+  const _Float16* in;
+  long ld, bs, plane;
+  int two;
+  float alpha, beta;
+  TRG_DEV void apply(int b, int, int m, int n, float (&v)[8]) const {
+    const long at = b * bs + m * ld + n;
+    if (in) {
+      mix_planes(in + at, plane, two, alpha, beta, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= alpha;
+    }
+    put_planes(out + at, plane, two, v);
+  }
+};
+
+// The last product: o = alpha v + beta in, written as it is or as a step of
+// the weights, w <- w (1 - decay) - step o, in fp32 and rounded once.
+struct Update {
+  const void* w;  // null: write o
+  const float* master;
+  float* master_out;
+  void* out;
+  float step, decay;
+  const float* lr_scale;
+};
+template <class T>
+struct EpiUpdate {
+  const _Float16* in;
+  long ld, bs, plane;
+  int two;
+  float alpha, beta;
+  int rows, cols;
+  Update u;
+  TRG_DEV void apply(int b, int, int m, int n, float (&v)[8]) const {
+    mix_planes(in + b * bs + m * ld + n, plane, two, alpha, beta, v);
+    const bool both = n + 8 <= cols;
+    const long at = ((long)b * rows + m) * cols + n;
+    if (u.w) {
+      const float sc = u.lr_scale ? *u.lr_scale : 1.0f;
+      const float keep = 1.0f - u.decay * sc, step = u.step * sc;
+      float base[8];
+      if (u.master) ld8(u.master + at, both, base);
+      else ld8((const T*)u.w + at, both, base);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = base[i] * keep - step * v[i];
+      if (u.master) st8(u.master_out + at, both, v);
+    }
+    st8((T*)u.out + at, both, v);
+  }
+};
+
+// What is orthogonalised: g, or (buf given) the momentum's step.
+struct Momentum {
+  const float* buf;
+  float* buf_out;
+  float mu;
+  int nesterov;
+};
+
+// One pass over a batch's gradients: buf_out = mu buf + g and the partial sums
+// of u^2, u = g, g + mu buf_out, or buf_out.  blockIdx.y: the matrix.
+template <class T>
+__global__ __launch_bounds__(256) void sumsq_kernel(const T* __restrict__ g, Momentum mo, long count, int blocks,
+                                                    double* __restrict__ part) {
+  constexpr int V = Elt<T>::kVec;
+  __shared__ double red[4];
+  const long first = (long)blockIdx.y * count;
+  double sum = 0.0;
+  for (long c = (long)blockIdx.x * 256 + threadIdx.x; c < count / V; c += (long)blocks * 256) {
+    const long at = first + c * V;
+    float u[V];
+    unpack16<T>(*(const uint4*)(g + at), u);
+    if (mo.buf) {
+      float bn[V];
+#pragma unroll
+      for (int h = 0; h < V; h += 4) unpack16<float>(*(const uint4*)(mo.buf + at + h), bn + h);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        bn[i] = mo.mu * bn[i] + u[i];
+        u[i] = mo.nesterov ? u[i] + mo.mu * bn[i] : bn[i];
+      }
+#pragma unroll
+      for (int h = 0; h < V; h += 4) *(uint4*)(mo.buf_out + at + h) = pack16<float>(bn + h);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += (double)u[i] * (double)u[i];
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) part[(long)blockIdx.y * blocks + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+}
+
+// X = u 2^8 / (|u| + eps) in planes of rows of ldx values (zeros behind cols).
+// A zero matrix stays zero; one that holds an infinity or NaN becomes NaN.
+template <class T>
+__global__ __launch_bounds__(256) void scale_kernel(const T* __restrict__ g, Momentum mo, int rows, int cols, int ldx,
+                                                    float eps, const double* __restrict__ part, int blocks, int two,
+                                                    long plane, _Float16* __restrict__ x) {
+  constexpr int V = Elt<T>::kVec;
+  __shared__ double s_inv;
+  const int b = blockIdx.y;
+  if (threadIdx.x < 64) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < blocks; i += 64) s += part[(long)b * blocks + i];
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o, kWave);
+    if (threadIdx.x == 0) s_inv = s == 0.0 ? 0.0 : (s < INFINITY ? (double)kS / (sqrt(s) + (double)eps) : (double)NAN);
+  }
+  __syncthreads();
+  const double inv = s_inv;
+  const int chunks = ldx / 8;
+  const long total = (long)rows * chunks;
+  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
+    const int r = (int)(i / chunks), c = (int)(i - (long)r * chunks) * 8;
+    float v[8];
+#pragma unroll
+    for (int h = 0; h < 8; h += V) {
+      float u[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) u[k] = 0.f;
+      if (c + h < cols) {
+        const long at = ((long)b * rows + r) * cols + c + h;
+        if (!mo.buf || mo.nesterov) unpack16<T>(*(const uint4*)(g + at), u);
+        if (mo.buf) {
+          float bn[V];
+#pragma unroll
+          for (int q = 0; q < V; q += 4) unpack16<float>(*(const uint4*)(mo.buf_out + at + q), bn + q);
+#pragma unroll
+          for (int k = 0; k < V; ++k) u[k] = mo.nesterov ? u[k] + mo.mu * bn[k] : bn[k];
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) v[h + k] = (float)((double)u[k] * inv);
+    }
+    put_planes(x + ((long)b * rows + r) * ldx + c, plane, two, v);
+  }
+}
+
+// Sizes, plans and places of a chunk of the batch.
+struct Layout {
+  int rows, cols, m, ldx, lda, planes;
+  int chunk;            // matrices at a time
+  long xs, as;          // values of one X, of one A
+  Plan gram, sq, upd;
+  int sum_blocks;
+  size_t x_b, a_b, sum_b, part_b, total;
+};
+// Matrices go through in chunks whose X and A (two of each) take at most 2 GiB:
+// far more than fills the chip (the smallest chunk that does takes some tens of
+// MiB), and what a training step can spare of 288 GB.
+constexpr size_t kChunkBytes = (size_t)2 << 30;
+
+static Layout layout(int B, int rows, int cols, int dt) {
+  Layout l{};
+  l.rows = rows;
+  l.cols = cols;
+  l.m = rows < cols ? rows : cols;
+  l.ldx = (cols + 7) / 8 * 8;
+  l.lda = (l.m + 7) / 8 * 8;
+  l.planes = dt == MOE_F32 ? 2 : 1;
+  l.xs = (long)rows * l.ldx;
+  l.as = (long)l.m * l.lda;
+  const size_t per = 4UL * l.planes * (l.xs + l.as);
+  size_t most = kChunkBytes / per;
+  most = most < 1 ? 1 : most > 32768 ? 32768 : most;  // a launch's blockIdx.y counts matrices
+  l.chunk = (size_t)B <= most ? B : (int)most;
+  const int runs = l.planes == 2 ? 3 : 1, n = rows < cols ? cols : rows;
+  l.gram = plan(l.chunk, l.m, l.lda, (long)runs * gg::cdiv(n, 64), 2, true);
+  l.sq = plan(l.chunk, l.m, l.lda, (long)runs * gg::cdiv(l.m, 64), 2, true);
+  l.upd = plan(l.chunk, rows, l.ldx, (long)runs * gg::cdiv(l.m, 64), 2, false);
+  const long want = gg::cdiv((long)rows * cols, 16384);
+  l.sum_blocks = (int)(want > kSumBlocks ? kSumBlocks : want);
+  auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+  l.x_b = up(2UL * l.planes * l.chunk * l.xs);
+  l.a_b = up(2UL * l.planes * l.chunk * l.as);
+  l.sum_b = up(8UL * l.chunk * l.sum_blocks);
+  size_t p = l.gram.part_bytes(l.chunk, l.m, l.lda);
+  const size_t p2 = l.sq.part_bytes(l.chunk, l.m, l.lda), p3 = l.upd.part_bytes(l.chunk, rows, l.ldx);
+  p = p > p2 ? p : p2;
+  l.part_b = up(p > p3 ? p : p3);
+  l.total = 2 * l.x_b + 2 * l.a_b + l.sum_b + l.part_b;
+  return l;
+}
+
+template <class T>
+static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, Momentum mo,
+                                Update u, char* ws, hipStream_t s) {
+  const Layout l = layout(B, rows, cols, dt);
+  const bool tall = rows > cols, two = l.planes == 2;
+  _Float16* x0 = (_Float16*)ws;
+  _Float16* x1 = (_Float16*)(ws + l.x_b);
+  _Float16* A = (_Float16*)(ws + 2 * l.x_b);
+  _Float16* Bm = (_Float16*)(ws + 2 * l.x_b + l.a_b);
+  double* sums = (double*)(ws + 2 * l.x_b + 2 * l.a_b);
+  float* parts = (float*)(ws + 2 * l.x_b + 2 * l.a_b + l.sum_b);
+  const long mat = (long)rows * cols;
+  for (int b0 = 0; b0 < B; b0 += l.chunk) {
+    const int nb = B - b0 < l.chunk ? B - b0 : l.chunk;
+    const T* gc = (const T*)g + b0 * mat;
+    Momentum mc = mo;
+    if (mo.buf) {
+      mc.buf += b0 * mat;
+      mc.buf_out += b0 * mat;
+    }
+    Update uc = u;
+    uc.out = (T*)u.out + b0 * mat;
+    if (u.w) uc.w = (const T*)u.w + b0 * mat;
+    if (u.master) {
+      uc.master += b0 * mat;
+      uc.master_out += b0 * mat;
+    }
+    const long xplane = nb * l.xs, aplane = nb * l.as;
+    sumsq_kernel<T><<<dim3(l.sum_blocks, nb), 256, 0, s>>>(gc, mc, mat, l.sum_blocks, sums);
+    const long want = gg::cdiv(l.xs / 8, 1024);
+    scale_kernel<T><<<dim3((unsigned)(want > 1024 ? 1024 : want), nb), 256, 0, s>>>(
+        gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, two, xplane, x0);
+    hipError_t err = hipGetLastError();
+    _Float16 *x = x0, *y = x1;
+    for (int it = 0; it < steps && err == hipSuccess; ++it) {
+      Args a{};
+      a.batch = nb;
+      a.nseg = two ? 3 : 1;
+      // A = X X^T, or X^T X
+      a.A = a.B = x;
+      a.lda = a.ldb = l.ldx;
+      a.a_bs = a.b_bs = l.xs;
+      a.a_plane = a.b_plane = xplane;
+      a.M = a.b_rows = l.m;
+      a.N = l.lda;
+      a.K = tall ? rows : cols;
+      a.sym = 1;
+      const EpiIter ea{A, nullptr, l.lda, l.as, aplane, two, 1.0f / kS, 0.f};
+      err = tall ? run<ElF16, false, false>(l.gram, a, ea, parts, s) : run<ElF16, true, true>(l.gram, a, ea, parts, s);
+      if (err != hipSuccess) break;
+      // B = b A + c A^2
+      a.A = a.B = A;
+      a.lda = a.ldb = l.lda;
+      a.a_bs = a.b_bs = l.as;
+      a.a_plane = a.b_plane = aplane;
+      a.K = l.m;
+      const EpiIter eb{Bm, A, l.lda, l.as, aplane, two, kC / kS, kB};
+      err = run<ElF16, true, true>(l.sq, a, eb, parts, s);
+      if (err != hipSuccess) break;
+      // X' = a X + B X, or a X + X B
+      a.sym = 0;
+      a.M = rows;
+      a.N = l.ldx;
+      if (tall) {
+        a.A = x;
+        a.lda = l.ldx;
+        a.a_bs = l.xs;
+        a.a_plane = xplane;
+        a.B = Bm;
+      } else {
+        a.A = Bm;
+        a.B = x;
+        a.ldb = l.ldx;
+        a.b_bs = l.xs;
+        a.b_plane = xplane;
+      }
+      if (it + 1 < steps) {
+        const EpiIter ex{y, x, l.ldx, l.xs, xplane, two, 1.0f / kS, kA};
+        err = tall ? run<ElF16, true, true>(l.upd, a, ex, parts, s) : run<ElF16, true, false>(l.upd, a, ex, parts, s);
+        _Float16* t = x;
+        x = y;
+        y = t;
+      } else {
+        const EpiUpdate<T> eu{x, l.ldx, l.xs, xplane, two, 1.0f / (kS * kS), kA / kS, rows, cols, uc};
+        err = tall ? run<ElF16, true, true>(l.upd, a, eu, parts, s) : run<ElF16, true, false>(l.upd, a, eu, parts, s);
+      }
+    }
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+}  // namespace dn
+
+using namespace dn;
+
+size_t orthogonalize_ws_bytes(int B, int rows, int cols, int dt) { return layout(B, rows, cols, dt).total; }
+
+hipError_t launch_orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, void* out,
+                                void* ws, hipStream_t s) {
+  Update u{};
+  u.out = out;
+  return dt == MOE_F32 ? orthogonalize<float>(g, B, rows, cols, dt, steps, eps, Momentum{}, u, (char*)ws, s)
+                       : orthogonalize<uint16_t>(g, B, rows, cols, dt, steps, eps, Momentum{}, u, (char*)ws, s);
+}
+
+hipError_t launch_muon_step(const moe_muon_args& a, hipStream_t s) {
+  const Momentum mo{a.buf, a.buf_out, a.momentum, a.nesterov};
+  const Update u{a.w, a.master, a.master_out, a.w_out, a.step, a.decay, a.lr_scale};
+  return a.dt == MOE_F32
+             ? orthogonalize<float>(a.g, a.B, a.rows, a.cols, a.dt, a.steps, a.eps, mo, u, (char*)a.ws, s)
+             : orthogonalize<uint16_t>(a.g, a.B, a.rows, a.cols, a.dt, a.steps, a.eps, mo, u, (char*)a.ws, s);
+}
+
+}  // namespace trg

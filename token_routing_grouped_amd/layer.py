@@ -422,3 +422,62 @@ class MoEBlockGPU:
         dxn = self.layer.backward(dy, self.xn, wr, w1, w3, w2)
         _abi.moe_rmsnorm_bwd(dxn, self.s, norm_w, self.rstd, self.dx, self.dnorm_w, self.ws_norm, ds=ds)
         return self.dx
+
+
+class LinearGPU:
+    """One dense product beside the experts, y = act(x w^T + bias) + res for T
+    tokens, with its gradients.  Weights stay the caller's; forward() keeps in
+    self.z what the activation's gradient needs, backward() returns x's gradient
+    and leaves w's and bias's in self.dw and self.dbias (res's is dy itself)."""
+
+    def __init__(self, T: int, n: int, K: int, dtype: torch.dtype, act: str = "none", device="cuda"):
+        self.T, self.n, self.K, self.act = T, n, K, act
+        e = lambda *s: torch.empty(*s, dtype=dtype, device=torch.device(device))
+        self.y, self.dx, self.dw, self.dbias = e(T, n), e(T, K), e(n, K), e(n)
+        self.z = e(T, n) if act != "none" else None
+        self.ws = _abi.workspace(max(_abi.moe_linear_workspace_size(T, n, K, dtype),
+                                     _abi.moe_linear_bwd_workspace_size(T, n, K, dtype)), device)
+
+    def forward(self, x, w, bias=None, res=None):
+        _abi.moe_linear_fwd(x, w, self.y, self.ws, bias=bias, res=res, act=self.act, z=self.z)
+        return self.y
+
+    def backward(self, dy, x, w):
+        _abi.moe_linear_bwd(dy, x, w, self.ws, act=self.act, z=self.z, dx=self.dx, dw=self.dw, dbias=self.dbias)
+        return self.dx
+
+
+class MuonGPU:
+    """Orthogonalised momentum updates, in place, of a list of weights: [E,r,c]
+    (one update a matrix: the layer's w1, w3, w2) or [r,c].  A matrix moves by
+    lr sqrt(max(1, r/c)) times its orthogonalised momentum, after decaying by
+    lr weight_decay.  bf16 weights have fp32 masters here unless master=False.
+    lr_scale (a device fp32 scalar) multiplies lr and is read at every step, a
+    captured one too.
+
+    Master weights are a copy made here: weights changed from outside afterwards
+    are overwritten by the next step.  One object's steps belong on one stream.
+    """
+
+    def __init__(self, weights, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
+                 weight_decay: float = 0.0, steps: int = 5, eps: float = 1e-7, master: bool = True, lr_scale=None):
+        self.weights = list(weights)
+        if not self.weights:
+            raise _abi.MoeError("no weights")
+        self.lr, self.momentum, self.nesterov, self.weight_decay = lr, momentum, nesterov, weight_decay
+        self.steps, self.eps, self.lr_scale = steps, eps, lr_scale
+        self.bufs = [torch.zeros_like(w, dtype=torch.float32) for w in self.weights]
+        self.masters = [w.float() if master and w.dtype != torch.float32 else None for w in self.weights]
+        need = max(_abi.moe_orthogonalize_workspace_size(*_abi._batch(w, "weight"), w.dtype) for w in self.weights)
+        self.ws = _abi.workspace(need, self.weights[0].device)
+
+    def step(self, grads):
+        """One update from the weights' gradients, in their order."""
+        grads = list(grads)
+        if len(grads) != len(self.weights):
+            raise _abi.MoeError(f"{len(self.weights)} gradients expected, got {len(grads)}")
+        for w, g, buf, master in zip(self.weights, grads, self.bufs, self.masters):
+            r, c = w.shape[-2:]
+            _abi.moe_muon_step(w, g, buf, self.ws, step=self.lr * max(1.0, r / c) ** 0.5,
+                               decay=self.lr * self.weight_decay, momentum=self.momentum, nesterov=self.nesterov,
+                               steps=self.steps, eps=self.eps, master=master, lr_scale=self.lr_scale)
