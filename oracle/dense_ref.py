@@ -73,16 +73,16 @@ def iterate(g, steps=5, eps=1e-7, store=lambda v: v, mul=lambda a, b: a @ b):
 
 
 def store_f16(v):
-    """fp16 after scaling by 2^8 (how the library keeps the iterates of bf16)."""
-    return (v * 256.0).astype(np.float16).astype(np.float64) / 256.0
+    """fp16 after scaling by 2^13 (how the library keeps the iterates of bf16)."""
+    return (v * 8192.0).astype(np.float16).astype(np.float64) / 8192.0
 
 
 def store_2f16(v):
-    """Two fp16 planes, hi + lo / 2^11, after scaling by 2^8."""
-    v = v * 256.0
+    """Two fp16 planes, hi + lo, after scaling by 2^13."""
+    v = v * 8192.0
     hi = v.astype(np.float16).astype(np.float64)
-    lo = ((v - hi) * 2048.0).astype(np.float16).astype(np.float64)
-    return (hi + lo / 2048.0) / 256.0
+    lo = (v - hi).astype(np.float16).astype(np.float64)
+    return (hi + lo) / 8192.0
 
 
 def mul_f32(a, b):

@@ -11,66 +11,113 @@
 namespace trg {
 namespace dn {
 
-// act and its slope in fp32.  gelu is z Phi(z) with the error function.
-TRG_DEV float act_f(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? z : (z == z ? 0.f : z);
-    case MOE_ACT_GELU: return z * (0.5f + 0.5f * erff(z * 0.70710678118654752f));
-    case MOE_ACT_SILU: return z / (1.0f + expf(-z));
-    default: return z;
+// act and its slope in fp32.  Phi is the normal distribution function.  For
+// values stored in bf16 it comes from Abramowitz and Stegun's 7.1.26 (erf to
+// 1.5e-7, a polynomial in 1 / (1 + p |x|) times exp(-x^2)), the exponential and
+// the reciprocal from the hardware (1 ulp): an epilogue of 256 x 256 values is a
+// sixth of its tile's products with erff and expf (16384 x 6144 x 2048, gelu: 535 us).
+// The exponential is that of the density, too.
+template <class T>
+TRG_DEV float phi_f(float z, float& density) {
+  if constexpr (sizeof(T) == 4) {
+    density = 0.39894228040143268f * expf(-0.5f * z * z);
+    return 0.5f + 0.5f * erff(z * 0.70710678118654752f);
+  } else {
+    const float e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
+    const float q = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float h = 0.5f * q * e;  // Phi(-|z|)
+    density = 0.39894228040143268f * e;
+    return z > 0.f ? 1.0f - h : h;
   }
 }
-TRG_DEV float act_slope(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.f ? 1.f : (z == z ? 0.f : z);
-    case MOE_ACT_GELU:
-      return 0.5f + 0.5f * erff(z * 0.70710678118654752f) + z * 0.39894228040143268f * expf(-0.5f * z * z);
-    case MOE_ACT_SILU: {
-      const float s = 1.0f / (1.0f + expf(-z));
-      return s + z * s * (1.0f - s);
-    }
-    default: return 1.f;
+template <class T>
+TRG_DEV float sigmoid_of(float z) {
+  if constexpr (sizeof(T) == 4) return 1.0f / (1.0f + expf(-z));
+  else return sigmoid_f(z);
+}
+template <class T, int ACT>
+TRG_DEV float act_f(float z) {
+  float d;
+  if constexpr (ACT == MOE_ACT_RELU) return z > 0.f ? z : (z == z ? 0.f : z);
+  else if constexpr (ACT == MOE_ACT_GELU) return z * phi_f<T>(z, d);
+  else if constexpr (ACT == MOE_ACT_SILU) return z * sigmoid_of<T>(z);
+  else return z;
+}
+template <class T, int ACT>
+TRG_DEV float act_slope(float z) {
+  if constexpr (ACT == MOE_ACT_RELU) {
+    return z > 0.f ? 1.f : (z == z ? 0.f : z);
+  } else if constexpr (ACT == MOE_ACT_GELU) {
+    float d;
+    const float p = phi_f<T>(z, d);
+    return fmaf(z, d, p);
+  } else if constexpr (ACT == MOE_ACT_SILU) {
+    const float s = sigmoid_of<T>(z);
+    return s + z * s * (1.0f - s);
+  } else {
+    return 1.f;
   }
 }
 
 // y = act(v + bias) + res, z = v + bias; everything but y may be absent.
-template <class T>
+template <class T, int ACT>
 struct EpiLinear {
+  static constexpr bool kMirror = false;
   T* y;
   T* z;
   const T* bias;
   const T* res;
-  long ld;
-  int N, act;
-  TRG_DEV void apply(int, int, int m, int n, float (&v)[8]) const {
-    const bool both = n + 8 <= N;
-    const long at = m * ld + n;
-    float f[8];
-    if (bias) {
-      ld8(bias + n, both, f);
+  int N;
+  struct Tile {
+    TileMat<T> y, z, bias, res;
+    bool has_z, has_bias, has_res;
+    TRG_DEV void apply(const At& a, float (&v)[8]) const {
+      float f[8];
+      if (has_bias) {
+        bias.load(a, f);  // (rows 0 bytes apart)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += f[i];
+        for (int i = 0; i < 8; ++i) v[i] += f[i];
+      }
+      if (has_z) z.store(a, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = act_f<T, ACT>(v[i]);
+      if (has_res) {
+        res.load(a, f);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += f[i];
+      }
+      y.store(a, v);
     }
-    if (z) st8(z + at, both, v);
-    if (act != MOE_ACT_NONE)
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = act_f(v[i], act);
-    if (res) {
-      ld8(res + at, both, f);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] += f[i];
-    }
-    st8(y + at, both, v);
+  };
+  TRG_DEV int cols() const { return N; }
+  TRG_DEV Tile tile(int, int, int m0, int n0) const {
+    const long at = (long)m0 * N + n0;
+    return {TileMat<T>(y, at, N), TileMat<T>(z, at, N), TileMat<T>(bias, n0, 0), TileMat<T>(res, at, N),
+            z != nullptr, bias != nullptr, res != nullptr};
   }
 };
+
+// 8 values of a row from column n on; `both`: the last four exist too (fp32).
+TRG_DEV void ld8(const uint16_t* p, bool, float (&f)[8]) { unpack16<uint16_t>(*(const uint4*)p, f); }
+TRG_DEV void ld8(const float* p, bool both, float (&f)[8]) {
+  unpack16<float>(*(const uint4*)p, f);
+  if (both) unpack16<float>(*(const uint4*)(p + 4), f + 4);
+  else f[4] = f[5] = f[6] = f[7] = 0.f;
+}
+TRG_DEV void st8(uint16_t* p, bool, const float (&f)[8]) { *(uint4*)p = pack16<uint16_t>(f); }
+TRG_DEV void st8(float* p, bool both, const float (&f)[8]) {
+  *(uint4*)p = pack16<float>(f);
+  if (both) *(uint4*)(p + 4) = pack16<float>(f + 4);
+}
 
 // dz = dy act'(z) and the bias gradient's partial sums: a thread takes 8
 // columns of every 8th row of its block's rows (wave w of 8: rows w, w + 8, ...),
 // adds them in fp32, and the waves' sums are added in order.  dz or part may be
 // absent; z too where the activation has none.
 constexpr int kDzWaves = 8;
-template <class T>
-__global__ __launch_bounds__(64 * kDzWaves) void dz_kernel(const T* __restrict__ dy, const T* __restrict__ z, int act,
+template <class T, int ACT>
+__global__ __launch_bounds__(64 * kDzWaves) void dz_kernel(const T* __restrict__ dy, const T* __restrict__ z,
                                                            int rows, int n, int block_rows, T* __restrict__ dz,
                                                            float* __restrict__ part) {
   __shared__ float red[kDzWaves][64][9];
@@ -84,11 +131,11 @@ __global__ __launch_bounds__(64 * kDzWaves) void dz_kernel(const T* __restrict__
       const long at = (long)r * n + col;
       float g[8];
       ld8(dy + at, both, g);
-      if (act != MOE_ACT_NONE) {
+      if constexpr (ACT != MOE_ACT_NONE) {
         float zz[8];
         ld8(z + at, both, zz);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= act_slope(zz[i], act);
+        for (int i = 0; i < 8; ++i) g[i] *= act_slope<T, ACT>(zz[i]);
       }
       if (dz) st8(dz + at, both, g);
 #pragma unroll
@@ -130,20 +177,38 @@ static Plan plan_of(int M, int N, int K, int dt) {
   return plan(1, M, N, gg::cdiv((long)K * es, 128), es, false);
 }
 
+// f(std::integral_constant<int, act>{})
+template <class F>
+static auto with_act(int act, F&& f) {
+  switch (act) {
+    case MOE_ACT_RELU: return f(std::integral_constant<int, MOE_ACT_RELU>{});
+    case MOE_ACT_GELU: return f(std::integral_constant<int, MOE_ACT_GELU>{});
+    case MOE_ACT_SILU: return f(std::integral_constant<int, MOE_ACT_SILU>{});
+    default: return f(std::integral_constant<int, MOE_ACT_NONE>{});
+  }
+}
+
+static Args product(const void* A, long lda, const void* B, long ldb, int M, int N, int K) {
+  Args a{};
+  a.A = A;
+  a.lda = lda;
+  a.B = B;
+  a.ldb = ldb;
+  a.M = M;
+  a.N = a.b_rows = N;
+  a.K = K;
+  a.batch = a.nseg = 1;
+  return a;
+}
+
 template <class El, class T>
 static hipError_t fwd(const void* x, const void* w, const void* bias, const void* res, int rows, int n, int K, int act,
                       int dt, void* z, void* y, void* ws, hipStream_t s) {
-  Args a{};
-  a.A = x;
-  a.lda = K;
-  a.B = w;
-  a.ldb = K;
-  a.M = rows;
-  a.N = a.b_rows = n;
-  a.K = K;
-  a.batch = a.nseg = 1;
-  const EpiLinear<T> e{(T*)y, (T*)z, (const T*)bias, (const T*)res, n, n, act};
-  return run<El, true, true>(plan_of(rows, n, K, dt), a, e, (float*)ws, s);
+  const Args a = product(x, K, w, K, rows, n, K);
+  return with_act(act, [&](auto ACT) {
+    const EpiLinear<T, decltype(ACT)::value> e{(T*)y, (T*)z, (const T*)bias, (const T*)res, n};
+    return run<El, true, true>(plan_of(rows, n, K, dt), a, e, (float*)ws, s);
+  });
 }
 
 template <class El, class T>
@@ -155,36 +220,20 @@ static hipError_t bwd(const void* dy, const void* x, const void* w, const void* 
   float* part = (float*)ws;
   const bool need_dz = dz && (dx || dw);
   if (rows > 0 && (need_dz || db))
-    dz_kernel<T><<<dim3(gg::cdiv(n, 512), blocks), 64 * kDzWaves, 0, s>>>((const T*)dy, (const T*)z, act, rows, n, br,
-                                                                         need_dz ? dz : nullptr, db ? part : nullptr);
+    with_act(act, [&](auto ACT) {
+      dz_kernel<T, decltype(ACT)::value><<<dim3(gg::cdiv(n, 512), blocks), 64 * kDzWaves, 0, s>>>(
+          (const T*)dy, (const T*)z, rows, n, br, need_dz ? dz : nullptr, db ? part : nullptr);
+    });
   if (db) dbias_kernel<T><<<gg::cdiv(n, 256), 256, 0, s>>>(part, rows > 0 ? blocks : 0, n, (T*)db);
   hipError_t err = hipGetLastError();
   const void* g = dz ? (const void*)dz : dy;
   if (dx && err == hipSuccess) {  // dx = dz W
-    Args a{};
-    a.A = g;
-    a.lda = n;
-    a.B = w;
-    a.ldb = K;
-    a.M = rows;
-    a.N = K;
-    a.K = n;
-    a.batch = a.nseg = 1;
-    const EpiLinear<T> e{(T*)dx, nullptr, nullptr, nullptr, K, K, MOE_ACT_NONE};
-    err = run<El, true, false>(plan_of(rows, K, n, dt), a, e, (float*)ws, s);
+    const EpiLinear<T, MOE_ACT_NONE> e{(T*)dx, nullptr, nullptr, nullptr, K};
+    err = run<El, true, false>(plan_of(rows, K, n, dt), product(g, n, w, K, rows, K, n), e, (float*)ws, s);
   }
   if (dw && err == hipSuccess) {  // dW = dz^T x
-    Args a{};
-    a.A = g;
-    a.lda = n;
-    a.B = x;
-    a.ldb = K;
-    a.M = n;
-    a.N = K;
-    a.K = rows;
-    a.batch = a.nseg = 1;
-    const EpiLinear<T> e{(T*)dw, nullptr, nullptr, nullptr, K, K, MOE_ACT_NONE};
-    err = run<El, false, false>(plan_of(n, K, rows, dt), a, e, (float*)ws, s);
+    const EpiLinear<T, MOE_ACT_NONE> e{(T*)dw, nullptr, nullptr, nullptr, K};
+    err = run<El, false, false>(plan_of(n, K, rows, dt), product(g, n, x, K, n, K, rows), e, (float*)ws, s);
   }
   return err;
 }

@@ -12,10 +12,9 @@
 //  * Three types in one kernel: a stage holds 128 bytes of K of every row, so
 //    bf16 and fp16 take 64 values a step and fp32 32; a 16-byte fragment is one
 //    32x32x16 instruction or four 32x32x2.
-//  * Split sums: an operand in two fp16 planes, hi and 2^11 lo, is multiplied in
-//    three runs over K (lo hi, hi lo, then hi hi after scaling by 2^-11), which
-//    keeps 22 mantissa bits at a third of the fp16 rate (the fp32 instruction
-//    has a sixteenth of it).
+//  * Split sums: operands in two fp16 planes, hi + lo, are multiplied in three
+//    runs over K (lo hi, hi lo, hi hi), which keeps 22 mantissa bits at a third
+//    of the fp16 rate (the fp32 instruction has a sixteenth of it).
 //  * Symmetric products compute the tiles on and above the diagonal and store
 //    each twice.
 //  * K may be cut into parts (few output tiles): each part's sums go to memory
@@ -73,55 +72,96 @@ struct Args {
   int tiles_m, tiles_n, tiles;     // tiles of one part of one matrix
 };
 
-// 8 values of a row, from column n (a multiple of 8) on; fp32 rows may end
-// after four of them.
-TRG_DEV void ld8(const uint16_t* p, bool, float (&f)[8]) { unpack16<uint16_t>(*(const uint4*)p, f); }
-TRG_DEV void ld8(const float* p, bool both, float (&f)[8]) {
-  unpack16<float>(*(const uint4*)p, f);
-  if (both) unpack16<float>(*(const uint4*)(p + 4), f + 4);
-  else f[4] = f[5] = f[6] = f[7] = 0.f;
-}
-TRG_DEV void st8(uint16_t* p, bool, const float (&f)[8]) { *(uint4*)p = pack16<uint16_t>(f); }
-TRG_DEV void st8(float* p, bool both, const float (&f)[8]) {
-  *(uint4*)p = pack16<float>(f);
-  if (both) *(uint4*)(p + 4) = pack16<float>(f + 4);
+// The part of a matrix that an epilogue's tile covers, through a buffer resource
+// with 32-bit offsets from the tile's corner: 8 values from (row, col) on, or
+// nothing where the offset is kPast (a load gives zeros, a store is dropped), so
+// that a tile's edge costs no branch.  fp32 rows may end after four of them.
+struct At {
+  int row, col;    // from the tile's corner
+  bool ok, ok2;    // the first and the last four values exist
+};
+template <class T>
+struct TileMat {
+  __amdgpu_buffer_rsrc_t rs;
+  int ld;  // bytes
+  TRG_DEV TileMat(const T* p, long at, long ld_elts) : ld((int)ld_elts * (int)sizeof(T)) {
+    const unsigned long a = (unsigned long)(p + at);
+    const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)a);
+    const unsigned hi = __builtin_amdgcn_readfirstlane((unsigned)(a >> 32));
+    rs = __builtin_amdgcn_make_buffer_rsrc((void*)((unsigned long)hi << 32 | lo), (short)0, kPast, gg::kRsrcFlags);
+  }
+  TRG_DEV int off(const At& a) const { return a.row * ld + a.col * (int)sizeof(T); }
+  TRG_DEV uint4 raw(int o) const {
+    return __builtin_bit_cast(uint4, __builtin_amdgcn_raw_buffer_load_b128(rs, o, 0, 0));
+  }
+  TRG_DEV void raw_st(int o, uint4 v) const {
+    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), rs, o, 0, 0);
+  }
+  TRG_DEV void load(const At& a, float (&f)[8]) const {
+    const int o = off(a);
+    if constexpr (sizeof(T) == 2) {
+      unpack16<uint16_t>(raw(a.ok ? o : kPast), f);
+    } else {
+      unpack16<float>(raw(a.ok ? o : kPast), f);
+      unpack16<float>(raw(a.ok2 ? o + 16 : kPast), f + 4);
+    }
+  }
+  TRG_DEV void store(const At& a, const float (&f)[8]) const {
+    const int o = off(a);
+    if constexpr (sizeof(T) == 2) {
+      raw_st(a.ok ? o : kPast, pack16<uint16_t>(f));
+    } else {
+      raw_st(a.ok ? o : kPast, pack16<float>(f));
+      raw_st(a.ok2 ? o + 16 : kPast, pack16<float>(f + 4));
+    }
+  }
+};
+
+// ---- operand tiles: memory -> LDS, a wave and 1 KiB block at a time ------------
+// A tile's resource: under 2^31 bytes (the caller's widths see to that), never
+// negative.  All of it is uniform, which the loads' scalar operands rely on: said
+// outright, since the compiler may have formed it in vector registers.
+TRG_DEV __amdgpu_buffer_rsrc_t tile_rsrc(const char* base, int bytes) {
+  const unsigned long p = (unsigned long)base;
+  const unsigned lo = __builtin_amdgcn_readfirstlane((unsigned)p);
+  const unsigned hi = __builtin_amdgcn_readfirstlane((unsigned)(p >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc((void*)((unsigned long)hi << 32 | lo), (short)0,
+                                           __builtin_amdgcn_readfirstlane(bytes), gg::kRsrcFlags);
 }
 
-// ---- operand tiles: memory -> LDS ------------------------------------------
-// K-contiguous: as gg::load_kc, with the lanes at or past the row's end (kend
-// bytes) sent past the resource.
-template <int BMN, int NW>
-TRG_DEV void load_kc(char* dst, int wave, int lane, __amdgpu_buffer_rsrc_t rs, int kbyte, int kend, int ld_bytes) {
-  constexpr int PER = BMN / 8 / NW;
-  static_assert(PER >= 1 && BMN / 8 % NW == 0, "blocks per wave");
+// gg::lds_load16 at an LDS byte offset.
+TRG_DEV void lds_load16(__amdgpu_buffer_rsrc_t rs, unsigned lds, int voff) {
+  unsigned saved;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\t"
+      "s_mov_b32 m0, %1\n\t"
+      "s_nop 0\n\t"
+      "buffer_load_dwordx4 %2, %3, 0 offen lds\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(saved)
+      : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(voff), "s"(rs)
+      : "memory");
+}
+
+// K-contiguous: block blk holds rows 8 blk .. 8 blk + 7, 128 bytes of each, their
+// 16-byte chunks swizzled as gg::load_kc does; the lanes at or past the row's end
+// (kend bytes) are sent past the resource.
+TRG_DEV void load_kc(unsigned dst, int blk, int lane, __amdgpu_buffer_rsrc_t rs, int kbyte, int kend, int ld_bytes) {
   const int l8 = lane >> 3;
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int blk = wave * PER + i;
-    const int c = ((lane & 7) ^ (((blk & 1) << 2) | (l8 >> 1))) << 4;
-    const int off = (blk * 8 + l8) * ld_bytes + kbyte + c;
-    gg::lds_load16(rs, dst + blk * 1024, kbyte + c < kend ? off : kPast);
-  }
+  const int c = ((lane & 7) ^ (((blk & 1) << 2) | (l8 >> 1))) << 4;
+  const int off = (blk * 8 + l8) * ld_bytes + c;
+  lds_load16(rs, dst + blk * 1024, c < kend - kbyte ? off + kbyte : kPast);
 }
 
 // MN-contiguous: 128 / ES rows of BMN values; the resource starts at the step's
 // first row and the tile's first column and ends with the last row.
 template <int ES, int BMN>
-TRG_DEV int mn_swizzle(int kr) {  // XOR of a 16-byte chunk's place in row kr
-  return ES == 2 ? (kr & 3) << 2 : ((kr >> 2) & 1) << 3;
-}
-template <int ES, int BMN, int NW>
-TRG_DEV void load_mn(char* dst, int wave, int lane, __amdgpu_buffer_rsrc_t rs, int ld_bytes) {
-  constexpr int ROWB = BMN * ES, NBLK = BMN / 8, PER = NBLK / NW;
-  static_assert(PER >= 1 && NBLK % NW == 0, "blocks per wave");
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int blk = wave * PER + i;
-    const int at = blk * 1024 + lane * 16;
-    const int kr = at / ROWB;
-    const int c = ((at % ROWB) >> 4) ^ mn_swizzle<ES, BMN>(kr);
-    gg::lds_load16(rs, dst + blk * 1024, kr * ld_bytes + c * 16);
-  }
+TRG_DEV void load_mn(unsigned dst, int blk, int lane, __amdgpu_buffer_rsrc_t rs, int ld_bytes) {
+  constexpr int ROWB = BMN * ES;
+  const int at = blk * 1024 + lane * 16;
+  const int kr = at / ROWB;
+  const int swizzle = ES == 2 ? (kr & 3) << 2 : ((kr >> 2) & 1) << 3;
+  lds_load16(rs, dst + blk * 1024, kr * ld_bytes + ((((at % ROWB) >> 4) ^ swizzle) << 4));
 }
 
 // ---- fragments: LDS -> registers --------------------------------------------
@@ -169,20 +209,32 @@ TRG_DEV TileAt tile_at(const Args& g, int t) {
   return r;
 }
 
-// Epi::apply(b, part, row, col, v): the epilogue of 8 consecutive columns of a
-// row, col a multiple of 8 under N.
-template <class El, int BM, int BN, int WM, int WN, int OCC, bool AKC, bool BKC, class Epi>
-__global__ __launch_bounds__(64 * WM * WN, OCC) void dense_kernel(Args g, Epi epi) {
+// Epi: `auto tile = epi.tile(b, part, m0, n0)` for a tile's corner, then
+// tile.apply(at, v): 8 consecutive columns of a row, at.col a multiple of 8.
+// epi.cols(): how many columns C has in memory (a multiple of four), Epi::kMirror:
+// whether C may be symmetric.
+//
+// 256-wide tiles: 8 waves, two on a SIMD, one of which computes while the other
+// waits for LDS; 128-wide ones: 4 waves, and two workgroups on a CU.  Four waves
+// with 128 x 128 products each (a third fewer LDS reads, every wait covered by
+// reading two slices ahead and loading across tiles) measured no better: 8192^3
+// bf16 925 us against 885, 16384 x 2048 x 6144 NN 352 against 341.
+template <class El, int BM, int BN, int WM, int WN, bool AKC, bool BKC, class Epi>
+__global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi) {
   constexpr int NW = WM * WN, ES = El::ES, KSTEP = 128 / ES;
   constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
   constexpr int SA = BM * 128, SB = BN * 128, STAGE = SA + SB;
+  constexpr int PA = BM / 8 / NW, PB = BN / 8 / NW;  // 1 KiB blocks of a stage a wave loads
+  constexpr int SC = 64, WLDS = 32 * SC * 4;         // epilogue: 32 rows of 64 columns a wave, in stage 1
+  static_assert(WTN == SC && NW * WLDS <= STAGE, "epilogue staging");
   __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
+  const unsigned lds0 = (unsigned)(unsigned long)(gg::lds_void_t*)smem;
 
   const int total = g.batch * g.nsplit * g.tiles;
-  const int xcd = blockIdx.x & 7, lb = blockIdx.x >> 3, nbx = gridDim.x >> 3;
+  const int xcd = blockIdx.x & 7, nbx = gridDim.x >> 3;
   const int per = (total + 7) >> 3;
   const int t_end = min(total, (xcd + 1) * per);
   const int lda_b = (int)g.lda * ES, ldb_b = (int)g.ldb * ES;
@@ -197,11 +249,10 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void dense_kernel(Args g, Epi ep
     c.m0 = c.at.mt * BM;
     c.n0 = c.at.nt * BN;
     c.k0 = c.at.part * g.split_steps * KSTEP;
-    const int left = (g.K - c.k0 + KSTEP - 1) / KSTEP;
-    c.nk = max(0, min(left, g.split_steps));
+    c.nk = max(0, min((g.K - c.k0 + KSTEP - 1) / KSTEP, g.split_steps));
     return c;
   };
-  // step it of nseg * nk: operand bytes of one K step into a stage
+  // step it of nseg * nk: this wave's share of one K step of both operands
   auto issue = [&](const Cur& c, int it, int stage) {
     int seg = 0, ks = it;
     if (g.nseg > 1) {
@@ -211,27 +262,30 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void dense_kernel(Args g, Epi ep
     const int k = c.k0 + ks * KSTEP;
     const char* A = (const char*)g.A + (c.at.b * g.a_bs + (g.nseg > 1 && seg == 0 ? g.a_plane : 0)) * ES;
     const char* B = (const char*)g.B + (c.at.b * g.b_bs + (seg == 1 ? g.b_plane : 0)) * ES;
-    char* sA = smem + stage * STAGE;
-    char* sB = sA + SA;
+    const unsigned sA = lds0 + stage * STAGE, sB = sA + SA;
     if constexpr (AKC) {
-      const auto rs = gg::make_rsrc(A + (long)c.m0 * lda_b, (long)min(BM, g.M - c.m0) * lda_b);
-      load_kc<BM, NW>(sA, wave, lane, rs, k * ES, g.K * ES, lda_b);
+      const auto rs = tile_rsrc(A + (long)c.m0 * lda_b, min(BM, g.M - c.m0) * lda_b);
+#pragma unroll
+      for (int i = 0; i < PA; ++i) load_kc(sA, wave * PA + i, lane, rs, k * ES, g.K * ES, lda_b);
     } else {
-      const auto rs = gg::make_rsrc(A + (long)k * lda_b + c.m0 * ES, (long)min(KSTEP, g.K - k) * lda_b - c.m0 * ES);
-      load_mn<ES, BM, NW>(sA, wave, lane, rs, lda_b);
+      const auto rs = tile_rsrc(A + (long)k * lda_b + c.m0 * ES, min(KSTEP, g.K - k) * lda_b - c.m0 * ES);
+#pragma unroll
+      for (int i = 0; i < PA; ++i) load_mn<ES, BM>(sA, wave * PA + i, lane, rs, lda_b);
     }
     if constexpr (BKC) {
-      const auto rs = gg::make_rsrc(B + (long)c.n0 * ldb_b, (long)min(BN, g.b_rows - c.n0) * ldb_b);
-      load_kc<BN, NW>(sB, wave, lane, rs, k * ES, g.K * ES, ldb_b);
+      const auto rs = tile_rsrc(B + (long)c.n0 * ldb_b, max(0, min(BN, g.b_rows - c.n0)) * ldb_b);
+#pragma unroll
+      for (int i = 0; i < PB; ++i) load_kc(sB, wave * PB + i, lane, rs, k * ES, g.K * ES, ldb_b);
     } else {
-      const auto rs = gg::make_rsrc(B + (long)k * ldb_b + c.n0 * ES, (long)min(KSTEP, g.K - k) * ldb_b - c.n0 * ES);
-      load_mn<ES, BN, NW>(sB, wave, lane, rs, ldb_b);
+      const auto rs = tile_rsrc(B + (long)k * ldb_b + c.n0 * ES, min(KSTEP, g.K - k) * ldb_b - c.n0 * ES);
+#pragma unroll
+      for (int i = 0; i < PB; ++i) load_mn<ES, BN>(sB, wave * PB + i, lane, rs, ldb_b);
     }
   };
 
   // As in the grouped GEMMs: a tile's first step is loaded into stage 0 before
   // the previous tile's epilogue, which stages through stage 1.
-  int t = xcd * per + lb;
+  int t = xcd * per + (blockIdx.x >> 3);
   Cur cur;
   if (t < t_end) {
     cur = decode(t);
@@ -251,14 +305,6 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void dense_kernel(Args g, Epi ep
       asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();  // this step's stage is complete; the other one is free
       if (it + 1 < steps) issue(c, it + 1, (it + 1) & 1);
-      if (g.nseg > 1 && it == 2 * c.nk) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[i][j][r] *= 1.0f / 2048.0f;
-      }
       const char* sA = smem + (it & 1) * STAGE;
       const char* sB = sA + SA;
       u32x4v af[2][TM], bf[2][TN];
@@ -289,45 +335,55 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void dense_kernel(Args g, Epi ep
       if (cur.nk > 0) issue(cur, 0, 0);
     }
 
-    // Epilogue.  Each wave stages 16 rows of its tile in fp32 in its part of
-    // stage 1, then a lane takes 8 consecutive columns of a row (and, for the
-    // mirrored tile, 8 rows of a column).
-    constexpr int WLDS = STAGE / NW, P = WTN * 4 + 16, SR = 16;
-    static_assert(SR * P <= WLDS, "epilogue staging");
+    // Epilogue, 32 rows of SC columns of a wave at a time: staged in fp32 (straight
+    // from the accumulators' registers; 16-byte chunk c of row r at c ^ r % 16:
+    // neither the rows' writes nor the reads meet in a bank), then a lane takes 8
+    // consecutive columns of a row and, for the mirrored tile, 8 rows of a column.
+    constexpr int ROWB = SC * 4, CPR = SC / 8;  // staged row; its pieces of 8 columns
+    auto place = [&](int r, int c) {
+      return r * ROWB + ((c ^ (r & 15)) << 4);
+    };
     char* wl = smem + STAGE + wave * WLDS;
-    const int lrow = lane & 31, lgrp = (lane >> 5) * 4;
-    const bool mirror = g.sym && c.at.mt != c.at.nt;
-    static_for<TM * 2>([&](auto IH) {
-      constexpr int i = decltype(IH)::value / 2, part = decltype(IH)::value % 2;
-      const int ms = c.m0 + wm * WTM + i * 32 + part * SR, ns = c.n0 + wn * WTN;
-      if (ms < g.M && ns < g.N) {
-        if (lrow / SR == part) {
-          static_for<TN>([&](auto J) {
-            constexpr int j = decltype(J)::value;
-            static_for<4>([&](auto Q) {
-              constexpr int q = decltype(Q)::value;
-              const f32x4_t v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
-              *(f32x4_t*)(wl + (lrow & (SR - 1)) * P + (j * 32 + q * 8 + lgrp) * 4) = v;
-            });
-          });
-        }
-        __builtin_amdgcn_wave_barrier();
+    const auto tile = epi.tile(c.at.b, c.at.part, c.m0, c.n0);
+    const auto twin = epi.tile(c.at.b, c.at.part, c.n0, c.m0);
+    const int cols = epi.cols() - c.n0, rows = g.M - c.m0;
+    const bool mirror = Epi::kMirror && g.sym && c.at.mt != c.at.nt;
+    static_for<TM * (WTN / SC)>([&](auto IH) {
+      constexpr int i = decltype(IH)::value / (WTN / SC), jh = decltype(IH)::value % (WTN / SC);
+      int ln = lane;  // a new value to the compiler, or it keeps every block's addresses at once
+      asm volatile("" : "+v"(ln));
+      const int lrow = ln & 31, lhalf = ln >> 5;
+      static_for<SC / 32>([&](auto J) {
+        constexpr int j = jh * (SC / 32) + decltype(J)::value;
+        static_for<4>([&](auto Q) {
+          constexpr int q = decltype(Q)::value;
+          const f32x4_t v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+          *(f32x4_t*)(wl + place(lrow, decltype(J)::value * 8 + q * 2 + lhalf)) = v;
+        });
+      });
+      __builtin_amdgcn_wave_barrier();
 #pragma unroll
-        for (int s = 0; s < SR * (WTN / 8) / 64; ++s) {
-          const int ch = lane + s * 64, row = ch / (WTN / 8), col = ch % (WTN / 8) * 8;
-          float v[8];
-          *(f32x4_t*)v = *(const f32x4_t*)(wl + row * P + col * 4);
-          *(f32x4_t*)(v + 4) = *(const f32x4_t*)(wl + row * P + col * 4 + 16);
-          if (ms + row < g.M && ns + col < g.N) epi.apply(c.at.b, c.at.part, ms + row, ns + col, v);
-        }
+      for (int s = 0; s < 32 * CPR / 64; ++s) {
+        const int r = s * (64 / CPR) + ln / CPR, c8 = ln % CPR;
+        float v[8];
+        *(f32x4_t*)v = *(const f32x4_t*)(wl + place(r, c8 * 2));
+        *(f32x4_t*)(v + 4) = *(const f32x4_t*)(wl + place(r, c8 * 2 + 1));
+        At at{wm * WTM + i * 32 + r, wn * WTN + jh * SC + c8 * 8, false, false};
+        at.ok = at.row < rows && at.col < cols;
+        at.ok2 = at.row < rows && at.col + 4 < cols;
+        tile.apply(at, v);
+      }
+      if constexpr (Epi::kMirror) {
         if (mirror) {
 #pragma unroll
-          for (int s = 0; s < SR / 8 * WTN / 64; ++s) {
-            const int ch = lane + s * 64, col = ch / (SR / 8), r8 = ch % (SR / 8) * 8;
+          for (int s = 0; s < 4 * SC / 64; ++s) {
+            const int col = s * 16 + (ln >> 2), r8 = (ln & 3) * 8;
             float v[8];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) v[r] = *(const float*)(wl + (r8 + r) * P + col * 4);
-            if (ns + col < g.M && ms + r8 < g.N) epi.apply(c.at.b, c.at.part, ns + col, ms + r8, v);
+            for (int r = 0; r < 8; ++r) v[r] = *(const float*)(wl + place(r8 + r, col >> 2) + (col & 3) * 4);
+            At at{wn * WTN + jh * SC + col, wm * WTM + i * 32 + r8, false, false};
+            at.ok = at.ok2 = at.row < g.M - c.n0 && at.col < epi.cols() - c.m0;
+            twin.apply(at, v);
           }
         }
       }
@@ -336,24 +392,32 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void dense_kernel(Args g, Epi ep
   }
 }
 
-// One K part's sums: [part][batch][M][ld] fp32.
+// One K part's sums: [part][batch][M][ld] fp32, ld a multiple of 8.
 struct EpiPart {
+  static constexpr bool kMirror = false;
   float* p;
   long ld, mat, all;  // row; one matrix; one part of all matrices
-  TRG_DEV void apply(int b, int part, int m, int n, const float (&v)[8]) const {
-    float* o = p + part * all + b * mat + m * ld + n;
-    *(f32x4_t*)o = *(const f32x4_t*)v;
-    *(f32x4_t*)(o + 4) = *(const f32x4_t*)(v + 4);
+  struct Tile {
+    TileMat<float> o;
+    TRG_DEV void apply(const At& a, const float (&v)[8]) const { o.store(a, v); }
+  };
+  TRG_DEV int cols() const { return (int)ld; }
+  TRG_DEV Tile tile(int b, int part, int m0, int n0) const {
+    return {TileMat<float>(p, part * all + b * mat + m0 * ld + n0, ld)};
   }
 };
 
+// blockIdx.y, z: 128-row tile and matrix.
 template <class Epi>
-__global__ __launch_bounds__(256) void join_kernel(EpiPart in, int nsplit, int batch, int M, Epi epi) {
-  const long i = (long)blockIdx.x * 256 + threadIdx.x, chunks = in.ld / 8;
-  if (i >= batch * (long)M * chunks) return;
-  const long row = i / chunks;
-  const int n = (int)(i - row * chunks) * 8, b = (int)(row / M), m = (int)(row - (long)b * M);
-  const float* p = in.p + b * in.mat + m * in.ld + n;
+__global__ __launch_bounds__(256) void join_kernel(EpiPart in, int nsplit, int M, Epi epi) {
+  const int chunks = (int)(in.ld / 8), i = blockIdx.x * 256 + threadIdx.x;
+  const int m0 = blockIdx.y * 128, b = blockIdx.z;
+  At a{i / chunks, 0, false, false};
+  a.col = (i - a.row * chunks) * 8;
+  a.ok = a.row < 128 && m0 + a.row < M && a.col < epi.cols();
+  a.ok2 = a.ok && a.col + 4 < epi.cols();
+  const auto tile = epi.tile(b, 0, m0, 0);
+  const float* p = in.p + b * in.mat + (m0 + (a.ok ? a.row : 0)) * in.ld + (a.ok ? a.col : 0);
   float v[8];
 #pragma unroll
   for (int c = 0; c < 8; ++c) v[c] = p[c];
@@ -362,7 +426,7 @@ __global__ __launch_bounds__(256) void join_kernel(EpiPart in, int nsplit, int b
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] += p[c];
   }
-  epi.apply(b, 0, m, n, v);
+  tile.apply(a, v);
 }
 
 // ---- host: which tiles, how many parts ----------------------------------------
@@ -419,9 +483,9 @@ hipError_t run(const Plan& p, Args a, const Epi& epi, float* parts, hipStream_t 
   auto go = [&](const auto& e) {
     if (p.tile == 256) {
       if constexpr (El::ES == 2)
-        dense_kernel<El, 256, 256, 2, 4, 2, AKC, BKC><<<need < 256 ? need : 256, 512, 0, s>>>(a, e);
+        dense_kernel<El, 256, 256, 2, 4, AKC, BKC><<<need < 256 ? need : 256, 512, 0, s>>>(a, e);
     } else {
-      dense_kernel<El, 128, 128, 2, 2, 2, AKC, BKC><<<need < 512 ? need : 512, 256, 0, s>>>(a, e);
+      dense_kernel<El, 128, 128, 2, 2, AKC, BKC><<<need < 512 ? need : 512, 256, 0, s>>>(a, e);
     }
   };
   if (p.nsplit == 1) {
@@ -430,8 +494,8 @@ hipError_t run(const Plan& p, Args a, const Epi& epi, float* parts, hipStream_t 
     const long ld = (a.N + 7) / 8 * 8;
     const EpiPart part{parts, ld, a.M * ld, a.batch * (long)a.M * ld};
     go(part);
-    const long n = (long)a.batch * a.M * (ld / 8);
-    join_kernel<<<(unsigned)((n + 255) / 256), 256, 0, s>>>(part, p.nsplit, a.batch, a.M, epi);
+    const dim3 grid((unsigned)gg::cdiv(128 * (ld / 8), 256), gg::cdiv(a.M, 128), a.batch);
+    join_kernel<<<grid, 256, 0, s>>>(part, p.nsplit, a.M, epi);
   }
   return hipGetLastError();
 }

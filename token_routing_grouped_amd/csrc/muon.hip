@@ -3,8 +3,7 @@
 //   X_0 = G / (|G|_F + eps);  A = X X^T (X^T X for tall ones: the smaller side)
 //   X <- a X + (b A + c A^2) X,  (a, b, c) = (3.4445, -4.7750, 2.0315)
 // The odd quintic takes singular values in (0, 1] towards 1 (it stays under
-// 1.21 on [0, 1.21]), so every iterate is bounded and fits fp16 after scaling by
-// 2^8: fp16 has the matrix rate of bf16 and three more mantissa bits, which the
+// 1.21 on [0, 1.21]), so every iterate is bounded and fits fp16: fp16 has the matrix rate of bf16 and three more mantissa bits, which the
 // quintic's slope at 0 (3.4 a step, 485 over five) makes worth having.  fp32
 // matrices are kept as two fp16 planes (22 bits) and multiplied as split sums.
 //
@@ -22,53 +21,70 @@ namespace trg {
 namespace dn {
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-constexpr float kS = 256.0f;  // scale of the stored X, A and B
+// Scale of the stored X, A and B: |X| <= 1.21, |A| <= 1.47 and |B| <= 2.81 (as
+// norms, so as entries) stay under fp16's 65504, and what is small, entries of
+// large matrices and low planes, keeps as many bits above fp16's smallest.
+constexpr float kS = 8192.0f;
 constexpr int kSumBlocks = 256;  // partial sums of squares a matrix, at most
 
-TRG_DEV f16x8_t ld_h8(const _Float16* p) { return *(const f16x8_t*)p; }
-
-// Stored = hi + lo / 2^11 where there are two planes.
-TRG_DEV void put_planes(_Float16* out, long plane, bool two, const float (&v)[8]) {
-  f16x8_t hi;
+// Stored = hi + lo where there are two planes.
+TRG_DEV void split_planes(const float (&v)[8], f16x8_t& hi, f16x8_t& lo) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) hi[i] = (_Float16)v[i];
-  *(f16x8_t*)out = hi;
-  if (two) {
-    f16x8_t lo;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) lo[i] = (_Float16)((v[i] - (float)hi[i]) * 2048.0f);
-    *(f16x8_t*)(out + plane) = lo;
-  }
-}
-// v = alpha v + beta stored
-TRG_DEV void mix_planes(const _Float16* in, long plane, bool two, float alpha, float beta, float (&v)[8]) {
-  const f16x8_t hi = ld_h8(in);
-  if (two) {
-    const f16x8_t lo = ld_h8(in + plane);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = alpha * v[i] + beta * ((float)hi[i] + (float)lo[i] * (1.0f / 2048.0f));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = alpha * v[i] + beta * (float)hi[i];
+  for (int i = 0; i < 8; ++i) {
+    hi[i] = (_Float16)v[i];
+    lo[i] = (_Float16)(v[i] - (float)hi[i]);
   }
 }
 
-// out = alpha v + beta in, in planes (in may be absent).
+// A tile of a matrix in one plane, or two `plane` values apart.
+template <bool TWO>
+struct TilePlanes {
+  TileMat<uint16_t> hi, lo;
+  TRG_DEV TilePlanes(const _Float16* p, long at, long ld, long plane)
+      : hi((const uint16_t*)p, at, ld), lo((const uint16_t*)p, at + (TWO ? plane : 0), ld) {}
+  TRG_DEV void store(const At& a, const float (&v)[8]) const {
+    const int o = a.ok ? hi.off(a) : kPast;
+    f16x8_t h, l;
+    split_planes(v, h, l);
+    hi.raw_st(o, __builtin_bit_cast(uint4, h));
+    if (TWO) lo.raw_st(o, __builtin_bit_cast(uint4, l));
+  }
+  // v = alpha v + beta stored
+  TRG_DEV void mix(const At& a, float alpha, float beta, float (&v)[8]) const {
+    const int o = a.ok ? hi.off(a) : kPast;
+    const f16x8_t h = __builtin_bit_cast(f16x8_t, hi.raw(o));
+    f16x8_t l = {};
+    if (TWO) l = __builtin_bit_cast(f16x8_t, lo.raw(o));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = alpha * v[i] + beta * (TWO ? (float)h[i] + (float)l[i] : (float)h[i]);
+  }
+};
+
+// out = alpha v + beta in (IN), in planes.
+template <bool TWO, bool IN>
 struct EpiIter {
+  static constexpr bool kMirror = true;
   _Float16* out;
   const _Float16* in;
   long ld, bs, plane;
-  int two;
   float alpha, beta;
-  TRG_DEV void apply(int b, int, int m, int n, float (&v)[8]) const {
-    const long at = b * bs + m * ld + n;
-    if (in) {
-      mix_planes(in + at, plane, two, alpha, beta, v);
-    } else {
+  struct Tile {
+    TilePlanes<TWO> out, in;
+    float alpha, beta;
+    TRG_DEV void apply(const At& a, float (&v)[8]) const {
+      if (IN) {
+        in.mix(a, alpha, beta, v);
+      } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] *= alpha;
+        for (int i = 0; i < 8; ++i) v[i] *= alpha;
+      }
+      out.store(a, v);
     }
-    put_planes(out + at, plane, two, v);
+  };
+  TRG_DEV int cols() const { return (int)ld; }
+  TRG_DEV Tile tile(int b, int, int m0, int n0) const {
+    const long at = b * bs + m0 * ld + n0;
+    return {TilePlanes<TWO>(out, at, ld, plane), TilePlanes<TWO>(in, at, ld, plane), alpha, beta};
   }
 };
 
@@ -84,27 +100,41 @@ struct Update {
 };
 template <class T>
 struct EpiUpdate {
+  static constexpr bool kMirror = false, kTwo = sizeof(T) == 4;
   const _Float16* in;
   long ld, bs, plane;
-  int two;
   float alpha, beta;
-  int rows, cols;
+  int rows, ncols;
   Update u;
-  TRG_DEV void apply(int b, int, int m, int n, float (&v)[8]) const {
-    mix_planes(in + b * bs + m * ld + n, plane, two, alpha, beta, v);
-    const bool both = n + 8 <= cols;
-    const long at = ((long)b * rows + m) * cols + n;
-    if (u.w) {
-      const float sc = u.lr_scale ? *u.lr_scale : 1.0f;
-      const float keep = 1.0f - u.decay * sc, step = u.step * sc;
-      float base[8];
-      if (u.master) ld8(u.master + at, both, base);
-      else ld8((const T*)u.w + at, both, base);
+  struct Tile {
+    TilePlanes<kTwo> in;
+    TileMat<T> out, w;
+    TileMat<float> master, master_out;
+    float alpha, beta, keep, step;
+    bool has_w, has_master;
+    TRG_DEV void apply(const At& a, float (&v)[8]) const {
+      in.mix(a, alpha, beta, v);
+      if (has_w) {
+        float base[8];
+        if (has_master) master.load(a, base);
+        else w.load(a, base);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = base[i] * keep - step * v[i];
-      if (u.master) st8(u.master_out + at, both, v);
+        for (int i = 0; i < 8; ++i) v[i] = base[i] * keep - step * v[i];
+        if (has_master) master_out.store(a, v);
+      }
+      out.store(a, v);
     }
-    st8((T*)u.out + at, both, v);
+  };
+  TRG_DEV int cols() const { return ncols; }
+  TRG_DEV Tile tile(int b, int, int m0, int n0) const {
+    const long at = ((long)b * rows + m0) * ncols + n0;
+    const float s = u.w && u.lr_scale ? *u.lr_scale : 1.0f;
+    return {TilePlanes<kTwo>(in, b * bs + m0 * ld + n0, ld, plane),
+            TileMat<T>((const T*)u.out, at, ncols),
+            TileMat<T>((const T*)u.w, at, ncols),
+            TileMat<float>(u.master, at, ncols),
+            TileMat<float>(u.master_out, at, ncols),
+            alpha, beta, 1.0f - u.decay * s, u.step * s, u.w != nullptr, u.master != nullptr};
   }
 };
 
@@ -151,7 +181,7 @@ __global__ __launch_bounds__(256) void sumsq_kernel(const T* __restrict__ g, Mom
   if (threadIdx.x == 0) part[(long)blockIdx.y * blocks + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// X = u 2^8 / (|u| + eps) in planes of rows of ldx values (zeros behind cols).
+// X = u 2^13 / (|u| + eps) in planes of rows of ldx values (zeros behind cols).
 // A zero matrix stays zero; one that holds an infinity or NaN becomes NaN.
 template <class T>
 __global__ __launch_bounds__(256) void scale_kernel(const T* __restrict__ g, Momentum mo, int rows, int cols, int ldx,
@@ -193,7 +223,11 @@ __global__ __launch_bounds__(256) void scale_kernel(const T* __restrict__ g, Mom
 #pragma unroll
       for (int k = 0; k < V; ++k) v[h + k] = (float)((double)u[k] * inv);
     }
-    put_planes(x + ((long)b * rows + r) * ldx + c, plane, two, v);
+    f16x8_t hi, lo;
+    split_planes(v, hi, lo);
+    _Float16* o = x + ((long)b * rows + r) * ldx + c;
+    *(f16x8_t*)o = hi;
+    if (two) *(f16x8_t*)(o + plane) = lo;
   }
 }
 
@@ -247,7 +281,8 @@ template <class T>
 static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, Momentum mo,
                                 Update u, char* ws, hipStream_t s) {
   const Layout l = layout(B, rows, cols, dt);
-  const bool tall = rows > cols, two = l.planes == 2;
+  constexpr bool TWO = sizeof(T) == 4;
+  const bool tall = rows > cols;
   _Float16* x0 = (_Float16*)ws;
   _Float16* x1 = (_Float16*)(ws + l.x_b);
   _Float16* A = (_Float16*)(ws + 2 * l.x_b);
@@ -274,13 +309,13 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt
     sumsq_kernel<T><<<dim3(l.sum_blocks, nb), 256, 0, s>>>(gc, mc, mat, l.sum_blocks, sums);
     const long want = gg::cdiv(l.xs / 8, 1024);
     scale_kernel<T><<<dim3((unsigned)(want > 1024 ? 1024 : want), nb), 256, 0, s>>>(
-        gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, two, xplane, x0);
+        gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, TWO, xplane, x0);
     hipError_t err = hipGetLastError();
     _Float16 *x = x0, *y = x1;
     for (int it = 0; it < steps && err == hipSuccess; ++it) {
       Args a{};
       a.batch = nb;
-      a.nseg = two ? 3 : 1;
+      a.nseg = TWO ? 3 : 1;
       // A = X X^T, or X^T X
       a.A = a.B = x;
       a.lda = a.ldb = l.ldx;
@@ -290,7 +325,7 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt
       a.N = l.lda;
       a.K = tall ? rows : cols;
       a.sym = 1;
-      const EpiIter ea{A, nullptr, l.lda, l.as, aplane, two, 1.0f / kS, 0.f};
+      const EpiIter<TWO, false> ea{A, nullptr, l.lda, l.as, aplane, 1.0f / kS, 0.f};
       err = tall ? run<ElF16, false, false>(l.gram, a, ea, parts, s) : run<ElF16, true, true>(l.gram, a, ea, parts, s);
       if (err != hipSuccess) break;
       // B = b A + c A^2
@@ -299,7 +334,7 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt
       a.a_bs = a.b_bs = l.as;
       a.a_plane = a.b_plane = aplane;
       a.K = l.m;
-      const EpiIter eb{Bm, A, l.lda, l.as, aplane, two, kC / kS, kB};
+      const EpiIter<TWO, true> eb{Bm, A, l.lda, l.as, aplane, kC / kS, kB};
       err = run<ElF16, true, true>(l.sq, a, eb, parts, s);
       if (err != hipSuccess) break;
       // X' = a X + B X, or a X + X B
@@ -320,13 +355,13 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt
         a.b_plane = xplane;
       }
       if (it + 1 < steps) {
-        const EpiIter ex{y, x, l.ldx, l.xs, xplane, two, 1.0f / kS, kA};
+        const EpiIter<TWO, true> ex{y, x, l.ldx, l.xs, xplane, 1.0f / kS, kA};
         err = tall ? run<ElF16, true, true>(l.upd, a, ex, parts, s) : run<ElF16, true, false>(l.upd, a, ex, parts, s);
         _Float16* t = x;
         x = y;
         y = t;
       } else {
-        const EpiUpdate<T> eu{x, l.ldx, l.xs, xplane, two, 1.0f / (kS * kS), kA / kS, rows, cols, uc};
+        const EpiUpdate<T> eu{x, l.ldx, l.xs, xplane, 1.0f / (kS * kS), kA / kS, rows, cols, uc};
         err = tall ? run<ElF16, true, true>(l.upd, a, eu, parts, s) : run<ElF16, true, false>(l.upd, a, eu, parts, s);
       }
     }
