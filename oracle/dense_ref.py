@@ -65,8 +65,8 @@ def iterate(g, steps=5, eps=1e-7, store=lambda v: v, mul=lambda a, b: a @ b):
     x = store(x / (np.sqrt((x * x).sum()) + eps))
     for k in range(steps):
         a = store(mul(x, x.T))
-        b = store(B * a + C * mul(a, a))
-        x = A * x + mul(b, x)
+        b = store(A * np.eye(len(a)) + B * a + C * mul(a, a))
+        x = mul(b, x)
         if k + 1 < steps:
             x = store(x)
     return x.T if tall else x

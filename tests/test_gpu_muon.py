@@ -13,9 +13,9 @@ single entries, plus the output's own rounding.
 What that model leaves out is the evaluation in fp32 (evaluation() below), which
 for a few rows of fp32 values is as large as E.  Of a step with singular values
 s (so |X|_F = |s|, |A|_F = |s^2|), in units of 4 2^-24:
-  B = b A + c A^2 from rounded b and c, two products, one sum: under 4 roundings
-  of |b| |A| + |c| |A^2|, times X: (|b| |s^2| + |c| |s^4|) max s;
-  X' = a X + B X the same way: a |s| + |(b s^2 + c s^4) s|;
+  B = a + b A + c A^2 from rounded a, b and c, two products, two sums: under 4
+  roundings of a |I| + |b| |A| + |c| |A^2| (r values s: |I| = sqrt(r)), times X:
+  (a sqrt(r) + |b| |s^2| + |c| |s^4|) max s;
   the planes' lo lo products, left out: 2^-22 of the products' terms, at most
   |X|_F^2 in A (whence |b| + 2 |c| max s^2 and X: times max s), |c| |A|_F^2 in
   A^2 (times max s), |B|_F |X|_F in B X.
@@ -79,8 +79,8 @@ def evaluation(u, steps, eps, planes):
         t = t[t > 0]
         if t.size:
             total *= max(np.abs(ref.A + 3 * ref.B * t ** 2 + 5 * ref.C * t ** 4).max(), (ref.quintic(t) / t).max())
-        top, m = s.max(), b * n(s ** 2) + c * n(s ** 4)
-        d = m * top + a * n(s) + n((ref.B * s ** 2 + ref.C * s ** 4) * s)
+        top, m = s.max(), a * len(s) ** 0.5 + b * n(s ** 2) + c * n(s ** 4)
+        d = m * top
         if planes:
             d += n(s) ** 2 * (b + 2 * c * top ** 2) * top + c * n(s ** 2) ** 2 * top + m * n(s)
         total += 2.0 ** -22 * d

@@ -215,19 +215,21 @@ TRG_DEV TileAt tile_at(const Args& g, int t) {
 // whether C may be symmetric.
 //
 // 256-wide tiles: 8 waves, two on a SIMD, one of which computes while the other
-// waits for LDS; 128-wide ones: 4 waves, and two workgroups on a CU.  Four waves
+// waits for LDS; 128-wide ones: 4 waves, and two workgroups on a CU or, where
+// there is one at most (the waits are then all there is), NST = 4 stages, three
+// of which are on their way.  Four waves
 // with 128 x 128 products each (a third fewer LDS reads, every wait covered by
 // reading two slices ahead and loading across tiles) measured no better: 8192^3
 // bf16 925 us against 885, 16384 x 2048 x 6144 NN 352 against 341.
-template <class El, int BM, int BN, int WM, int WN, bool AKC, bool BKC, class Epi>
+template <class El, int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC, class Epi>
 __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi) {
   constexpr int NW = WM * WN, ES = El::ES, KSTEP = 128 / ES;
   constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
   constexpr int SA = BM * 128, SB = BN * 128, STAGE = SA + SB;
   constexpr int PA = BM / 8 / NW, PB = BN / 8 / NW;  // 1 KiB blocks of a stage a wave loads
-  constexpr int SC = 64, WLDS = 32 * SC * 4;         // epilogue: 32 rows of 64 columns a wave, in stage 1
+  constexpr int SC = 64, WLDS = 32 * SC * 4;         // epilogue: 32 rows of 64 columns a wave, in the last stage
   static_assert(WTN == SC && NW * WLDS <= STAGE, "epilogue staging");
-  __shared__ __attribute__((aligned(1024))) char smem[2 * STAGE];
+  __shared__ __attribute__((aligned(1024))) char smem[NST * STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -283,13 +285,18 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     }
   };
 
-  // As in the grouped GEMMs: a tile's first step is loaded into stage 0 before
-  // the previous tile's epilogue, which stages through stage 1.
+  // A tile's first NST - 1 steps are loaded into the first stages before the
+  // previous tile's epilogue, which stages through the last one.
+  auto start = [&](const Cur& c) {
+#pragma unroll
+    for (int s = 0; s < NST - 1; ++s)
+      if (s < c.nk * g.nseg) issue(c, s, s);
+  };
   int t = xcd * per + (blockIdx.x >> 3);
   Cur cur;
   if (t < t_end) {
     cur = decode(t);
-    if (cur.nk > 0) issue(cur, 0, 0);
+    start(cur);
   }
   for (; t < t_end; t += nbx) {
     const Cur c = cur;
@@ -302,10 +309,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
     const int steps = c.nk * g.nseg;
     for (int it = 0; it < steps; ++it) {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-      __syncthreads();  // this step's stage is complete; the other one is free
-      if (it + 1 < steps) issue(c, it + 1, (it + 1) & 1);
-      const char* sA = smem + (it & 1) * STAGE;
+      // this step's loads are done once no more are under way than the later
+      // steps' (whatever was issued after those only makes the wait longer)
+      const int later = min(NST - 2, steps - 1 - it);
+      if (NST > 2 && later == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"i"(2 * (PA + PB)) : "memory");
+      else if (NST > 2 && later == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"i"(PA + PB) : "memory");
+      else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+      __syncthreads();  // this step's stage is complete; the one read last is free
+      if (it + NST - 1 < steps) issue(c, it + NST - 1, (it + NST - 1) % NST);
+      const char* sA = smem + (it % NST) * STAGE;
       const char* sB = sA + SA;
       u32x4v af[2][TM], bf[2][TN];
 #pragma unroll
@@ -332,7 +344,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     __syncthreads();  // every wave is done with the last stage
     if (t + nbx < t_end) {
       cur = decode(t + nbx);
-      if (cur.nk > 0) issue(cur, 0, 0);
+      start(cur);
     }
 
     // Epilogue, 32 rows of SC columns of a wave at a time: staged in fp32 (straight
@@ -343,7 +355,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     auto place = [&](int r, int c) {
       return r * ROWB + ((c ^ (r & 15)) << 4);
     };
-    char* wl = smem + STAGE + wave * WLDS;
+    char* wl = smem + (NST - 1) * STAGE + wave * WLDS;
     const auto tile = epi.tile(c.at.b, c.at.part, c.m0, c.n0);
     const auto twin = epi.tile(c.at.b, c.at.part, c.n0, c.m0);
     const int cols = epi.cols() - c.n0, rows = g.M - c.m0;
@@ -483,9 +495,10 @@ hipError_t run(const Plan& p, Args a, const Epi& epi, float* parts, hipStream_t 
   auto go = [&](const auto& e) {
     if (p.tile == 256) {
       if constexpr (El::ES == 2)
-        dense_kernel<El, 256, 256, 2, 4, AKC, BKC><<<need < 256 ? need : 256, 512, 0, s>>>(a, e);
+        dense_kernel<El, 256, 256, 2, 4, 2, AKC, BKC><<<need < 256 ? need : 256, 512, 0, s>>>(a, e);
     } else {
-      dense_kernel<El, 128, 128, 2, 2, AKC, BKC><<<need < 512 ? need : 512, 256, 0, s>>>(a, e);
+      if (total <= 256) dense_kernel<El, 128, 128, 2, 2, 4, AKC, BKC><<<need, 256, 0, s>>>(a, e);
+      else dense_kernel<El, 128, 128, 2, 2, 2, AKC, BKC><<<need < 512 ? need : 512, 256, 0, s>>>(a, e);
     }
   };
   if (p.nsplit == 1) {

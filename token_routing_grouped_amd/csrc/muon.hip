@@ -1,15 +1,18 @@
 // Orthogonalised updates (Newton-Schulz products, as the Muon optimiser uses
 // them) for batches of matrices: the experts' weight gradients.
 //   X_0 = G / (|G|_F + eps);  A = X X^T (X^T X for tall ones: the smaller side)
-//   X <- a X + (b A + c A^2) X,  (a, b, c) = (3.4445, -4.7750, 2.0315)
+//   X <- B X,  B = a + b A + c A^2,  (a, b, c) = (3.4445, -4.7750, 2.0315)
 // The odd quintic takes singular values in (0, 1] towards 1 (it stays under
 // 1.21 on [0, 1.21]), so every iterate is bounded and fits fp16: fp16 has the matrix rate of bf16 and three more mantissa bits, which the
 // quintic's slope at 0 (3.4 a step, 485 over five) makes worth having.  fp32
 // matrices are kept as two fp16 planes (22 bits) and multiplied as split sums.
 //
 // A step is three products of dense_impl.h: A (symmetric: tiles on and above
-// the diagonal), b A + c A^2 (symmetric, A in the epilogue) and a X + B X (X in
-// the epilogue).  A wide matrix reads X as rows in the first and as columns (the
+// the diagonal), B (symmetric, with a and b A in the epilogue) and B X.  With a in
+// B's diagonal the last one, half of a step's operations, has nothing to read in
+// its epilogue, and B's diagonal is stored as what is left of the sum: near the
+// end 0.70, not -2.74 to be added to 3.44, so fp16 rounds it to a quarter of
+// that (the result's error is a tenth smaller).  A wide matrix reads X as rows in the first and as columns (the
 // transpose read) in the last, a tall one the other way round, so no
 // transposed copy is made.  Before them one pass forms the momentum and the
 // sum of squares (in 64 bits: the square of any fp32 value fits) and one
@@ -21,7 +24,7 @@ namespace trg {
 namespace dn {
 
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
-// Scale of the stored X, A and B: |X| <= 1.21, |A| <= 1.47 and |B| <= 2.81 (as
+// Scale of the stored X, A and B: |X| <= 1.21, |A| <= 1.47 and |B| <= 3.45 (as
 // norms, so as entries) stay under fp16's 65504, and what is small, entries of
 // large matrices and low planes, keeps as many bits above fp16's smallest.
 constexpr float kS = 8192.0f;
@@ -60,20 +63,24 @@ struct TilePlanes {
   }
 };
 
-// out = alpha v + beta in (IN), in planes.
+// out = alpha v + beta in + gamma I (IN), or alpha v, in planes.
 template <bool TWO, bool IN>
 struct EpiIter {
   static constexpr bool kMirror = true;
   _Float16* out;
   const _Float16* in;
   long ld, bs, plane;
-  float alpha, beta;
+  float alpha, beta, gamma;
   struct Tile {
     TilePlanes<TWO> out, in;
-    float alpha, beta;
+    float alpha, beta, gamma;
+    int diag;  // the tile's row less its column
     TRG_DEV void apply(const At& a, float (&v)[8]) const {
       if (IN) {
         in.mix(a, alpha, beta, v);
+        const int d = diag + a.row - a.col;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] += d == i ? gamma : 0.f;
       } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] *= alpha;
@@ -84,11 +91,11 @@ struct EpiIter {
   TRG_DEV int cols() const { return (int)ld; }
   TRG_DEV Tile tile(int b, int, int m0, int n0) const {
     const long at = b * bs + m0 * ld + n0;
-    return {TilePlanes<TWO>(out, at, ld, plane), TilePlanes<TWO>(in, at, ld, plane), alpha, beta};
+    return {TilePlanes<TWO>(out, at, ld, plane), TilePlanes<TWO>(in, at, ld, plane), alpha, beta, gamma, m0 - n0};
   }
 };
 
-// The last product: o = alpha v + beta in, written as it is or as a step of
+// The last product: o = alpha v, written as it is or as a step of
 // the weights, w <- w (1 - decay) - step o, in fp32 and rounded once.
 struct Update {
   const void* w;  // null: write o
@@ -100,20 +107,18 @@ struct Update {
 };
 template <class T>
 struct EpiUpdate {
-  static constexpr bool kMirror = false, kTwo = sizeof(T) == 4;
-  const _Float16* in;
-  long ld, bs, plane;
-  float alpha, beta;
+  static constexpr bool kMirror = false;
+  float alpha;
   int rows, ncols;
   Update u;
   struct Tile {
-    TilePlanes<kTwo> in;
     TileMat<T> out, w;
     TileMat<float> master, master_out;
-    float alpha, beta, keep, step;
+    float alpha, keep, step;
     bool has_w, has_master;
     TRG_DEV void apply(const At& a, float (&v)[8]) const {
-      in.mix(a, alpha, beta, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] *= alpha;
       if (has_w) {
         float base[8];
         if (has_master) master.load(a, base);
@@ -129,12 +134,11 @@ struct EpiUpdate {
   TRG_DEV Tile tile(int b, int, int m0, int n0) const {
     const long at = ((long)b * rows + m0) * ncols + n0;
     const float s = u.w && u.lr_scale ? *u.lr_scale : 1.0f;
-    return {TilePlanes<kTwo>(in, b * bs + m0 * ld + n0, ld, plane),
-            TileMat<T>((const T*)u.out, at, ncols),
+    return {TileMat<T>((const T*)u.out, at, ncols),
             TileMat<T>((const T*)u.w, at, ncols),
             TileMat<float>(u.master, at, ncols),
             TileMat<float>(u.master_out, at, ncols),
-            alpha, beta, 1.0f - u.decay * s, u.step * s, u.w != nullptr, u.master != nullptr};
+            alpha, 1.0f - u.decay * s, u.step * s, u.w != nullptr, u.master != nullptr};
   }
 };
 
@@ -182,14 +186,41 @@ __global__ __launch_bounds__(256) void sumsq_kernel(const T* __restrict__ g, Mom
 }
 
 // X = u 2^13 / (|u| + eps) in planes of rows of ldx values (zeros behind cols).
-// A zero matrix stays zero; one that holds an infinity or NaN becomes NaN.
-template <class T>
+// A zero matrix stays zero; one that holds an infinity or NaN becomes NaN.  A
+// thread's kScaleChunks pieces of 8 values are loaded before the norm is put
+// together from its partial sums.
+constexpr int kScaleChunks = 4;
+template <class T, bool MOM>
 __global__ __launch_bounds__(256) void scale_kernel(const T* __restrict__ g, Momentum mo, int rows, int cols, int ldx,
                                                     float eps, const double* __restrict__ part, int blocks, int two,
                                                     long plane, _Float16* __restrict__ x) {
   constexpr int V = Elt<T>::kVec;
   __shared__ double s_inv;
-  const int b = blockIdx.y;
+  const int b = blockIdx.y, chunks = ldx / 8;
+  const long total = (long)rows * chunks, i0 = (long)blockIdx.x * (256 * kScaleChunks) + threadIdx.x;
+  const bool use_g = !MOM || mo.nesterov;
+  float u[kScaleChunks][8];
+#pragma unroll
+  for (int k = 0; k < kScaleChunks; ++k) {
+    const long i = i0 + k * 256;
+    const int r = ldx == cols ? 0 : (int)(i / chunks);  // (rows without padding are one long row)
+    const long c = (i - (long)r * chunks) * 8;
+#pragma unroll
+    for (int h = 0; h < 8; h += V) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) u[k][h + e] = 0.f;
+      if (i >= total || (ldx != cols && c + h >= cols)) continue;
+      const long at = ((long)b * rows + r) * cols + c + h;
+      if (use_g) unpack16<T>(*(const uint4*)(g + at), u[k] + h);
+      if (MOM) {
+        float bn[V];
+#pragma unroll
+        for (int q = 0; q < V; q += 4) unpack16<float>(*(const uint4*)(mo.buf_out + at + q), bn + q);
+#pragma unroll
+        for (int e = 0; e < V; ++e) u[k][h + e] = mo.nesterov ? u[k][h + e] + mo.mu * bn[e] : bn[e];
+      }
+    }
+  }
   if (threadIdx.x < 64) {
     double s = 0.0;
     for (int i = threadIdx.x; i < blocks; i += 64) s += part[(long)b * blocks + i];
@@ -199,33 +230,16 @@ __global__ __launch_bounds__(256) void scale_kernel(const T* __restrict__ g, Mom
   }
   __syncthreads();
   const double inv = s_inv;
-  const int chunks = ldx / 8;
-  const long total = (long)rows * chunks;
-  for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < total; i += (long)gridDim.x * 256) {
-    const int r = (int)(i / chunks), c = (int)(i - (long)r * chunks) * 8;
+#pragma unroll
+  for (int k = 0; k < kScaleChunks; ++k) {
+    const long i = i0 + k * 256;
+    if (i >= total) return;
     float v[8];
 #pragma unroll
-    for (int h = 0; h < 8; h += V) {
-      float u[V];
-#pragma unroll
-      for (int k = 0; k < V; ++k) u[k] = 0.f;
-      if (c + h < cols) {
-        const long at = ((long)b * rows + r) * cols + c + h;
-        if (!mo.buf || mo.nesterov) unpack16<T>(*(const uint4*)(g + at), u);
-        if (mo.buf) {
-          float bn[V];
-#pragma unroll
-          for (int q = 0; q < V; q += 4) unpack16<float>(*(const uint4*)(mo.buf_out + at + q), bn + q);
-#pragma unroll
-          for (int k = 0; k < V; ++k) u[k] = mo.nesterov ? u[k] + mo.mu * bn[k] : bn[k];
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < V; ++k) v[h + k] = (float)((double)u[k] * inv);
-    }
+    for (int e = 0; e < 8; ++e) v[e] = (float)((double)u[k][e] * inv);
     f16x8_t hi, lo;
     split_planes(v, hi, lo);
-    _Float16* o = x + ((long)b * rows + r) * ldx + c;
+    _Float16* o = x + (long)b * rows * ldx + i * 8;
     *(f16x8_t*)o = hi;
     if (two) *(f16x8_t*)(o + plane) = lo;
   }
@@ -307,9 +321,9 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt
     }
     const long xplane = nb * l.xs, aplane = nb * l.as;
     sumsq_kernel<T><<<dim3(l.sum_blocks, nb), 256, 0, s>>>(gc, mc, mat, l.sum_blocks, sums);
-    const long want = gg::cdiv(l.xs / 8, 1024);
-    scale_kernel<T><<<dim3((unsigned)(want > 1024 ? 1024 : want), nb), 256, 0, s>>>(
-        gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, TWO, xplane, x0);
+    const dim3 grid(gg::cdiv(l.xs / 8, 256 * kScaleChunks), nb);
+    if (mo.buf) scale_kernel<T, true><<<grid, 256, 0, s>>>(gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, TWO, xplane, x0);
+    else scale_kernel<T, false><<<grid, 256, 0, s>>>(gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, TWO, xplane, x0);
     hipError_t err = hipGetLastError();
     _Float16 *x = x0, *y = x1;
     for (int it = 0; it < steps && err == hipSuccess; ++it) {
@@ -325,19 +339,19 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt
       a.N = l.lda;
       a.K = tall ? rows : cols;
       a.sym = 1;
-      const EpiIter<TWO, false> ea{A, nullptr, l.lda, l.as, aplane, 1.0f / kS, 0.f};
+      const EpiIter<TWO, false> ea{A, nullptr, l.lda, l.as, aplane, 1.0f / kS, 0.f, 0.f};
       err = tall ? run<ElF16, false, false>(l.gram, a, ea, parts, s) : run<ElF16, true, true>(l.gram, a, ea, parts, s);
       if (err != hipSuccess) break;
-      // B = b A + c A^2
+      // B = a + b A + c A^2
       a.A = a.B = A;
       a.lda = a.ldb = l.lda;
       a.a_bs = a.b_bs = l.as;
       a.a_plane = a.b_plane = aplane;
       a.K = l.m;
-      const EpiIter<TWO, true> eb{Bm, A, l.lda, l.as, aplane, kC / kS, kB};
+      const EpiIter<TWO, true> eb{Bm, A, l.lda, l.as, aplane, kC / kS, kB, kA * kS};
       err = run<ElF16, true, true>(l.sq, a, eb, parts, s);
       if (err != hipSuccess) break;
-      // X' = a X + B X, or a X + X B
+      // X' = B X, or X B
       a.sym = 0;
       a.M = rows;
       a.N = l.ldx;
@@ -355,13 +369,13 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt
         a.b_plane = xplane;
       }
       if (it + 1 < steps) {
-        const EpiIter<TWO, true> ex{y, x, l.ldx, l.xs, xplane, 1.0f / kS, kA};
+        const EpiIter<TWO, false> ex{y, nullptr, l.ldx, l.xs, xplane, 1.0f / kS, 0.f, 0.f};
         err = tall ? run<ElF16, true, true>(l.upd, a, ex, parts, s) : run<ElF16, true, false>(l.upd, a, ex, parts, s);
         _Float16* t = x;
         x = y;
         y = t;
       } else {
-        const EpiUpdate<T> eu{x, l.ldx, l.xs, xplane, 1.0f / (kS * kS), kA / kS, rows, cols, uc};
+        const EpiUpdate<T> eu{1.0f / (kS * kS), rows, cols, uc};
         err = tall ? run<ElF16, true, true>(l.upd, a, eu, parts, s) : run<ElF16, true, false>(l.upd, a, eu, parts, s);
       }
     }
