@@ -63,11 +63,11 @@ def test_linear_forward_refusals():
     assert call(T=0, x=None, w=None, y=None, ws=None, bytes=0) == 0
     size = _abi().lib().moe_linear_workspace_size
     assert size(-1, 64, 64, 1) == 0 and size(4, 60, 64, 1) == 0 and size(4, 64, 64, 3) == 0 and size(0, 64, 64, 1) > 0
-    need = size(64, 64, 8192, 1)  # few tiles, a long sum: in parts
+    need = size(128, 64, 8192, 1)  # few tiles, a long sum: in parts
     assert need > 16
-    _says(call(T=64, K=8192, ws=None), WORKSPACE, "workspace needs")
-    _says(call(T=64, K=8192, bytes=need - 17), WORKSPACE, "workspace needs")
-    _says(call(T=64, K=8192, ws=ODD), ALIGN, "ws is not")
+    _says(call(T=128, K=8192, ws=None), WORKSPACE, "workspace needs")
+    _says(call(T=128, K=8192, bytes=need - 17), WORKSPACE, "workspace needs")
+    _says(call(T=128, K=8192, ws=ODD), ALIGN, "ws is not")
 
 
 def test_linear_backward_refusals():

@@ -182,6 +182,117 @@ static Plan plan_of(int M, int N, int K, int dt) {
   return plan(1, M, N, gg::cdiv((long)K * es, 128), es, false);
 }
 
+// ---- a few tokens -------------------------------------------------------------
+// A few tokens are a stream of weights.  Those go straight from memory to
+// registers as the matrix instruction's A operand (16 rows), tokens as its B
+// operand (16 columns): in one step a wave reads a 128-byte line of each of 16
+// rows, lane l 32 bytes (quarter l / 16) of row l % 16, and the tokens' operand
+// with the same places, so the order of k is the same for both.  A workgroup has
+// 16 rows, its waves take the row's lines in turn and their sums are added in
+// order through LDS, so one launch does it all.
+struct FewBf16 {
+  using Acc = f32x4_t;
+  static TRG_DEV Acc mma(u32x4v a, u32x4v b, Acc c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c,
+                                                   0, 0, 0);
+  }
+};
+struct FewF32 {  // (instruction r takes value r of both pieces)
+  using Acc = f32x4_t;
+  static TRG_DEV Acc mma(u32x4v a, u32x4v b, Acc c) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      c = __builtin_amdgcn_mfma_f32_16x16x4f32(__uint_as_float(a[r]), __uint_as_float(b[r]), c, 0, 0, 0);
+    return c;
+  }
+};
+
+// NM: tiles of 16 rows; NT: of 16 tokens; U: lines a wave has under way.
+template <class Few, class T, int ACT, int NM, int NT, int U, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const T* __restrict__ x, const T* __restrict__ w,
+                                                                const T* __restrict__ bias, const T* __restrict__ res,
+                                                                int tokens, int n, int K, T* __restrict__ z,
+                                                                T* __restrict__ y) {
+  __shared__ __attribute__((aligned(16))) float red[WAVES][NM][NT][256];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, q = (lane >> 4) * 16, row0 = blockIdx.x * (16 * NM);
+  const int rb = K * (int)sizeof(T), lines = (rb + 127) >> 7;
+  const auto rw = tile_rsrc((const char*)(w + (long)row0 * K), min(16 * NM, n - row0) * rb);
+  const auto rx = tile_rsrc((const char*)x, tokens * rb);
+  int wo[NM], xo[NT];
+#pragma unroll
+  for (int m = 0; m < NM; ++m) wo[m] = min(m * 16 + r, n - 1 - row0) * rb;
+#pragma unroll
+  for (int i = 0; i < NT; ++i) xo[i] = min(i * 16 + r, tokens - 1) * rb;
+  f32x4_t acc[NM][NT] = {};
+  for (int l0 = wv; l0 < lines; l0 += WAVES * U) {
+    u32x4v a[U][2][NM], b[U][2][NT];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int p = 0; p < 2; ++p) {
+        const int at = (l0 + u * WAVES) * 128 + p * 64 + q;  // zeros past the row's end
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+          a[u][p][m] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rw, at < rb ? wo[m] + at : kPast, 0, 0));
+#pragma unroll
+        for (int i = 0; i < NT; ++i)
+          b[u][p][i] = __builtin_bit_cast(u32x4v, __builtin_amdgcn_raw_buffer_load_b128(rx, at < rb ? xo[i] + at : kPast, 0, 0));
+      }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int m = 0; m < NM; ++m)
+#pragma unroll
+          for (int i = 0; i < NT; ++i) acc[m][i] = Few::mma(a[u][p][m], b[u][p][i], acc[m][i]);
+  }
+#pragma unroll
+  for (int m = 0; m < NM; ++m)
+#pragma unroll
+    for (int i = 0; i < NT; ++i) *(f32x4_t*)&red[wv][m][i][lane * 4] = acc[m][i];
+  __syncthreads();
+  for (int o = threadIdx.x; o < 16 * NM * tokens; o += 64 * WAVES) {
+    const int ro = o % (16 * NM), t = o / (16 * NM), row = row0 + ro;
+    if (row >= n) continue;
+    // (lane 16 (row / 4) + column of a tile holds four rows)
+    const int at = (((ro & 15) >> 2) * 16 + (t & 15)) * 4 + (ro & 3);
+    float v = red[0][ro >> 4][t >> 4][at];
+#pragma unroll
+    for (int s = 1; s < WAVES; ++s) v += red[s][ro >> 4][t >> 4][at];
+    if (bias) v += Elt<T>::ld(bias + row);
+    const long yo = (long)t * n + row;
+    if (z) Elt<T>::st(z + yo, v);
+    v = act_f<T, ACT>(v);
+    if (res) v += Elt<T>::ld(res + yo);
+    Elt<T>::st(y + yo, v);
+  }
+}
+
+// Where it is taken, by what a CU has to fetch: its rows' weights, and every
+// token's whole row for each workgroup.  Up to 16 tokens always; up to 32 where
+// those rows are short (bf16, 2048 x 2048, 32 tokens 7.6 us against the tiles' 11.5,
+// 6144 x 2048 12.5 / 17.5, but 2048 x 6144 22 / 18).  Two row tiles a workgroup
+// halve the tokens' share where that leaves enough workgroups (16 tokens, 6144 x
+// 2048 11.1 -> 10.1 us, 24576 x 6144 87 -> 71; one token 8.2 -> 8.9; 2048 x 6144, 16
+// tokens 15.7 -> 22.5).
+static bool takes_few(int tokens, long row_bytes) { return tokens <= 16 || (tokens <= 32 && row_bytes <= 4096); }
+
+template <class Few, class T, int ACT>
+static hipError_t few(const T* x, const T* w, const T* bias, const T* res, int tokens, int n, int K, T* z, T* y,
+                      hipStream_t s) {
+  auto go = [&](auto kernel, int nm, int waves) {
+    kernel<<<gg::cdiv(n, 16 * nm), 64 * waves, 0, s>>>(x, w, bias, res, tokens, n, K, z, y);
+  };
+  const bool two = n >= 6144 && tokens > 4;
+  if (tokens <= 16 && !two) go(linear_few_kernel<Few, T, ACT, 1, 1, 4, 8>, 1, 8);
+  else if (tokens <= 16) go(linear_few_kernel<Few, T, ACT, 2, 1, 4, 8>, 2, 8);
+  else if (!two) go(linear_few_kernel<Few, T, ACT, 1, 2, 4, 8>, 1, 8);
+  else go(linear_few_kernel<Few, T, ACT, 2, 2, 2, 8>, 2, 8);
+  return hipGetLastError();
+}
+
 // f(std::integral_constant<int, act>{})
 template <class F>
 static auto with_act(int act, F&& f) {
@@ -211,6 +322,9 @@ static hipError_t fwd(const void* x, const void* w, const void* bias, const void
                       int dt, void* z, void* y, void* ws, hipStream_t s) {
   const Args a = product(x, K, w, K, rows, n, K);
   return with_act(act, [&](auto ACT) {
+    if (takes_few(rows, (long)K * sizeof(T)))
+      return few<std::conditional_t<sizeof(T) == 4, FewF32, FewBf16>, T, decltype(ACT)::value>(
+          (const T*)x, (const T*)w, (const T*)bias, (const T*)res, rows, n, K, (T*)z, (T*)y, s);
     const EpiLinear<T, decltype(ACT)::value> e{(T*)y, (T*)z, (const T*)bias, (const T*)res, n};
     return run<El, true, true>(plan_of(rows, n, K, dt), a, e, (float*)ws, s);
   });
@@ -247,7 +361,9 @@ static hipError_t bwd(const void* dy, const void* x, const void* w, const void* 
 
 using namespace dn;
 
-size_t linear_ws_bytes(int T, int n, int K, int dt) { return plan_of(T, n, K, dt).part_bytes(1, T, n); }
+size_t linear_ws_bytes(int T, int n, int K, int dt) {
+  return takes_few(T, (long)K * es_of(dt)) ? 0 : plan_of(T, n, K, dt).part_bytes(1, T, n);
+}
 
 size_t linear_bwd_ws_bytes(int T, int n, int K, int dt) {
   size_t need = (size_t)gg::cdiv(T, dz_block_rows(T)) * n * 4;

@@ -220,15 +220,15 @@ TRG_DEV TileAt tile_at(const Args& g, int t) {
 // of which are on their way.  Four waves
 // with 128 x 128 products each (a third fewer LDS reads, every wait covered by
 // reading two slices ahead and loading across tiles) measured no better: 8192^3
-// bf16 925 us against 885, 16384 x 2048 x 6144 NN 352 against 341.
+// bf16 925 us against 885.
 template <class El, int BM, int BN, int WM, int WN, int NST, bool AKC, bool BKC, class Epi>
 __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi) {
   constexpr int NW = WM * WN, ES = El::ES, KSTEP = 128 / ES;
   constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
   constexpr int SA = BM * 128, SB = BN * 128, STAGE = SA + SB;
   constexpr int PA = BM / 8 / NW, PB = BN / 8 / NW;  // 1 KiB blocks of a stage a wave loads
-  constexpr int SC = 64, WLDS = 32 * SC * 4;         // epilogue: 32 rows of 64 columns a wave, in the last stage
-  static_assert(WTN == SC && NW * WLDS <= STAGE, "epilogue staging");
+  constexpr int SC = WTN, WLDS = 32 * SC * 4;        // epilogue: 32 rows of a wave's columns, in the last stage
+  static_assert((SC == 64 || SC == 32) && NW * WLDS <= STAGE, "epilogue staging");
   __shared__ __attribute__((aligned(1024))) char smem[NST * STAGE];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -254,8 +254,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     c.nk = max(0, min((g.K - c.k0 + KSTEP - 1) / KSTEP, g.split_steps));
     return c;
   };
-  // step it of nseg * nk: this wave's share of one K step of both operands
-  auto issue = [&](const Cur& c, int it, int stage) {
+  // step it of nseg * nk: blocks i0 to i1 of this wave's share of one K step of
+  // both operands
+  auto issue = [&](const Cur& c, int it, int stage, int i0, int i1) {
     int seg = 0, ks = it;
     if (g.nseg > 1) {
       seg = it >= 2 * c.nk ? 2 : it >= c.nk ? 1 : 0;
@@ -268,20 +269,24 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     if constexpr (AKC) {
       const auto rs = tile_rsrc(A + (long)c.m0 * lda_b, min(BM, g.M - c.m0) * lda_b);
 #pragma unroll
-      for (int i = 0; i < PA; ++i) load_kc(sA, wave * PA + i, lane, rs, k * ES, g.K * ES, lda_b);
+      for (int i = 0; i < PA; ++i)
+        if (i >= i0 && i < i1) load_kc(sA, wave * PA + i, lane, rs, k * ES, g.K * ES, lda_b);
     } else {
       const auto rs = tile_rsrc(A + (long)k * lda_b + c.m0 * ES, min(KSTEP, g.K - k) * lda_b - c.m0 * ES);
 #pragma unroll
-      for (int i = 0; i < PA; ++i) load_mn<ES, BM>(sA, wave * PA + i, lane, rs, lda_b);
+      for (int i = 0; i < PA; ++i)
+        if (i >= i0 && i < i1) load_mn<ES, BM>(sA, wave * PA + i, lane, rs, lda_b);
     }
     if constexpr (BKC) {
       const auto rs = tile_rsrc(B + (long)c.n0 * ldb_b, max(0, min(BN, g.b_rows - c.n0)) * ldb_b);
 #pragma unroll
-      for (int i = 0; i < PB; ++i) load_kc(sB, wave * PB + i, lane, rs, k * ES, g.K * ES, ldb_b);
+      for (int i = 0; i < PB; ++i)
+        if (PA + i >= i0 && PA + i < i1) load_kc(sB, wave * PB + i, lane, rs, k * ES, g.K * ES, ldb_b);
     } else {
       const auto rs = tile_rsrc(B + (long)k * ldb_b + c.n0 * ES, min(KSTEP, g.K - k) * ldb_b - c.n0 * ES);
 #pragma unroll
-      for (int i = 0; i < PB; ++i) load_mn<ES, BN>(sB, wave * PB + i, lane, rs, ldb_b);
+      for (int i = 0; i < PB; ++i)
+        if (PA + i >= i0 && PA + i < i1) load_mn<ES, BN>(sB, wave * PB + i, lane, rs, ldb_b);
     }
   };
 
@@ -290,7 +295,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
   auto start = [&](const Cur& c) {
 #pragma unroll
     for (int s = 0; s < NST - 1; ++s)
-      if (s < c.nk * g.nseg) issue(c, s, s);
+      if (s < c.nk * g.nseg) issue(c, s, s, 0, PA + PB);
   };
   int t = xcd * per + (blockIdx.x >> 3);
   Cur cur;
@@ -316,7 +321,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
       else if (NST > 2 && later == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"i"(PA + PB) : "memory");
       else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();  // this step's stage is complete; the one read last is free
-      if (it + NST - 1 < steps) issue(c, it + NST - 1, (it + NST - 1) % NST);
+      const bool more = it + NST - 1 < steps;
       const char* sA = smem + (it % NST) * STAGE;
       const char* sB = sA + SA;
       u32x4v af[2][TM], bf[2][TN];
@@ -334,6 +339,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
           for (int j = 0; j < TN; ++j) bf[fb ^ 1][j] = frag<El, BN, BKC>(sB, wn * WTN + j * 32, kk + 1, lane);
         }
         __builtin_amdgcn_sched_barrier(0);
+        // The loads of the step NST - 1 ahead, half of them before each of the first
+        // two slices' products: a wave that issues them stalls until the memory
+        // pipe takes them (16 cycles each), so all at once leave the matrix unit
+        // idle, and later than this they have too little time to land.  8192^3
+        // bf16: all ahead of the first slice 885 us, before slices 0 and 1 843, a
+        // quarter before each 942, one between every two products 966.
+        if (kk < 2 && more)
+          issue(c, it + NST - 1, (it + NST - 1) % NST, kk * (PA + PB) / 2, (kk + 1) * (PA + PB) / 2);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -348,12 +362,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     }
 
     // Epilogue, 32 rows of SC columns of a wave at a time: staged in fp32 (straight
-    // from the accumulators' registers; 16-byte chunk c of row r at c ^ r % 16:
+    // from the accumulators' registers; 16-byte chunk c of row r at a place XORed with r:
     // neither the rows' writes nor the reads meet in a bank), then a lane takes 8
     // consecutive columns of a row and, for the mirrored tile, 8 rows of a column.
     constexpr int ROWB = SC * 4, CPR = SC / 8;  // staged row; its pieces of 8 columns
     auto place = [&](int r, int c) {
-      return r * ROWB + ((c ^ (r & 15)) << 4);
+      return r * ROWB + ((c ^ (SC == 64 ? r & 15 : (r >> 1) & 7)) << 4);
     };
     char* wl = smem + (NST - 1) * STAGE + wave * WLDS;
     const auto tile = epi.tile(c.at.b, c.at.part, c.m0, c.n0);
@@ -455,21 +469,32 @@ inline long tiles_of(int M, int N, int tile, bool sym) {
   return sym ? tm * (tm + 1) / 2 : tm * tn;
 }
 
-// es: bytes an element; ksteps: 128-byte steps of K, over all runs.
+// Tile and parts by an estimate in us, with constants fitted to the times of 294
+// sizes (64 to 16384 rows, 64 to 16384 sums, all layouts, bf16 and fp32), each with
+// every tile and 1 to 16 parts: what it picks takes 0.3 % longer than the best on
+// average, 16 % at most.  es: bytes an element; ksteps: 128-byte steps of K, over
+// all runs; a part has two at least.
 inline Plan plan(int batch, int M, int N, long ksteps, int es, bool sym) {
   Plan best{128, 1};
   double t_best = 1e300;
   for (int tile = 256; tile >= 128; tile /= 2) {
     if (tile == 256 && es == 4) continue;
-    const int slots = tile == 256 ? 256 : 512;
-    for (int split = 1; split <= 16; split *= 2) {
-      if (split > 1 && ksteps < 4L * split) break;
-      const long tiles = batch * tiles_of(M, N, tile, sym && split == 1);
-      const long steps = gg::cdiv(ksteps, split);
-      const double step = tile == 256 ? 1.6 : (es == 4 ? 4.0 : 1.1);
-      const double rounds = (double)gg::cdiv(tiles * split, slots);
-      double t = rounds * (steps * step + (tile == 256 ? 8.0 : 4.0));
-      if (split > 1) t += 5.0 + 8.0 * split * batch * (double)M * N / 3e6;
+    for (int split = 1; split <= 16 && (split == 1 || ksteps >= 2L * split); split *= 2) {
+      const long wgs = (long)batch * split * tiles_of(M, N, tile, sym && split == 1);
+      const double steps = (double)gg::cdiv(ksteps, split);
+      double t;
+      if (tile == 256) {
+        t = 4.9 + (double)gg::cdiv(wgs, 256) * (steps * 1.05 + 6.1);
+      } else if (wgs <= 256) {  // one a CU, four stages
+        t = 3.2 + steps * (es == 4 ? 2.09 : 0.557);
+      } else if (es == 4) {
+        t = 1.9 + (double)gg::cdiv(wgs, 512) * (steps * 3.5 + 2.7);
+      } else {
+        const long rest = wgs % 512;
+        t = 1.9 + (double)(wgs / 512) * (steps * 0.98 + 2.7);
+        if (rest > 0) t += steps * (rest > 256 ? 0.98 : 0.742) + 2.7;
+      }
+      if (split > 1) t += 3.1 + 2.22e-6 * split * batch * (double)M * N;  // the sums' way out and in again
       if (t < t_best) {
         t_best = t;
         best = Plan{tile, split};
@@ -497,7 +522,7 @@ hipError_t run(const Plan& p, Args a, const Epi& epi, float* parts, hipStream_t 
       if constexpr (El::ES == 2)
         dense_kernel<El, 256, 256, 2, 4, 2, AKC, BKC><<<need < 256 ? need : 256, 512, 0, s>>>(a, e);
     } else {
-      if (total <= 256) dense_kernel<El, 128, 128, 2, 2, 4, AKC, BKC><<<need, 256, 0, s>>>(a, e);
+      if (total <= 256) dense_kernel<El, 128, 128, 2, 4, 4, AKC, BKC><<<need, 512, 0, s>>>(a, e);
       else dense_kernel<El, 128, 128, 2, 2, 2, AKC, BKC><<<need < 512 ? need : 512, 256, 0, s>>>(a, e);
     }
   };
