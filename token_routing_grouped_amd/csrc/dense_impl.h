@@ -144,24 +144,28 @@ TRG_DEV void lds_load16(__amdgpu_buffer_rsrc_t rs, unsigned lds, int voff) {
 }
 
 // K-contiguous: block blk holds rows 8 blk .. 8 blk + 7, 128 bytes of each, their
-// 16-byte chunks swizzled as gg::load_kc does; the lanes at or past the row's end
-// (kend bytes) are sent past the resource.
-TRG_DEV void load_kc(unsigned dst, int blk, int lane, __amdgpu_buffer_rsrc_t rs, int kbyte, int kend, int ld_bytes) {
-  const int l8 = lane >> 3;
-  const int c = ((lane & 7) ^ (((blk & 1) << 2) | (l8 >> 1))) << 4;
-  const int off = (blk * 8 + l8) * ld_bytes + c;
-  lds_load16(rs, dst + blk * 1024, c < kend - kbyte ? off + kbyte : kPast);
+// 16-byte chunks swizzled as gg::load_kc does.  kc_chunk: the byte of those 128
+// that a lane takes (the same for every other block); kc_offset: its place from
+// the tile's first row on.
+TRG_DEV int kc_chunk(int blk, int lane) { return ((lane & 7) ^ (((blk & 1) << 2) | (lane >> 4))) << 4; }
+TRG_DEV int kc_offset(int blk, int lane, int ld_bytes) {
+  return (blk * 8 + (lane >> 3)) * ld_bytes + kc_chunk(blk, lane);
 }
 
 // MN-contiguous: 128 / ES rows of BMN values; the resource starts at the step's
-// first row and the tile's first column and ends with the last row.
+// first row and the tile's first column and ends with the last row.  Chunk c of row
+// kr lies at c ^ mn_swizzle: the rows that one fragment read takes at once (four,
+// or in fp32 two, four apart) are in different banks.
 template <int ES, int BMN>
-TRG_DEV void load_mn(unsigned dst, int blk, int lane, __amdgpu_buffer_rsrc_t rs, int ld_bytes) {
+TRG_DEV int mn_swizzle(int kr) {
+  if (ES == 4) return ((kr >> 2) & 1) << 3;
+  return BMN == 64 ? ((kr >> 1) & 1) << 2 : (kr & 3) << 2;
+}
+template <int ES, int BMN>
+TRG_DEV int mn_offset(int blk, int lane, int ld_bytes) {
   constexpr int ROWB = BMN * ES;
-  const int at = blk * 1024 + lane * 16;
-  const int kr = at / ROWB;
-  const int swizzle = ES == 2 ? (kr & 3) << 2 : ((kr >> 2) & 1) << 3;
-  lds_load16(rs, dst + blk * 1024, kr * ld_bytes + ((((at % ROWB) >> 4) ^ swizzle) << 4));
+  const int at = blk * 1024 + lane * 16, kr = at / ROWB;
+  return kr * ld_bytes + ((((at % ROWB) >> 4) ^ mn_swizzle<ES, BMN>(kr)) << 4);
 }
 
 // ---- fragments: LDS -> registers --------------------------------------------
@@ -171,7 +175,14 @@ TRG_DEV u32x4v frag(const char* s, int base, int kk, int lane) {
   if constexpr (KC) {
     return __builtin_bit_cast(u32x4v, gg::frag_kc(s, base, kk, lane));
   } else if constexpr (El::ES == 2) {
-    return __builtin_bit_cast(u32x4v, gg::frag_mnc<BMN>(s, base, kk, lane));
+    // as gg::frag_mnc: a transpose read hands 16 lanes a 4 (k) x 16 block of columns
+    const int g = lane >> 4, s16 = lane & 15;
+    const int col = base + (g & 1) * 16 + (s16 & 3) * 4;
+    const int kr = kk * 16 + (g >> 1) * 8 + (s16 >> 2);
+    const char* p = s + kr * (BMN * 2) + (((col >> 3) ^ mn_swizzle<2, BMN>(kr)) << 4) + (col & 7) * 2;
+    const auto lo = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((gg::lds_bf16x4_t*)p);
+    const auto hi = __builtin_amdgcn_ds_read_tr16_b64_v4bf16((gg::lds_bf16x4_t*)(p + 4 * (BMN * 2)));
+    return __builtin_bit_cast(u32x4v, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
   } else {
     const int h = lane >> 5, col = base + (lane & 31);
     const char* p = s + (kk * 2 + h) * 4 * (BMN * 4) + (((col >> 2) ^ (h << 3)) << 4) + (col & 3) * 4;
@@ -216,8 +227,10 @@ TRG_DEV TileAt tile_at(const Args& g, int t) {
 //
 // 256-wide tiles: 8 waves, two on a SIMD, one of which computes while the other
 // waits for LDS; 128-wide ones: 4 waves, and two workgroups on a CU or, where
-// there is one at most (the waits are then all there is), NST = 4 stages, three
-// of which are on their way.  Four waves
+// there is one at most (the waits are then all there is), 8 and NST = 4 stages,
+// three of which are on their way.  64-wide ones, for few or short sums: 4 waves,
+// four stages, two workgroups on a CU (8 waves, two sharing a quarter with half of
+// every step's slices each, measured 7 % slower).  Four waves
 // with 128 x 128 products each (a third fewer LDS reads, every wait covered by
 // reading two slices ahead and loading across tiles) measured no better: 8192^3
 // bf16 925 us against 885.
@@ -254,48 +267,62 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     c.nk = max(0, min((g.K - c.k0 + KSTEP - 1) / KSTEP, g.split_steps));
     return c;
   };
-  // step it of nseg * nk: blocks i0 to i1 of this wave's share of one K step of
-  // both operands
-  auto issue = [&](const Cur& c, int it, int stage, int i0, int i1) {
-    int seg = 0, ks = it;
-    if (g.nseg > 1) {
-      seg = it >= 2 * c.nk ? 2 : it >= c.nk ? 1 : 0;
-      ks = it - seg * c.nk;
+  // The loads: a lane's offsets in its wave's blocks, and the next step's place, all
+  // of it moved on from step to step (formed anew each time it cost some 300 cycles a
+  // step, which nothing hides where a CU has one workgroup).
+  static_assert(PA % 2 == 0 && PB % 2 == 0, "kc_chunk by a block's place in its wave");
+  int aoff[PA], boff[PB];
+#pragma unroll
+  for (int i = 0; i < PA; ++i)
+    aoff[i] = AKC ? kc_offset(wave * PA + i, lane, lda_b) : mn_offset<ES, BM>(wave * PA + i, lane, lda_b);
+#pragma unroll
+  for (int i = 0; i < PB; ++i)
+    boff[i] = BKC ? kc_offset(wave * PB + i, lane, ldb_b) : mn_offset<ES, BN>(wave * PB + i, lane, ldb_b);
+  const char *pa = nullptr, *pb = nullptr;  // K-contiguous: the tile's first row; else the step's
+  int lk = 0, lleft = 0, lseg = 0;          // its first k, steps left in this run, run
+  auto aim = [&](const Cur& c) {            // at the first step of run lseg
+    const long ea = c.at.b * g.a_bs + (g.nseg > 1 && lseg == 0 ? g.a_plane : 0);
+    const long eb = c.at.b * g.b_bs + (lseg == 1 ? g.b_plane : 0);
+    pa = (const char*)g.A + (AKC ? ea + c.m0 * g.lda : ea + c.k0 * g.lda + c.m0) * ES;
+    pb = (const char*)g.B + (BKC ? eb + c.n0 * g.ldb : eb + c.k0 * g.ldb + c.n0) * ES;
+    lk = c.k0;
+    lleft = c.nk;
+  };
+  // half HALF (or, 2, all) of this wave's blocks of the next step; the second one moves on
+  auto issue = [&](const Cur& c, int stage, auto HALF) {
+    constexpr int half = decltype(HALF)::value, P = PA + PB;
+    constexpr int i0 = half == 1 ? P / 2 : 0, i1 = half == 0 ? P / 2 : P;
+    const unsigned sA = lds0 + stage * STAGE + wave * (PA * 1024), sB = lds0 + stage * STAGE + SA + wave * (PB * 1024);
+    const int past = (g.K - lk) * ES;  // bytes to the end of a K-contiguous row
+    const int mn = min(KSTEP, g.K - lk);
+    if (i0 < PA) {
+      const auto rs = tile_rsrc(pa, AKC ? min(BM, g.M - c.m0) * lda_b : mn * lda_b - c.m0 * ES);
+#pragma unroll
+      for (int i = i0; i < (i1 < PA ? i1 : PA); ++i)
+        lds_load16(rs, sA + i * 1024, !AKC ? aoff[i] : kc_chunk(i, lane) < past ? aoff[i] + lk * ES : kPast);
     }
-    const int k = c.k0 + ks * KSTEP;
-    const char* A = (const char*)g.A + (c.at.b * g.a_bs + (g.nseg > 1 && seg == 0 ? g.a_plane : 0)) * ES;
-    const char* B = (const char*)g.B + (c.at.b * g.b_bs + (seg == 1 ? g.b_plane : 0)) * ES;
-    const unsigned sA = lds0 + stage * STAGE, sB = sA + SA;
-    if constexpr (AKC) {
-      const auto rs = tile_rsrc(A + (long)c.m0 * lda_b, min(BM, g.M - c.m0) * lda_b);
+    if (i1 > PA) {
+      const auto rs = tile_rsrc(pb, BKC ? max(0, min(BN, g.b_rows - c.n0)) * ldb_b : mn * ldb_b - c.n0 * ES);
 #pragma unroll
-      for (int i = 0; i < PA; ++i)
-        if (i >= i0 && i < i1) load_kc(sA, wave * PA + i, lane, rs, k * ES, g.K * ES, lda_b);
-    } else {
-      const auto rs = tile_rsrc(A + (long)k * lda_b + c.m0 * ES, min(KSTEP, g.K - k) * lda_b - c.m0 * ES);
-#pragma unroll
-      for (int i = 0; i < PA; ++i)
-        if (i >= i0 && i < i1) load_mn<ES, BM>(sA, wave * PA + i, lane, rs, lda_b);
+      for (int i = (i0 > PA ? i0 - PA : 0); i < i1 - PA; ++i)
+        lds_load16(rs, sB + i * 1024, !BKC ? boff[i] : kc_chunk(i, lane) < past ? boff[i] + lk * ES : kPast);
     }
-    if constexpr (BKC) {
-      const auto rs = tile_rsrc(B + (long)c.n0 * ldb_b, max(0, min(BN, g.b_rows - c.n0)) * ldb_b);
-#pragma unroll
-      for (int i = 0; i < PB; ++i)
-        if (PA + i >= i0 && PA + i < i1) load_kc(sB, wave * PB + i, lane, rs, k * ES, g.K * ES, ldb_b);
-    } else {
-      const auto rs = tile_rsrc(B + (long)k * ldb_b + c.n0 * ES, min(KSTEP, g.K - k) * ldb_b - c.n0 * ES);
-#pragma unroll
-      for (int i = 0; i < PB; ++i)
-        if (PA + i >= i0 && PA + i < i1) load_mn<ES, BN>(sB, wave * PB + i, lane, rs, ldb_b);
+    if (half > 0) {
+      lk += KSTEP;
+      if (!AKC) pa += (long)KSTEP * lda_b;
+      if (!BKC) pb += (long)KSTEP * ldb_b;
+      if (--lleft == 0 && ++lseg < g.nseg) aim(c);
     }
   };
 
   // A tile's first NST - 1 steps are loaded into the first stages before the
   // previous tile's epilogue, which stages through the last one.
   auto start = [&](const Cur& c) {
+    lseg = 0;
+    aim(c);
 #pragma unroll
     for (int s = 0; s < NST - 1; ++s)
-      if (s < c.nk * g.nseg) issue(c, s, s, 0, PA + PB);
+      if (s < c.nk * g.nseg) issue(c, s, std::integral_constant<int, 2>{});
   };
   int t = xcd * per + (blockIdx.x >> 3);
   Cur cur;
@@ -322,6 +349,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
       else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();  // this step's stage is complete; the one read last is free
       const bool more = it + NST - 1 < steps;
+      constexpr bool AHEAD = BM == 128 && NST == 2;
+      if (AHEAD && more) issue(c, (it + NST - 1) % NST, std::integral_constant<int, 2>{});
       const char* sA = smem + (it % NST) * STAGE;
       const char* sB = sA + SA;
       u32x4v af[2][TM], bf[2][TN];
@@ -345,8 +374,10 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
         // idle, and later than this they have too little time to land.  8192^3
         // bf16: all ahead of the first slice 885 us, before slices 0 and 1 843, a
         // quarter before each 942, one between every two products 966.
-        if (kk < 2 && more)
-          issue(c, it + NST - 1, (it + NST - 1) % NST, kk * (PA + PB) / 2, (kk + 1) * (PA + PB) / 2);
+        // (Two workgroups on a CU wait for each other's loads anyway: all ahead, 24.8
+        // against 26.3 us for 8 x 1024 x 1024 x 1024 symmetric.)
+        if constexpr (!AHEAD && kk < 2)
+          if (more) issue(c, (it + NST - 1) % NST, KK);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -360,7 +391,6 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
       cur = decode(t + nbx);
       start(cur);
     }
-
     // Epilogue, 32 rows of SC columns of a wave at a time: staged in fp32 (straight
     // from the accumulators' registers; 16-byte chunk c of row r at a place XORed with r:
     // neither the rows' writes nor the reads meet in a bank), then a lane takes 8
@@ -457,7 +487,7 @@ __global__ __launch_bounds__(256) void join_kernel(EpiPart in, int nsplit, int M
 
 // ---- host: which tiles, how many parts ----------------------------------------
 struct Plan {
-  int tile;    // 256 or 128
+  int tile;    // 256, 128 or 64
   int nsplit;  // parts of K
   size_t part_bytes(int batch, int M, int N) const {
     return nsplit > 1 ? (size_t)nsplit * batch * M * ((N + 7) / 8 * 8) * 4 : 0;
@@ -470,31 +500,31 @@ inline long tiles_of(int M, int N, int tile, bool sym) {
 }
 
 // Tile and parts by an estimate in us, with constants fitted to the times of 294
-// sizes (64 to 16384 rows, 64 to 16384 sums, all layouts, bf16 and fp32), each with
-// every tile and 1 to 16 parts: what it picks takes 0.3 % longer than the best on
-// average, 16 % at most.  es: bytes an element; ksteps: 128-byte steps of K, over
-// all runs; a part has two at least.
+// sizes (64 to 16384 rows, sums of 64 to 16384, all layouts, bf16 and fp32), each
+// with every tile and 1 to 16 parts: what it picks takes 1 % longer than the best on
+// average, 27 % at most (16384 x 1000 x 128, all epilogue).  es: bytes an element;
+// ksteps: 128-byte steps of K, over all runs; a part has two at least.
 inline Plan plan(int batch, int M, int N, long ksteps, int es, bool sym) {
+  const bool f32 = es == 4;
   Plan best{128, 1};
   double t_best = 1e300;
-  for (int tile = 256; tile >= 128; tile /= 2) {
-    if (tile == 256 && es == 4) continue;
+  for (int tile = 256; tile >= 64; tile /= 2) {
+    if (tile == 256 && f32) continue;
     for (int split = 1; split <= 16 && (split == 1 || ksteps >= 2L * split); split *= 2) {
-      const long wgs = (long)batch * split * tiles_of(M, N, tile, sym && split == 1);
+      const long wgs = (long)batch * split * tiles_of(M, N, tile, sym && split == 1), rest = wgs % 512;
       const double steps = (double)gg::cdiv(ksteps, split);
+      // a round of workgroups that share their CU, and one that does not
+      auto rounds = [&](double shared, double lone, double each) {
+        double t = (double)(wgs / 512) * (steps * shared + each);
+        if (rest > 0) t += steps * (rest > 256 ? shared : lone) + each;
+        return t;
+      };
       double t;
-      if (tile == 256) {
-        t = 4.9 + (double)gg::cdiv(wgs, 256) * (steps * 1.05 + 6.1);
-      } else if (wgs <= 256) {  // one a CU, four stages
-        t = 3.2 + steps * (es == 4 ? 2.09 : 0.557);
-      } else if (es == 4) {
-        t = 1.9 + (double)gg::cdiv(wgs, 512) * (steps * 3.5 + 2.7);
-      } else {
-        const long rest = wgs % 512;
-        t = 1.9 + (double)(wgs / 512) * (steps * 0.98 + 2.7);
-        if (rest > 0) t += steps * (rest > 256 ? 0.98 : 0.742) + 2.7;
-      }
-      if (split > 1) t += 3.1 + 2.22e-6 * split * batch * (double)M * N;  // the sums' way out and in again
+      if (tile == 256) t = 3.2 + (double)gg::cdiv(wgs, 256) * (steps * 1.17 + 4.3);
+      else if (tile == 64) t = 2.3 + rounds(f32 ? 1.17 : 0.425, f32 ? 0.54 : 0.27, 1.0);
+      else if (wgs <= 256) t = 4.7 + steps * (f32 ? 2.24 : 0.50);  // (four stages)
+      else t = 3.2 + rounds(f32 ? 3.6 : 0.82, f32 ? 2.2 : 0.405, 2.1);
+      if (split > 1) t += 2.1 + 2.14e-6 * split * batch * (double)M * N;  // the sums' way out and in again
       if (t < t_best) {
         t_best = t;
         best = Plan{tile, split};
@@ -518,7 +548,9 @@ hipError_t run(const Plan& p, Args a, const Epi& epi, float* parts, hipStream_t 
   const long total = (long)a.tiles * a.nsplit * a.batch;
   const int need = (int)((total + 7) / 8 * 8);
   auto go = [&](const auto& e) {
-    if (p.tile == 256) {
+    if (p.tile == 64) {
+      dense_kernel<El, 64, 64, 2, 2, 4, AKC, BKC><<<need < 512 ? need : 512, 256, 0, s>>>(a, e);
+    } else if (p.tile == 256) {
       if constexpr (El::ES == 2)
         dense_kernel<El, 256, 256, 2, 4, 2, AKC, BKC><<<need < 256 ? need : 256, 512, 0, s>>>(a, e);
     } else {
