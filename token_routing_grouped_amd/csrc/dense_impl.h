@@ -34,6 +34,7 @@ constexpr int kPast = 0x7ffffff0;  // a byte offset past every operand tile's re
 
 struct ElBf16 {
   static constexpr int ES = 2;
+  static constexpr bool kRuns = false;  // nseg may be 3
   static TRG_DEV f32x16_t mma(u32x4v b, u32x4v a, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, b), __builtin_bit_cast(bf16x8_t, a), c,
                                                    0, 0, 0);
@@ -41,6 +42,7 @@ struct ElBf16 {
 };
 struct ElF16 {
   static constexpr int ES = 2;
+  static constexpr bool kRuns = true;
   static TRG_DEV f32x16_t mma(u32x4v b, u32x4v a, f32x16_t c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, b), __builtin_bit_cast(f16x8_t, a), c, 0,
                                                   0, 0);
@@ -50,6 +52,7 @@ struct ElF16 {
 // are 4 apart: any order of K will do as long as both operands have the same.
 struct ElF32 {
   static constexpr int ES = 4;
+  static constexpr bool kRuns = false;
   static TRG_DEV f32x16_t mma(u32x4v b, u32x4v a, f32x16_t c) {
 #pragma unroll
     for (int r = 0; r < 4; ++r)
@@ -289,7 +292,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     lleft = c.nk;
   };
   // half HALF (or, 2, all) of this wave's blocks of the next step; the second one moves on
-  auto issue = [&](const Cur& c, int stage, auto HALF) {
+  // (TAIL: it may end a K-contiguous row)
+  auto issue = [&](const Cur& c, int stage, auto HALF, auto TAIL) {
     constexpr int half = decltype(HALF)::value, P = PA + PB;
     constexpr int i0 = half == 1 ? P / 2 : 0, i1 = half == 0 ? P / 2 : P;
     const unsigned sA = lds0 + stage * STAGE + wave * (PA * 1024), sB = lds0 + stage * STAGE + SA + wave * (PB * 1024);
@@ -299,13 +303,13 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
       const auto rs = tile_rsrc(pa, AKC ? min(BM, g.M - c.m0) * lda_b : mn * lda_b - c.m0 * ES);
 #pragma unroll
       for (int i = i0; i < (i1 < PA ? i1 : PA); ++i)
-        lds_load16(rs, sA + i * 1024, !AKC ? aoff[i] : kc_chunk(i, lane) < past ? aoff[i] + lk * ES : kPast);
+        lds_load16(rs, sA + i * 1024, !AKC ? aoff[i] : !decltype(TAIL)::value || kc_chunk(i, lane) < past ? aoff[i] + lk * ES : kPast);
     }
     if (i1 > PA) {
       const auto rs = tile_rsrc(pb, BKC ? max(0, min(BN, g.b_rows - c.n0)) * ldb_b : mn * ldb_b - c.n0 * ES);
 #pragma unroll
       for (int i = (i0 > PA ? i0 - PA : 0); i < i1 - PA; ++i)
-        lds_load16(rs, sB + i * 1024, !BKC ? boff[i] : kc_chunk(i, lane) < past ? boff[i] + lk * ES : kPast);
+        lds_load16(rs, sB + i * 1024, !BKC ? boff[i] : !decltype(TAIL)::value || kc_chunk(i, lane) < past ? boff[i] + lk * ES : kPast);
     }
     if (half > 0) {
       lk += KSTEP;
@@ -322,7 +326,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     aim(c);
 #pragma unroll
     for (int s = 0; s < NST - 1; ++s)
-      if (s < c.nk * g.nseg) issue(c, s, std::integral_constant<int, 2>{});
+      if (s < c.nk * g.nseg) issue(c, s, std::integral_constant<int, 2>{}, std::true_type{});
   };
   int t = xcd * per + (blockIdx.x >> 3);
   Cur cur;
@@ -339,19 +343,25 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
       for (int j = 0; j < TN; ++j)
 #pragma unroll
         for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.f;
-    const int steps = c.nk * g.nseg;
-    for (int it = 0; it < steps; ++it) {
-      // this step's loads are done once no more are under way than the later
-      // steps' (whatever was issued after those only makes the wait longer)
-      const int later = min(NST - 2, steps - 1 - it);
-      if (NST > 2 && later == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"i"(2 * (PA + PB)) : "memory");
-      else if (NST > 2 && later == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"i"(PA + PB) : "memory");
+    // One step: FULL, one of NST in a row after which NST more exist.  stage: a constant
+    // there, so that every LDS address is one of a few registers and an immediate.
+    auto step = [&](int it, int steps, auto stage, auto FULL) {
+      constexpr bool full = decltype(FULL)::value;
+      constexpr int P = PA + PB;
+      // (the last step of all is never loaded from a FULL one; of several runs each has its own)
+      const std::integral_constant<bool, !full || El::kRuns> TAIL{};
+      const int st = stage;
+      // this step's loads are done once no more are under way than the later steps'
+      // (whatever was issued after those only makes the wait longer)
+      const int later = full ? NST - 2 : min(NST - 2, steps - 1 - it);
+      if (NST > 2 && later == 2) asm volatile("s_waitcnt vmcnt(%0)" ::"i"(2 * P) : "memory");
+      else if (NST > 2 && later == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"i"(P) : "memory");
       else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
       __syncthreads();  // this step's stage is complete; the one read last is free
-      const bool more = it + NST - 1 < steps;
+      const bool more = full || it + NST - 1 < steps;
       constexpr bool AHEAD = BM == 128 && NST == 2;
-      if (AHEAD && more) issue(c, (it + NST - 1) % NST, std::integral_constant<int, 2>{});
-      const char* sA = smem + (it % NST) * STAGE;
+      if (AHEAD && more) issue(c, (st + NST - 1) % NST, std::integral_constant<int, 2>{}, TAIL);
+      const char* sA = smem + st * STAGE;
       const char* sB = sA + SA;
       u32x4v af[2][TM], bf[2][TN];
 #pragma unroll
@@ -377,7 +387,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
         // (Two workgroups on a CU wait for each other's loads anyway: all ahead, 24.8
         // against 26.3 us for 8 x 1024 x 1024 x 1024 symmetric.)
         if constexpr (!AHEAD && kk < 2)
-          if (more) issue(c, (it + NST - 1) % NST, KK);
+          if (more) issue(c, (st + NST - 1) % NST, KK, TAIL);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -385,7 +395,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
           for (int j = 0; j < TN; ++j) acc[i][j] = El::mma(bf[fb][j], af[fb][i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
       });
-    }
+    };
+    const int steps = c.nk * g.nseg;
+    int it = 0;
+    for (; it + 2 * NST - 1 < steps; it += NST)
+      static_for<NST>([&](auto S) { step(it + decltype(S)::value, steps, S, std::true_type{}); });
+    for (; it < steps; ++it) step(it, steps, it % NST, std::false_type{});
     __syncthreads();  // every wave is done with the last stage
     if (t + nbx < t_end) {
       cur = decode(t + nbx);
@@ -485,6 +500,47 @@ __global__ __launch_bounds__(256) void join_kernel(EpiPart in, int nsplit, int M
   tile.apply(a, v);
 }
 
+// The same for a symmetric product, of which the parts hold what lies on and above
+// the diagonal of the product's tiles: blockIdx.x counts pairs of 64-row and
+// 64-column tiles on and above it, each written once more across it.
+template <class Epi>
+__global__ __launch_bounds__(256) void join_sym_kernel(EpiPart in, int nsplit, int M, Epi epi) {
+  __shared__ float turn[64][65];
+  int i = blockIdx.x, nt = 0;
+  while (i > nt) i -= ++nt;
+  const int m0 = i * 64, n0 = nt * 64, b = blockIdx.y;
+  const auto tile = epi.tile(b, 0, m0, n0);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    At a{h * 32 + (int)threadIdx.x / 8, (int)threadIdx.x % 8 * 8, false, false};
+    a.ok = a.ok2 = m0 + a.row < M && n0 + a.col < epi.cols();
+    const float* p = in.p + b * in.mat + (a.ok ? (m0 + a.row) * in.ld + n0 + a.col : 0);
+    float v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = p[c];
+    for (int s = 1; s < nsplit; ++s) {
+      p += in.all;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) v[c] += p[c];
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) turn[a.row][a.col + c] = a.ok ? v[c] : 0.f;
+    tile.apply(a, v);
+  }
+  if (i == nt) return;
+  __syncthreads();
+  const auto twin = epi.tile(b, 0, n0, m0);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    At a{h * 32 + (int)threadIdx.x / 8, (int)threadIdx.x % 8 * 8, false, false};
+    a.ok = a.ok2 = n0 + a.row < M && m0 + a.col < epi.cols();
+    float v[8];
+#pragma unroll
+    for (int c = 0; c < 8; ++c) v[c] = turn[a.col + c][a.row];
+    twin.apply(a, v);
+  }
+}
+
 // ---- host: which tiles, how many parts ----------------------------------------
 struct Plan {
   int tile;    // 256, 128 or 64
@@ -501,30 +557,31 @@ inline long tiles_of(int M, int N, int tile, bool sym) {
 
 // Tile and parts by an estimate in us, with constants fitted to the times of 294
 // sizes (64 to 16384 rows, sums of 64 to 16384, all layouts, bf16 and fp32), each
-// with every tile and 1 to 16 parts: what it picks takes 1 % longer than the best on
-// average, 27 % at most (16384 x 1000 x 128, all epilogue).  es: bytes an element;
-// ksteps: 128-byte steps of K, over all runs; a part has two at least.
+// with every tile and 1 to 16 parts: what it picks takes 0.6 % longer than the best
+// on average, 21 % at most.  es: bytes an element; ksteps: 128-byte steps of K, over
+// all runs; a part has two at least.
 inline Plan plan(int batch, int M, int N, long ksteps, int es, bool sym) {
   const bool f32 = es == 4;
   Plan best{128, 1};
   double t_best = 1e300;
   for (int tile = 256; tile >= 64; tile /= 2) {
     if (tile == 256 && f32) continue;
-    for (int split = 1; split <= 16 && (split == 1 || ksteps >= 2L * split); split *= 2) {
-      const long wgs = (long)batch * split * tiles_of(M, N, tile, sym && split == 1), rest = wgs % 512;
+    for (int split = 1; split <= 16 && (split == 1 || ksteps >= 2L * split); ++split) {
+      const long wgs = (long)batch * split * tiles_of(M, N, tile, sym), rest = wgs % 512;
       const double steps = (double)gg::cdiv(ksteps, split);
-      // a round of workgroups that share their CU, and one that does not
+      // rounds of workgroups that share their CU, and one that does not
       auto rounds = [&](double shared, double lone, double each) {
         double t = (double)(wgs / 512) * (steps * shared + each);
         if (rest > 0) t += steps * (rest > 256 ? shared : lone) + each;
         return t;
       };
       double t;
-      if (tile == 256) t = 3.2 + (double)gg::cdiv(wgs, 256) * (steps * 1.17 + 4.3);
-      else if (tile == 64) t = 2.3 + rounds(f32 ? 1.17 : 0.425, f32 ? 0.54 : 0.27, 1.0);
-      else if (wgs <= 256) t = 4.7 + steps * (f32 ? 2.24 : 0.50);  // (four stages)
-      else t = 3.2 + rounds(f32 ? 3.6 : 0.82, f32 ? 2.2 : 0.405, 2.1);
-      if (split > 1) t += 2.1 + 2.14e-6 * split * batch * (double)M * N;  // the sums' way out and in again
+      if (tile == 256) t = 3.5 + (double)gg::cdiv(wgs, 256) * (steps * 1.02 + 5.0);
+      else if (tile == 64) t = 2.1 + rounds(f32 ? 0.98 : 0.459, f32 ? 0.554 : 0.175, 1.35);
+      else if (wgs <= 256) t = 5.0 + steps * (f32 ? 1.93 : 0.434);  // (four stages)
+      else t = 3.5 + rounds(f32 ? 3.9 : 0.742, f32 ? 1.92 : 0.402, 1.6);
+      // the sums' way out and in again (a symmetric product's: half as many)
+      if (split > 1) t += 4.9 + (sym ? 1.1e-6 : 2.17e-6) * split * batch * (double)M * N;
       if (t < t_best) {
         t_best = t;
         best = Plan{tile, split};
@@ -540,7 +597,6 @@ hipError_t run(const Plan& p, Args a, const Epi& epi, float* parts, hipStream_t 
   constexpr int KSTEP = 128 / El::ES;
   a.tiles_m = gg::cdiv(a.M, p.tile);
   a.tiles_n = gg::cdiv(a.N, p.tile);
-  a.sym = a.sym && p.nsplit == 1;
   a.tiles = (int)tiles_of(a.M, a.N, p.tile, a.sym);
   a.nsplit = p.nsplit;
   const int ksteps = gg::cdiv(a.K, KSTEP);
@@ -564,6 +620,13 @@ hipError_t run(const Plan& p, Args a, const Epi& epi, float* parts, hipStream_t 
     const long ld = (a.N + 7) / 8 * 8;
     const EpiPart part{parts, ld, a.M * ld, a.batch * (long)a.M * ld};
     go(part);
+    if constexpr (Epi::kMirror) {
+      if (a.sym) {
+        const int side = gg::cdiv(a.N, 64);
+        join_sym_kernel<<<dim3(side * (side + 1) / 2, a.batch), 256, 0, s>>>(part, p.nsplit, a.M, epi);
+        return hipGetLastError();
+      }
+    }
     const dim3 grid((unsigned)gg::cdiv(128 * (ld / 8), 256), gg::cdiv(a.M, 128), a.batch);
     join_kernel<<<grid, 256, 0, s>>>(part, p.nsplit, a.M, epi);
   }
