@@ -72,7 +72,10 @@ struct EpiLinear {
   struct Tile {
     TileMat<T> y, z, bias, res;
     bool has_z, has_bias, has_res;
-    TRG_DEV void apply(const At& a, float (&v)[8]) const {
+    TRG_DEV void fetch(const At& a, Held& h) const {
+      if (has_res) res.fetch(a, h);
+    }
+    TRG_DEV void apply(const At& a, float (&v)[8], const Held& h) const {
       float f[8];
       if (has_bias) {
         bias.load(a, f);  // (rows 0 bytes apart)
@@ -83,7 +86,7 @@ struct EpiLinear {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = act_f<T, ACT>(v[i]);
       if (has_res) {
-        res.load(a, f);
+        TileMat<T>::unpack(h, f);
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += f[i];
       }

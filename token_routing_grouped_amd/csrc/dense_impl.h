@@ -83,6 +83,9 @@ struct At {
   int row, col;    // from the tile's corner
   bool ok, ok2;    // the first and the last four values exist
 };
+struct Held {  // 8 values (or 8 of two planes) on their way
+  uint4 v[2];
+};
 template <class T>
 struct TileMat {
   __amdgpu_buffer_rsrc_t rs;
@@ -100,14 +103,19 @@ struct TileMat {
   TRG_DEV void raw_st(int o, uint4 v) const {
     __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4v, v), rs, o, 0, 0);
   }
-  TRG_DEV void load(const At& a, float (&f)[8]) const {
+  TRG_DEV void fetch(const At& a, Held& h) const {
     const int o = off(a);
-    if constexpr (sizeof(T) == 2) {
-      unpack16<uint16_t>(raw(a.ok ? o : kPast), f);
-    } else {
-      unpack16<float>(raw(a.ok ? o : kPast), f);
-      unpack16<float>(raw(a.ok2 ? o + 16 : kPast), f + 4);
-    }
+    h.v[0] = raw(a.ok ? o : kPast);
+    if constexpr (sizeof(T) == 4) h.v[1] = raw(a.ok2 ? o + 16 : kPast);
+  }
+  static TRG_DEV void unpack(const Held& h, float (&f)[8]) {
+    unpack16<T>(h.v[0], f);
+    if constexpr (sizeof(T) == 4) unpack16<T>(h.v[1], f + 4);
+  }
+  TRG_DEV void load(const At& a, float (&f)[8]) const {
+    Held h;
+    fetch(a, h);
+    unpack(h, f);
   }
   TRG_DEV void store(const At& a, const float (&f)[8]) const {
     const int o = off(a);
@@ -224,7 +232,8 @@ TRG_DEV TileAt tile_at(const Args& g, int t) {
 }
 
 // Epi: `auto tile = epi.tile(b, part, m0, n0)` for a tile's corner, then
-// tile.apply(at, v): 8 consecutive columns of a row, at.col a multiple of 8.
+// tile.fetch(at, held), which loads what the epilogue has to add, and
+// tile.apply(at, v, held): 8 consecutive columns of a row, at.col a multiple of 8.
 // epi.cols(): how many columns C has in memory (a multiple of four), Epi::kMirror:
 // whether C may be symmetric.
 //
@@ -419,7 +428,20 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
     const auto twin = epi.tile(c.at.b, c.at.part, c.n0, c.m0);
     const int cols = epi.cols() - c.n0, rows = g.M - c.m0;
     const bool mirror = Epi::kMirror && g.sym && c.at.mt != c.at.nt;
-    static_for<TM * (WTN / SC)>([&](auto IH) {
+    // What it adds is fetched one block of 32 rows ahead, each piece ahead of the
+    // current one's store, which it would otherwise wait for.
+    constexpr int NS = 32 * CPR / 64, NB = TM * (WTN / SC);
+    Held held[NS];
+    auto at_of = [&](int ln, int ih, int s) {
+      At at{wm * WTM + ih / (WTN / SC) * 32 + s * (64 / CPR) + ln / CPR, wn * WTN + ih % (WTN / SC) * SC + ln % CPR * 8,
+            false, false};
+      at.ok = at.row < rows && at.col < cols;
+      at.ok2 = at.row < rows && at.col + 4 < cols;
+      return at;
+    };
+#pragma unroll
+    for (int s = 0; s < NS; ++s) tile.fetch(at_of(lane, 0, s), held[s]);
+    static_for<NB>([&](auto IH) {
       constexpr int i = decltype(IH)::value / (WTN / SC), jh = decltype(IH)::value % (WTN / SC);
       int ln = lane;  // a new value to the compiler, or it keeps every block's addresses at once
       asm volatile("" : "+v"(ln));
@@ -433,16 +455,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
         });
       });
       __builtin_amdgcn_wave_barrier();
+      constexpr int ih = decltype(IH)::value;
 #pragma unroll
-      for (int s = 0; s < 32 * CPR / 64; ++s) {
+      for (int s = 0; s < NS; ++s) {
         const int r = s * (64 / CPR) + ln / CPR, c8 = ln % CPR;
         float v[8];
         *(f32x4_t*)v = *(const f32x4_t*)(wl + place(r, c8 * 2));
         *(f32x4_t*)(v + 4) = *(const f32x4_t*)(wl + place(r, c8 * 2 + 1));
-        At at{wm * WTM + i * 32 + r, wn * WTN + jh * SC + c8 * 8, false, false};
-        at.ok = at.row < rows && at.col < cols;
-        at.ok2 = at.row < rows && at.col + 4 < cols;
-        tile.apply(at, v);
+        const Held now = held[s];
+        if (ih + 1 < NB) tile.fetch(at_of(ln, ih + 1, s), held[s]);
+        tile.apply(at_of(ln, ih, s), v, now);
       }
       if constexpr (Epi::kMirror) {
         if (mirror) {
@@ -454,7 +476,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void dense_kernel(Args g, Epi epi)
             for (int r = 0; r < 8; ++r) v[r] = *(const float*)(wl + place(r8 + r, col >> 2) + (col & 3) * 4);
             At at{wn * WTN + jh * SC + col, wm * WTM + i * 32 + r8, false, false};
             at.ok = at.ok2 = at.row < g.M - c.n0 && at.col < epi.cols() - c.m0;
-            twin.apply(at, v);
+            Held h;
+            twin.fetch(at, h);
+            twin.apply(at, v, h);
           }
         }
       }
@@ -470,7 +494,8 @@ struct EpiPart {
   long ld, mat, all;  // row; one matrix; one part of all matrices
   struct Tile {
     TileMat<float> o;
-    TRG_DEV void apply(const At& a, const float (&v)[8]) const { o.store(a, v); }
+    TRG_DEV void fetch(const At&, Held&) const {}
+    TRG_DEV void apply(const At& a, const float (&v)[8], const Held&) const { o.store(a, v); }
   };
   TRG_DEV int cols() const { return (int)ld; }
   TRG_DEV Tile tile(int b, int part, int m0, int n0) const {
@@ -488,6 +513,8 @@ __global__ __launch_bounds__(256) void join_kernel(EpiPart in, int nsplit, int M
   a.ok = a.row < 128 && m0 + a.row < M && a.col < epi.cols();
   a.ok2 = a.ok && a.col + 4 < epi.cols();
   const auto tile = epi.tile(b, 0, m0, 0);
+  Held held;
+  tile.fetch(a, held);
   const float* p = in.p + b * in.mat + (m0 + (a.ok ? a.row : 0)) * in.ld + (a.ok ? a.col : 0);
   float v[8];
 #pragma unroll
@@ -497,7 +524,7 @@ __global__ __launch_bounds__(256) void join_kernel(EpiPart in, int nsplit, int M
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] += p[c];
   }
-  tile.apply(a, v);
+  tile.apply(a, v, held);
 }
 
 // The same for a symmetric product, of which the parts hold what lies on and above
@@ -514,6 +541,8 @@ __global__ __launch_bounds__(256) void join_sym_kernel(EpiPart in, int nsplit, i
   for (int h = 0; h < 2; ++h) {
     At a{h * 32 + (int)threadIdx.x / 8, (int)threadIdx.x % 8 * 8, false, false};
     a.ok = a.ok2 = m0 + a.row < M && n0 + a.col < epi.cols();
+    Held held;
+    tile.fetch(a, held);
     const float* p = in.p + b * in.mat + (a.ok ? (m0 + a.row) * in.ld + n0 + a.col : 0);
     float v[8];
 #pragma unroll
@@ -525,7 +554,7 @@ __global__ __launch_bounds__(256) void join_sym_kernel(EpiPart in, int nsplit, i
     }
 #pragma unroll
     for (int c = 0; c < 8; ++c) turn[a.row][a.col + c] = a.ok ? v[c] : 0.f;
-    tile.apply(a, v);
+    tile.apply(a, v, held);
   }
   if (i == nt) return;
   __syncthreads();
@@ -534,10 +563,12 @@ __global__ __launch_bounds__(256) void join_sym_kernel(EpiPart in, int nsplit, i
   for (int h = 0; h < 2; ++h) {
     At a{h * 32 + (int)threadIdx.x / 8, (int)threadIdx.x % 8 * 8, false, false};
     a.ok = a.ok2 = n0 + a.row < M && m0 + a.col < epi.cols();
+    Held held;
+    twin.fetch(a, held);
     float v[8];
 #pragma unroll
     for (int c = 0; c < 8; ++c) v[c] = turn[a.col + c][a.row];
-    twin.apply(a, v);
+    twin.apply(a, v, held);
   }
 }
 

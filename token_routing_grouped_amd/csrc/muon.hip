@@ -52,12 +52,16 @@ struct TilePlanes {
     hi.raw_st(o, __builtin_bit_cast(uint4, h));
     if (TWO) lo.raw_st(o, __builtin_bit_cast(uint4, l));
   }
-  // v = alpha v + beta stored
-  TRG_DEV void mix(const At& a, float alpha, float beta, float (&v)[8]) const {
+  TRG_DEV void fetch(const At& a, Held& h) const {
     const int o = a.ok ? hi.off(a) : kPast;
-    const f16x8_t h = __builtin_bit_cast(f16x8_t, hi.raw(o));
+    h.v[0] = hi.raw(o);
+    if (TWO) h.v[1] = lo.raw(o);
+  }
+  // v = alpha v + beta stored
+  static TRG_DEV void mix(const Held& held, float alpha, float beta, float (&v)[8]) {
+    const f16x8_t h = __builtin_bit_cast(f16x8_t, held.v[0]);
     f16x8_t l = {};
-    if (TWO) l = __builtin_bit_cast(f16x8_t, lo.raw(o));
+    if (TWO) l = __builtin_bit_cast(f16x8_t, held.v[1]);
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = alpha * v[i] + beta * (TWO ? (float)h[i] + (float)l[i] : (float)h[i]);
   }
@@ -75,9 +79,12 @@ struct EpiIter {
     TilePlanes<TWO> out, in;
     float alpha, beta, gamma;
     int diag;  // the tile's row less its column
-    TRG_DEV void apply(const At& a, float (&v)[8]) const {
+    TRG_DEV void fetch(const At& a, Held& h) const {
+      if (IN) in.fetch(a, h);
+    }
+    TRG_DEV void apply(const At& a, float (&v)[8], const Held& h) const {
       if (IN) {
-        in.mix(a, alpha, beta, v);
+        TilePlanes<TWO>::mix(h, alpha, beta, v);
         const int d = diag + a.row - a.col;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] += d == i ? gamma : 0.f;
@@ -113,18 +120,23 @@ struct EpiUpdate {
   Update u;
   struct Tile {
     TileMat<T> out, w;
-    TileMat<float> master, master_out;
+    TileMat<float> master, master_out, base;  // base: where master or w starts
     float alpha, keep, step;
     bool has_w, has_master;
-    TRG_DEV void apply(const At& a, float (&v)[8]) const {
+    TRG_DEV void fetch(const At& a, Held& h) const {  // the base: master, w, or nothing
+      const int o = has_master ? master.off(a) : w.off(a);
+      h.v[0] = base.raw(has_w && a.ok ? o : kPast);
+      h.v[1] = base.raw(has_w && a.ok2 && (has_master || sizeof(T) == 4) ? o + 16 : kPast);
+    }
+    TRG_DEV void apply(const At& a, float (&v)[8], const Held& h) const {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] *= alpha;
       if (has_w) {
-        float base[8];
-        if (has_master) master.load(a, base);
-        else w.load(a, base);
+        float f[8];
+        if (has_master) TileMat<float>::unpack(h, f);
+        else TileMat<T>::unpack(h, f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = base[i] * keep - step * v[i];
+        for (int i = 0; i < 8; ++i) v[i] = f[i] * keep - step * v[i];
         if (has_master) master_out.store(a, v);
       }
       out.store(a, v);
@@ -138,6 +150,8 @@ struct EpiUpdate {
             TileMat<T>((const T*)u.w, at, ncols),
             TileMat<float>(u.master, at, ncols),
             TileMat<float>(u.master_out, at, ncols),
+            u.master ? TileMat<float>(u.master, at, ncols)
+                     : TileMat<float>((const float*)((const T*)u.w + at), 0, ncols),
             alpha, 1.0f - u.decay * s, u.step * s, u.w != nullptr, u.master != nullptr};
   }
 };
