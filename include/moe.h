@@ -607,8 +607,8 @@ moe_status_t moe_few_fwd(const moe_few_args* args, void* stream);
  *     dz = dy act'(z),  dx = dz w,  dw = dz^T x,  dbias = sum_t dz
  *   relu's slope at 0 is 0.  With an activation dz is rounded to dt once before
  *   the two products (dbias is summed from the unrounded values); sums are fp32,
- *   in a fixed order.  dx, dw and dbias may each be null (not computed); w is
- *   needed for dx, x for dw.  T = 0 gives dw = 0 and dbias = 0.
+ *   in a fixed order.  dx, dw and dbias may each be null (not computed); w is needed for dx,
+ *   x for dw; none may overlap another buffer.  T = 0 gives dw = 0 and dbias = 0.
  * n and K at most 2^20; (T/128 + 1) * (max(n,K)/128 + 1) < 2^27.
  * ws: moe_linear_workspace_size / moe_linear_bwd_workspace_size bytes for these
  * sizes exactly (a smaller T may need more); calls that may run concurrently
@@ -631,12 +631,13 @@ moe_status_t moe_linear_bwd(const void* dy, const void* x, const void* w, const 
  * moe_orthogonalize: every matrix by itself,
  *     X = g / (|g|_F + eps);  `steps` times  X <- a X + (b A + c A^2) X,
  *     A = X X^T (X^T X where rows > cols),  (a, b, c) = (3.4445, -4.7750, 2.0315)
- *   which moves the singular values towards 1; out [B,rows,cols] dt.  dt MOE_BF16:
- *   the iterates are kept in fp16 (11 bits), sums in fp32; dt MOE_F32: in pairs
- *   of fp16 (22 bits).  A singular value below about 2^-11 (2^-22) of |g|_F is
- *   thus lost in the others' rounding.  A zero matrix gives zeros; one that
- *   holds an infinity or NaN gives NaNs, and no other is touched.  |g|_F is
- *   summed in 64 bits.  out may be g.
+ *   which moves the singular values towards 1; out [B,rows,cols] dt.  The
+ *   iterates are kept in fp16 (11 bits), sums in fp32; with dt MOE_F32, with
+ *   master weights and where a side is at most 32, in pairs of fp16 (22 bits).
+ *   A singular value below about 2^-11 (2^-22) of |g|_F is thus lost in the
+ *   others' rounding.  A zero matrix gives zeros; one that holds an infinity or
+ *   NaN gives NaNs, and no other is touched.  |g|_F is summed in 64 bits.  out
+ *   may be g.
  * moe_muon_step: momentum, orthogonalisation and the weights' step,
  *     buf_out = momentum buf + g
  *     u = g + momentum buf_out (nesterov != 0) or buf_out

@@ -3,7 +3,7 @@
 //   C[b] = epilogue(A[b] B[b]^T),  A [M,K], B [N,K], fp32 accumulation,
 // each operand stored K-contiguous (KC) or MN-contiguous (X[k][mn]), in bf16,
 // fp16 or fp32.  The tile pipeline is the grouped GEMMs' (ggemm.hip): operands
-// move from memory to LDS without registers, two stages of 128 bytes of K, the
+// move from memory to LDS without registers, two or four stages of 128 bytes of K, the
 // next 16-byte slice's fragments are read while the current one's matrix
 // instructions run.  What differs:
 //  * Any K, M, N: a buffer resource bounds each operand's rows, and the lanes

@@ -3,9 +3,10 @@
 //   X_0 = G / (|G|_F + eps);  A = X X^T (X^T X for tall ones: the smaller side)
 //   X <- B X,  B = a + b A + c A^2,  (a, b, c) = (3.4445, -4.7750, 2.0315)
 // The odd quintic takes singular values in (0, 1] towards 1 (it stays under
-// 1.21 on [0, 1.21]), so every iterate is bounded and fits fp16: fp16 has the matrix rate of bf16 and three more mantissa bits, which the
-// quintic's slope at 0 (3.4 a step, 485 over five) makes worth having.  fp32
-// matrices are kept as two fp16 planes (22 bits) and multiplied as split sums.
+// 1.21 on [0, 1.21]), so every iterate is bounded and fits fp16: fp16 has the
+// matrix rate of bf16 and three more mantissa bits, which the quintic's slope at 0
+// (3.4 a step, 485 over five) makes worth having.  fp32 matrices are kept as two
+// fp16 planes (22 bits) and multiplied as split sums (takes_planes: which others are).
 //
 // A step is three products of dense_impl.h: A (symmetric: tiles on and above
 // the diagonal), B (symmetric, with a and b A in the epilogue) and B X.  With a in
@@ -273,14 +274,23 @@ struct Layout {
 // MiB), and what a training step can spare of 288 GB.
 constexpr size_t kChunkBytes = (size_t)2 << 30;
 
-static Layout layout(int B, int rows, int cols, int dt) {
+// One plane leaves 1e-3 to 2e-3 of the result as error, half of what rounding it to
+// bf16 does.  fp32 results (with master weights: 2e-3 of a step is some 1e-5 of small
+// matrices' weights, hundreds of their roundings) have two.  So have matrices with a
+// side of at most 32, of whose few roundings single ones stand out (up to twice the
+// result's own rounding).  128 x [2048, 1024] with master weights: 6.9 -> 17.7 ms.
+static bool takes_planes(int rows, int cols, int dt, bool master) {
+  return dt == MOE_F32 || master || rows <= 32 || cols <= 32;
+}
+
+static Layout layout(int B, int rows, int cols, bool planes) {
   Layout l{};
   l.rows = rows;
   l.cols = cols;
   l.m = rows < cols ? rows : cols;
   l.ldx = (cols + 7) / 8 * 8;
   l.lda = (l.m + 7) / 8 * 8;
-  l.planes = dt == MOE_F32 ? 2 : 1;
+  l.planes = planes ? 2 : 1;
   l.xs = (long)rows * l.ldx;
   l.as = (long)l.m * l.lda;
   const size_t per = 4UL * l.planes * (l.xs + l.as);
@@ -305,11 +315,10 @@ static Layout layout(int B, int rows, int cols, int dt) {
   return l;
 }
 
-template <class T>
-static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, Momentum mo,
+template <class T, bool TWO>
+static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int steps, float eps, Momentum mo,
                                 Update u, char* ws, hipStream_t s) {
-  const Layout l = layout(B, rows, cols, dt);
-  constexpr bool TWO = sizeof(T) == 4;
+  const Layout l = layout(B, rows, cols, TWO);
   const bool tall = rows > cols;
   _Float16* x0 = (_Float16*)ws;
   _Float16* x1 = (_Float16*)(ws + l.x_b);
@@ -402,22 +411,31 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int dt
 
 using namespace dn;
 
-size_t orthogonalize_ws_bytes(int B, int rows, int cols, int dt) { return layout(B, rows, cols, dt).total; }
+static hipError_t by_type(const void* g, int B, int rows, int cols, int dt, int steps, float eps, Momentum mo, Update u,
+                          void* ws, hipStream_t s) {
+  if (dt == MOE_F32) return orthogonalize<float, true>(g, B, rows, cols, steps, eps, mo, u, (char*)ws, s);
+  if (takes_planes(rows, cols, dt, u.master != nullptr))
+    return orthogonalize<uint16_t, true>(g, B, rows, cols, steps, eps, mo, u, (char*)ws, s);
+  return orthogonalize<uint16_t, false>(g, B, rows, cols, steps, eps, mo, u, (char*)ws, s);
+}
+
+size_t orthogonalize_ws_bytes(int B, int rows, int cols, int dt) {
+  const size_t two = layout(B, rows, cols, true).total;  // (with master weights, any may take two planes)
+  const size_t one = takes_planes(rows, cols, dt, false) ? 0 : layout(B, rows, cols, false).total;
+  return two > one ? two : one;
+}
 
 hipError_t launch_orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, void* out,
                                 void* ws, hipStream_t s) {
   Update u{};
   u.out = out;
-  return dt == MOE_F32 ? orthogonalize<float>(g, B, rows, cols, dt, steps, eps, Momentum{}, u, (char*)ws, s)
-                       : orthogonalize<uint16_t>(g, B, rows, cols, dt, steps, eps, Momentum{}, u, (char*)ws, s);
+  return by_type(g, B, rows, cols, dt, steps, eps, Momentum{}, u, ws, s);
 }
 
 hipError_t launch_muon_step(const moe_muon_args& a, hipStream_t s) {
   const Momentum mo{a.buf, a.buf_out, a.momentum, a.nesterov};
   const Update u{a.w, a.master, a.master_out, a.w_out, a.step, a.decay, a.lr_scale};
-  return a.dt == MOE_F32
-             ? orthogonalize<float>(a.g, a.B, a.rows, a.cols, a.dt, a.steps, a.eps, mo, u, (char*)a.ws, s)
-             : orthogonalize<uint16_t>(a.g, a.B, a.rows, a.cols, a.dt, a.steps, a.eps, mo, u, (char*)a.ws, s);
+  return by_type(a.g, a.B, a.rows, a.cols, a.dt, a.steps, a.eps, mo, u, a.ws, s);
 }
 
 }  // namespace trg
