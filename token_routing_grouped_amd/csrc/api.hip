@@ -877,6 +877,8 @@ moe_status_t moe_linear_fwd(const void* x, const void* w, const void* bias, cons
   TRY(check_ptrs(fn, {{"x", x}, {"w", w}, {"y", y}}));
   TRY(check_optional_aligned(fn, {{"bias", bias}, {"res", res}, {"z", z}}));
   if (y == x || y == w || z == y) return fail(MOE_ERR_INVALID_ARG, "%s: y, x, w and z must be different buffers", fn);
+  if (y == bias || (z != nullptr && (z == x || z == w || z == bias || z == res)))
+    return fail(MOE_ERR_INVALID_ARG, "%s: an output is also an input (only y may be res)", fn);
   TRY(check_workspace(fn, ws, ws_bytes, trg::linear_ws_bytes(T, n, K, dt)));
   TRY(check_device());
   trg::ProfScope ps(fn, (hipStream_t)stream);
@@ -904,6 +906,9 @@ moe_status_t moe_linear_bwd(const void* dy, const void* x, const void* w, const 
       return fail(MOE_ERR_INVALID_ARG, "%s: dx must be a buffer of its own", fn);
     if (dw != nullptr && (dw == dy || dw == w || dw == x || dw == z || dw == dx))
       return fail(MOE_ERR_INVALID_ARG, "%s: dw must be a buffer of its own", fn);
+    for (const void* p : {dy, x, w, z, (const void*)dx, (const void*)dw})
+      if (dbias != nullptr && dbias == p)
+        return fail(MOE_ERR_INVALID_ARG, "%s: dbias must be a buffer of its own", fn);
   }
   TRY(check_optional_aligned(fn, {{"dx", dx}, {"dw", dw}, {"dbias", dbias}}));
   TRY(check_workspace(fn, ws, ws_bytes, trg::linear_bwd_ws_bytes(T, n, K, dt)));

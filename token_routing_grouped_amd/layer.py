@@ -457,6 +457,7 @@ class MuonGPU:
 
     Master weights are a copy made here: weights changed from outside afterwards
     are overwritten by the next step.  One object's steps belong on one stream.
+    4-bit copies of the weights are the caller's to make anew.
     """
 
     def __init__(self, weights, lr: float = 0.02, momentum: float = 0.95, nesterov: bool = True,
@@ -464,6 +465,8 @@ class MuonGPU:
         self.weights = list(weights)
         if not self.weights:
             raise _abi.MoeError("no weights")
+        if len({w.data_ptr() for w in self.weights}) != len(self.weights):
+            raise _abi.MoeError("a weight is given twice")
         self.lr, self.momentum, self.nesterov, self.weight_decay = lr, momentum, nesterov, weight_decay
         self.steps, self.eps, self.lr_scale = steps, eps, lr_scale
         self.bufs = [torch.zeros_like(w, dtype=torch.float32) for w in self.weights]
@@ -476,6 +479,9 @@ class MuonGPU:
         grads = list(grads)
         if len(grads) != len(self.weights):
             raise _abi.MoeError(f"{len(self.weights)} gradients expected, got {len(grads)}")
+        for i, (w, g) in enumerate(zip(self.weights, grads)):  # all of them before any weight moves
+            if g.shape != w.shape or g.dtype != w.dtype or g.device != w.device or not g.is_contiguous():
+                raise _abi.MoeError(f"gradient {i} must be contiguous {w.dtype} {list(w.shape)} on {w.device}")
         for w, g, buf, master in zip(self.weights, grads, self.bufs, self.masters):
             r, c = w.shape[-2:]
             _abi.moe_muon_step(w, g, buf, self.ws, step=self.lr * max(1.0, r / c) ** 0.5,
