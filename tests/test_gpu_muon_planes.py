@@ -48,3 +48,31 @@ def test_chunked_and_one_plane_fit_the_same_workspace():
     for B, rows, cols in ((1, 64, 64), (128, 40, 4096), (3, 4096, 40), (600, 512, 512), (1, 33, 40)):
         one = abi.moe_orthogonalize_workspace_size(B, rows, cols, torch.bfloat16)
         assert one >= abi.moe_orthogonalize_workspace_size(B, rows, cols, torch.float32)
+
+
+@pytest.mark.parametrize("master", [True, False])
+def test_two_streams_at_once(master):
+    """Two updates under way together, each with its own state and workspace."""
+    say(f"muon two streams {master}")
+    abi = _abi()
+    g = _gradients(3, 200, 264, "bf16", 53)
+    w0 = torch.randn(3, 200, 264, device=DEV, generator=torch.Generator(device=DEV).manual_seed(4)).mul_(0.05)
+
+    def state():
+        return [w0.bfloat16(), torch.zeros_like(w0), w0.clone(), _ws(abi, g)]
+
+    def step(t):
+        abi.moe_muon_step(t[0], g, t[1], t[3], step=0.1, decay=0.01, master=t[2] if master else None)
+
+    want, both = state(), [state(), state()]
+    for _ in range(4):
+        step(want)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, t in zip(streams, both):
+            with torch.cuda.stream(s):
+                step(t)
+    torch.cuda.synchronize()
+    for t in both:
+        assert all(torch.equal(p, q) for p, q in zip(t[:3], want[:3]))
