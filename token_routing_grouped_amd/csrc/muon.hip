@@ -202,21 +202,20 @@ __global__ __launch_bounds__(256) void sumsq_kernel(const T* __restrict__ g, Mom
 
 // X = u 2^13 / (|u| + eps) in planes of rows of ldx values (zeros behind cols).
 // A zero matrix stays zero; one that holds an infinity or NaN becomes NaN.  A
-// thread's kScaleChunks pieces of 8 values are loaded before the norm is put
-// together from its partial sums.
-constexpr int kScaleChunks = 4;
-template <class T, bool MOM>
+// thread's NC pieces of 8 values are loaded before the norm is put together from
+// its partial sums.
+template <class T, bool MOM, int NC>
 __global__ __launch_bounds__(256) void scale_kernel(const T* __restrict__ g, Momentum mo, int rows, int cols, int ldx,
                                                     float eps, const double* __restrict__ part, int blocks, int two,
                                                     long plane, _Float16* __restrict__ x) {
   constexpr int V = Elt<T>::kVec;
   __shared__ double s_inv;
   const int b = blockIdx.y, chunks = ldx / 8;
-  const long total = (long)rows * chunks, i0 = (long)blockIdx.x * (256 * kScaleChunks) + threadIdx.x;
+  const long total = (long)rows * chunks, i0 = (long)blockIdx.x * (256 * NC) + threadIdx.x;
   const bool use_g = !MOM || mo.nesterov;
-  float u[kScaleChunks][8];
+  float u[NC][8];
 #pragma unroll
-  for (int k = 0; k < kScaleChunks; ++k) {
+  for (int k = 0; k < NC; ++k) {
     const long i = i0 + k * 256;
     const int r = ldx == cols ? 0 : (int)(i / chunks);  // (rows without padding are one long row)
     const long c = (i - (long)r * chunks) * 8;
@@ -246,7 +245,7 @@ __global__ __launch_bounds__(256) void scale_kernel(const T* __restrict__ g, Mom
   __syncthreads();
   const double inv = s_inv;
 #pragma unroll
-  for (int k = 0; k < kScaleChunks; ++k) {
+  for (int k = 0; k < NC; ++k) {
     const long i = i0 + k * 256;
     if (i >= total) return;
     float v[8];
@@ -303,8 +302,11 @@ static Layout layout(int B, int rows, int cols, bool planes) {
   l.gram = plan(l.chunk, l.m, l.lda, (long)runs * gg::cdiv(n, 64), 2, true);
   l.sq = plan(l.chunk, l.m, l.lda, (long)runs * gg::cdiv(l.m, 64), 2, true);
   l.upd = plan(l.chunk, rows, l.ldx, (long)runs * gg::cdiv(l.m, 64), 2, false);
-  const long want = gg::cdiv((long)rows * cols, 16384);
-  l.sum_blocks = (int)(want > kSumBlocks ? kSumBlocks : want);
+  // 16384 values a workgroup; 4096 where that gives a matrix at most 64 of them (8 x
+  // [128, 256]: 6.1 -> 3.3 us; more partial sums cost the scaling pass that reads them,
+  // 128 x [2048, 1024] 345 -> 369 us with 256 instead of 128)
+  const long v = (long)rows * cols, many = gg::cdiv(v, 16384), few = gg::cdiv(v, 4096);
+  l.sum_blocks = (int)(many > kSumBlocks ? kSumBlocks : few <= 64 ? few : many > 64 ? many : 64);
   auto up = [](size_t v) { return (v + 255) / 256 * 256; };
   l.x_b = up(2UL * l.planes * l.chunk * l.xs);
   l.a_b = up(2UL * l.planes * l.chunk * l.as);
@@ -346,9 +348,16 @@ static hipError_t orthogonalize(const void* g, int B, int rows, int cols, int st
     }
     const long xplane = nb * l.xs, aplane = nb * l.as;
     sumsq_kernel<T><<<dim3(l.sum_blocks, nb), 256, 0, s>>>(gc, mc, mat, l.sum_blocks, sums);
-    const dim3 grid(gg::cdiv(l.xs / 8, 256 * kScaleChunks), nb);
-    if (mo.buf) scale_kernel<T, true><<<grid, 256, 0, s>>>(gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, TWO, xplane, x0);
-    else scale_kernel<T, false><<<grid, 256, 0, s>>>(gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, TWO, xplane, x0);
+    // four pieces a thread; one where that leaves CUs without a workgroup (8 x [128,
+    // 256] with momentum 7.4 -> 3.9 us)
+    const long pieces = l.xs / 8;
+    auto scale = [&](auto kernel, int nc) {
+      kernel<<<dim3(gg::cdiv(pieces, 256L * nc), nb), 256, 0, s>>>(gc, mc, rows, cols, l.ldx, eps, sums, l.sum_blocks, TWO,
+                                                                   xplane, x0);
+    };
+    const bool few = gg::cdiv(pieces, 1024L) * nb < 256;
+    if (mo.buf) few ? scale(scale_kernel<T, true, 1>, 1) : scale(scale_kernel<T, true, 4>, 4);
+    else few ? scale(scale_kernel<T, false, 1>, 1) : scale(scale_kernel<T, false, 4>, 4);
     hipError_t err = hipGetLastError();
     _Float16 *x = x0, *y = x1;
     for (int it = 0; it < steps && err == hipSuccess; ++it) {
