@@ -100,3 +100,24 @@ def test_more_than_2_31_values_of_matrices():
     for b in at:
         assert torch.equal(buf[b], g[b].float())
         _check_one(_f64(w[b]), _f64(g[b]), "bf16", scale=-0.5, base=w0[b])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T,n", [(1, 8), (63, 72), (64, 64), (256, 136), (257, 520), (319, 56), (320, 264), (321, 200), (513, 72)])
+def test_bias_gradient(T, n, dt):
+    """In one launch with dz up to 320 rows, from partial sums above."""
+    K, act = 64, ACTS[(T + n // 8) % 4]
+    if dt == "f32":
+        n -= 4
+    say(f"bias gradient {T} {n} {dt} {act}")
+    abi, i = _abi(), _inputs(T, n, K, dt, 64)
+    ws = _ws(abi, abi.moe_linear_bwd_workspace_size, T, n, K, DT[dt])
+    db, dx, alone = torch.full_like(i["b"], np.nan), torch.full_like(i["x"], np.nan), torch.full_like(i["x"], np.nan)
+    z = None if act == "none" else i["z"]
+    abi.moe_linear_bwd(i["dy"], i["x"], i["w"], ws, act=act, z=z, dbias=db, dx=dx)
+    abi.moe_linear_bwd(i["dy"], i["x"], i["w"], ws.fill_(0xFF), act=act, z=z, dx=alone)
+    assert torch.equal(dx, alone)
+    dy, zz = _f64(i["dy"]), _f64(i["z"])
+    _, _, rb, rz = ref.linear_bwd(dy, _f64(i["x"]), _f64(i["w"]), zz, act)
+    ez = 0 * dy if act == "none" else 16 * U * np.abs(dy) * (1 + np.abs(zz))
+    _check("db", db, rb, g_of(T) * (np.abs(rz) + ez).sum(0) + ez.sum(0), HALF[dt])

@@ -159,6 +159,53 @@ __global__ __launch_bounds__(64 * kDzWaves) void dz_kernel(const T* __restrict__
   if (c < n) part[(long)blockIdx.y * n + c] = s;
 }
 
+// The same for at most kDzShort rows, in one launch with the bias gradient: a
+// workgroup has 64 columns and every row, eight lanes a row and 64 rows at a time;
+// its lanes' sums are added in order.  With dx, 2048 columns: 253 rows bf16 16.5 ->
+// 13.8 us, fp32 22.3 -> 19.5; 320 rows 16.4 -> 14.4 and 22.4 -> 20.6; 500 rows 16.2 ->
+// 15.7, but fp32 22.7 -> 25.2.
+constexpr int kDzShort = 320;
+template <class T, int ACT>
+__global__ __launch_bounds__(512) void dz_short_kernel(const T* __restrict__ dy, const T* __restrict__ z, int rows,
+                                                       int n, T* __restrict__ dz, T* __restrict__ db) {
+  __shared__ float red[64][68], half[8][64];
+  const int row = threadIdx.x >> 3, c8 = (threadIdx.x & 7) * 8, col = blockIdx.x * 64 + c8;
+  float sum[8] = {};
+  if (col < n) {
+    const bool both = col + 8 <= n;
+#pragma unroll
+    for (int i = 0; i < kDzShort / 64; ++i) {
+      const int r = i * 64 + row;
+      if (r >= rows) continue;
+      const long at = (long)r * n + col;
+      float g[8];
+      ld8(dy + at, both, g);
+      if constexpr (ACT != MOE_ACT_NONE) {
+        float zz[8];
+        ld8(z + at, both, zz);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] *= act_slope<T, ACT>(zz[e]);
+      }
+      if (dz) st8(dz + at, both, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum[e] += g[e];
+    }
+  }
+  *(f32x4_t*)&red[row][c8] = f32x4_t{sum[0], sum[1], sum[2], sum[3]};
+  *(f32x4_t*)&red[row][c8 + 4] = f32x4_t{sum[4], sum[5], sum[6], sum[7]};
+  __syncthreads();
+  const int l = threadIdx.x & 63, q = threadIdx.x >> 6, c = blockIdx.x * 64 + l;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += red[q * 8 + i][l];
+  half[q][l] = s;
+  __syncthreads();
+  if (q > 0 || c >= n) return;
+#pragma unroll
+  for (int i = 1; i < 8; ++i) s += half[i][l];
+  Elt<T>::st(db + c, s);
+}
+
 // db[c] = sum of the blocks' partials: four threads a column take every fourth
 // block in order, and their sums are added in order.
 template <class T>
@@ -344,12 +391,18 @@ static hipError_t bwd(const void* dy, const void* x, const void* w, const void* 
   const int br = dz_block_rows(rows), blocks = gg::cdiv(rows, br);
   float* part = (float*)ws;
   const bool need_dz = dz && (dx || dw);
-  if (rows > 0 && (need_dz || db))
+  const bool brief = db && rows > 0 && rows <= kDzShort;
+  if (brief)
+    with_act(act, [&](auto ACT) {
+      dz_short_kernel<T, decltype(ACT)::value><<<gg::cdiv(n, 64), 512, 0, s>>>((const T*)dy, (const T*)z, rows, n,
+                                                                               need_dz ? dz : nullptr, (T*)db);
+    });
+  else if (rows > 0 && (need_dz || db))
     with_act(act, [&](auto ACT) {
       dz_kernel<T, decltype(ACT)::value><<<dim3(gg::cdiv(n, 512), blocks), 64 * kDzWaves, 0, s>>>(
           (const T*)dy, (const T*)z, rows, n, br, need_dz ? dz : nullptr, db ? part : nullptr);
     });
-  if (db) dbias_kernel<T><<<gg::cdiv(n, 64), 256, 0, s>>>(part, rows > 0 ? blocks : 0, n, (T*)db);
+  if (db && !brief) dbias_kernel<T><<<gg::cdiv(n, 64), 256, 0, s>>>(part, rows > 0 ? blocks : 0, n, (T*)db);
   hipError_t err = hipGetLastError();
   const void* g = dz ? (const void*)dz : dy;
   if (dx && err == hipSuccess) {  // dx = dz W
