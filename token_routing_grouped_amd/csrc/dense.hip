@@ -13,22 +13,26 @@
 namespace trg {
 namespace dn {
 
-// act and its slope in fp32.  Phi is the normal distribution function.  For
-// values stored in bf16 it comes from Abramowitz and Stegun's 7.1.26 (erf to
-// 1.5e-7, a polynomial in 1 / (1 + p |x|) times exp(-x^2)), the exponential and
-// the reciprocal from the hardware (1 ulp): with erff and expf an epilogue of 256 x
-// 256 values took a sixth of its tile's products (16384 x 6144 x 2048, gelu and z
-// kept: 398 us, 1036 TFLOP/s).
+// act and its slope in fp32.  Phi is the normal distribution function, Phi(z) =
+// erfc(-z / sqrt 2) / 2, whose left tail keeps its relative exactness (1 + erf(z / sqrt 2)
+// cancels there: 4 % of Phi(-5) was wrong, all of it below -5.7).  For values stored in bf16 it comes from
+//   erfc(x) = exp(-x^2) t P(t),  t = 1 / (1 + p x),  x = |z| / sqrt 2,
+// P of degree 6 and p fitted over x in [0, 9.5] (all that fp32 holds) for the least largest
+// relative error, 5.3e-7; the exponential and the reciprocal are the hardware's (1 ulp):
+// with erff and expf an epilogue of 256 x 256 values took a sixth of its tile's products
+// (16384 x 6144 x 2048, gelu and z kept: 398 us, 1036 TFLOP/s).
 // The exponential is that of the density, too.
 template <class T>
 TRG_DEV float phi_f(float z, float& density) {
   if constexpr (sizeof(T) == 4) {
     density = 0.39894228040143268f * expf(-0.5f * z * z);
-    return 0.5f + 0.5f * erff(z * 0.70710678118654752f);
+    return 0.5f * erfcf(z * -0.70710678118654752f);
   } else {
     const float e = __builtin_amdgcn_exp2f(z * z * -0.72134752044448170f);
-    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.3275911f * 0.70710678118654752f, 1.0f));
-    const float q = t * (0.254829592f + t * (-0.284496736f + t * (1.421413741f + t * (-1.453152027f + t * 1.061405429f))));
+    const float t = __builtin_amdgcn_rcpf(fmaf(fabsf(z), 0.37314241f * 0.70710678118654752f, 1.0f));
+    const float q =
+        t * (0.21022014557f + t * (0.21564321789f + t * (0.16017091088f + t * (0.29918176371f + t * (-0.15544663812f +
+             t * (0.40920448903f + t * -0.13897441406f))))));
     const float h = 0.5f * q * e;  // Phi(-|z|)
     density = 0.39894228040143268f * e;
     return z > 0.f ? 1.0f - h : h;
