@@ -609,7 +609,7 @@ moe_status_t moe_few_fwd(const moe_few_args* args, void* stream);
  *   the two products (dbias is summed from the unrounded values); sums are fp32,
  *   in a fixed order.  dx, dw and dbias may each be null (not computed); w is needed for dx,
  *   x for dw; none may overlap another buffer.  T = 0 gives dw = 0 and dbias = 0.
- * n and K at most 2^20; (T/128 + 1) * (max(n,K)/128 + 1) < 2^27.
+ * n and K at most 2^20; T at most 2^30; (T/128 + 1) * (max(n,K)/128 + 1) < 2^27.
  * ws: moe_linear_workspace_size / moe_linear_bwd_workspace_size bytes for these
  * sizes exactly (a smaller T may need more); calls that may run concurrently
  * need separate workspaces.

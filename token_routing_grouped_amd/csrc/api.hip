@@ -851,9 +851,10 @@ static moe_status_t check_linear(const char* fn, int T, int n, int K, int dt) {
   TRY(check_row(fn, "K", K, dt));
   if (n > kDenseSide || K > kDenseSide)
     return fail(MOE_ERR_UNSUPPORTED, "%s: n and K must be at most %d", fn, kDenseSide);
-  // output tiles (in up to 16 parts each) and the join's threads are counted in 32 bits
+  // output tiles (in up to 16 parts each) and the join's threads are counted in 32 bits, and so
+  // are tokens, by kernels that step past the last one by up to 64 rows of each of 16 parts
   const long side = n > K ? n : K;
-  if (((long)T / 128 + 1) * (side / 128 + 1) >= (1L << 27))
+  if (T > (1 << 30) || ((long)T / 128 + 1) * (side / 128 + 1) >= (1L << 27))
     return fail(MOE_ERR_UNSUPPORTED, "%s: problem too large", fn);
   return MOE_OK;
 }
