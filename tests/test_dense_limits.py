@@ -37,3 +37,23 @@ def test_tokens_whose_next_rows_pass_32_bits(dt):
         _refused(lib.moe_linear_fwd(P[0], P[1], None, None, T, 8, 8, 0, dt, None, P[2], P[3], BIG, None))
     assert lib.moe_linear_workspace_size(1 << 30, 8, 8, dt) > 0
     assert lib.moe_linear_bwd_workspace_size(1 << 30, 8, 8, dt) > 0
+
+
+def test_sizes_past_32_bits_are_not_cut_down():
+    """2^32 + 5 rows are not 5: refused by the binding (host views of one row)."""
+    import torch
+
+    from token_routing_grouped_amd import _abi
+
+    bf, n = torch.bfloat16, (1 << 32) + 5
+    x, w, ws = torch.zeros(1, 8, dtype=bf).expand(n, 8), torch.zeros(8, 8, dtype=bf), torch.zeros(64, dtype=torch.uint8)
+    g = torch.zeros(1, 1, 8).expand(n, 1, 8)
+    for call in (lambda: _abi.moe_linear_fwd(x, w, x, ws), lambda: _abi.moe_linear_fwd(w, x, w, ws),
+                 lambda: _abi.moe_linear_bwd(x, x, w, ws, dx=x), lambda: _abi.moe_orthogonalize(g, g, ws),
+                 lambda: _abi.moe_muon_step(g, g, g, ws, step=0.1),
+                 lambda: _abi.moe_linear_workspace_size(n, 8, 8, bf), lambda: _abi.moe_linear_workspace_size(8, 8, n + 3, bf),
+                 lambda: _abi.moe_linear_bwd_workspace_size(n, 8, 8, bf),
+                 lambda: _abi.moe_orthogonalize_workspace_size(n, 8, 8, bf)):
+        with pytest.raises(_abi.MoeError, match="can be counted"):
+            call()
+    assert _abi.moe_linear_workspace_size(1 << 30, 8, 8, bf) > 0

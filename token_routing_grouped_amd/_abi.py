@@ -520,9 +520,20 @@ def _arg(t, dtype, numel, name, dev):
     raise MoeError(f"{name} must be contiguous")
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _fit(name, *sizes):
+    """The library counts in 32 bits, and ctypes would cut a larger size down to them."""
+    for n in sizes:
+        if n > _INT_MAX:
+            raise MoeError(f"{name}: a size of {n}, at most {_INT_MAX} can be counted")
+
+
 def _matrix(t, name):
     if not isinstance(t, torch.Tensor) or t.dim() != 2:
         raise MoeError(f"{name} must be a matrix")
+    _fit(name, *t.shape)
     return t.shape
 
 
@@ -669,10 +680,12 @@ def _act(act) -> int:
 
 
 def moe_linear_workspace_size(T: int, n: int, K: int, dtype) -> int:
+    _fit("workspace", T, n, K)
     return _size(lib().moe_linear_workspace_size(T, n, K, _dtype(dtype)))
 
 
 def moe_linear_bwd_workspace_size(T: int, n: int, K: int, dtype) -> int:
+    _fit("workspace", T, n, K)
     return _size(lib().moe_linear_bwd_workspace_size(T, n, K, _dtype(dtype)))
 
 
@@ -706,10 +719,12 @@ def moe_linear_bwd(dy, x, w, ws, act="none", z=None, dx=None, dw=None, dbias=Non
 def _batch(t, name):
     if not isinstance(t, torch.Tensor) or t.dim() not in (2, 3):
         raise MoeError(f"{name} must be a matrix or a batch of matrices")
+    _fit(name, *t.shape)
     return t.shape if t.dim() == 3 else (1, *t.shape)
 
 
 def moe_orthogonalize_workspace_size(B: int, rows: int, cols: int, dtype) -> int:
+    _fit("workspace", B, rows, cols)
     return _size(lib().moe_orthogonalize_workspace_size(B, rows, cols, _dtype(dtype)))
 
 
