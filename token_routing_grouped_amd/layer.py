@@ -465,12 +465,22 @@ class MuonGPU:
         self.weights = list(weights)
         if not self.weights:
             raise _abi.MoeError("no weights")
-        if len({w.data_ptr() for w in self.weights}) != len(self.weights):
-            raise _abi.MoeError("a weight is given twice")
+        for i, w in enumerate(self.weights):  # what an update would refuse after others have moved
+            if w.device != self.weights[0].device:
+                raise _abi.MoeError(f"weight {i} is on {w.device}, weight 0 on {self.weights[0].device}")
+            if not w.is_contiguous() or w.data_ptr() % 16:
+                raise _abi.MoeError(f"weight {i} must be contiguous and 16-byte aligned")
+        spans = sorted((w.data_ptr(), w.data_ptr() + w.numel() * w.element_size(), i)
+                       for i, w in enumerate(self.weights) if w.numel())
+        for (a, end, i), (b, _, j) in zip(spans, spans[1:]):
+            if a == b:
+                raise _abi.MoeError("a weight is given twice")
+            if b < end:
+                raise _abi.MoeError(f"weights {min(i, j)} and {max(i, j)} overlap")
         self.lr, self.momentum, self.nesterov, self.weight_decay = lr, momentum, nesterov, weight_decay
         self.steps, self.eps, self.lr_scale = steps, eps, lr_scale
         self.bufs = [torch.zeros_like(w, dtype=torch.float32) for w in self.weights]
-        self.masters = [w.float() if master and w.dtype != torch.float32 else None for w in self.weights]
+        self.masters = [w.detach().float() if master and w.dtype != torch.float32 else None for w in self.weights]
         need = max(_abi.moe_orthogonalize_workspace_size(*_abi._batch(w, "weight"), w.dtype) for w in self.weights)
         self.ws = _abi.workspace(need, self.weights[0].device)
 
@@ -479,9 +489,14 @@ class MuonGPU:
         grads = list(grads)
         if len(grads) != len(self.weights):
             raise _abi.MoeError(f"{len(self.weights)} gradients expected, got {len(grads)}")
+        moved = {t.data_ptr() for t in (*self.weights, *self.bufs, *self.masters) if t is not None and t.numel()}
         for i, (w, g) in enumerate(zip(self.weights, grads)):  # all of them before any weight moves
             if g.shape != w.shape or g.dtype != w.dtype or g.device != w.device or not g.is_contiguous():
                 raise _abi.MoeError(f"gradient {i} must be contiguous {w.dtype} {list(w.shape)} on {w.device}")
+            if g.data_ptr() % 16:
+                raise _abi.MoeError(f"gradient {i} must be 16-byte aligned")
+            if g.data_ptr() in moved:
+                raise _abi.MoeError(f"gradient {i} is a weight or a state of this object")
         for w, g, buf, master in zip(self.weights, grads, self.bufs, self.masters):
             r, c = w.shape[-2:]
             _abi.moe_muon_step(w, g, buf, self.ws, step=self.lr * max(1.0, r / c) ** 0.5,
