@@ -264,12 +264,11 @@ struct FewF32 {  // (instruction r takes value r of both pieces)
   }
 };
 
-// NM: tiles of 16 rows; NT: of 16 tokens; U: lines a wave has under way.
+// NM: tiles of 16 rows; NT: of 16 tokens; U: lines a wave has under way.  (y may be res.)
 template <class Few, class T, int ACT, int NM, int NT, int U, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const T* __restrict__ x, const T* __restrict__ w,
-                                                                const T* __restrict__ bias, const T* __restrict__ res,
-                                                                int tokens, int n, int K, T* __restrict__ z,
-                                                                T* __restrict__ y) {
+                                                                const T* __restrict__ bias, const T* res, int tokens,
+                                                                int n, int K, T* __restrict__ z, T* y) {
   __shared__ __attribute__((aligned(16))) float red[WAVES][NM][NT][256];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, q = (lane >> 4) * 16, row0 = blockIdx.x * (16 * NM);
