@@ -247,6 +247,8 @@ static Plan plan_of(int M, int N, int K, int dt) {
 // with the same places, so the order of k is the same for both.  A workgroup has
 // 16 rows, its waves take the row's lines in turn and their sums are added in
 // order through LDS, so one launch does it all.
+constexpr int kFewWaves = 8;
+constexpr int few_lines(int row_tiles, int tokens) { return row_tiles == 2 && tokens > 16 ? 2 : 4; }
 struct FewBf16 {
   using Acc = f32x4_t;
   static TRG_DEV Acc mma(u32x4v a, u32x4v b, Acc c) {
@@ -264,7 +266,8 @@ struct FewF32 {  // (instruction r takes value r of both pieces)
   }
 };
 
-// NM: tiles of 16 rows; NT: of 16 tokens; U: lines a wave has under way.  (y may be res.)
+// NM: tiles of 16 rows; NT: of 16 tokens; U: lines of a row in one round of a wave's
+// loop.  (y may be res.)
 template <class Few, class T, int ACT, int NM, int NT, int U, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const T* __restrict__ x, const T* __restrict__ w,
                                                                 const T* __restrict__ bias, const T* res, int tokens,
@@ -326,26 +329,45 @@ __global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const T* __restr
   }
 }
 
-// Where it is taken, by what a CU has to fetch: its rows' weights, and every
-// token's whole row for each workgroup.  Up to 16 tokens always; up to 32 where
-// those rows are short (bf16, 2048 x 2048, 32 tokens 7.6 us against the tiles' 11.5,
-// 6144 x 2048 12.5 / 17.5, but 2048 x 6144 22 / 18).  Two row tiles a workgroup
-// halve the tokens' share where that leaves enough workgroups (16 tokens, 6144 x
-// 2048 11.1 -> 10.1 us, 24576 x 6144 87 -> 71; one token 8.2 -> 8.9; 2048 x 6144, 16
-// tokens 15.7 -> 22.5).
-static bool takes_few(int tokens, long row_bytes) { return tokens <= 16 || (tokens <= 32 && row_bytes <= 4096); }
+// Row tiles a workgroup has, 1 or 2, or 0 where the other kernels' tiles take a
+// product.  By estimates in us, fitted to 5134 times (1 to 32 tokens, 64 to 65536 rows
+// of 64 to 17000 values, bf16 and fp32, weights that come from memory): a launch, the
+// rounds of loads that a wave waits for, all weights, and the fullest CU's weights and
+// tokens (every token's whole row for each workgroup, which two row tiles halve).  What
+// is picked takes 0.8 % longer than the best of the three on average, 26 % at most.  Both
+// sides of some borders, us with one row tile / two / the other tiles:
+//   16 tokens, rows of 2048 bf16: 4096 rows 6.9 / 9.0 / 10.4, 5120 10.1 / 8.8 / 9.7, 8192
+//   11.3 / 11.9 / 11.4, 12288 14.9 / 17.1 / 11.9
+//   32 tokens, rows of 1024 fp32: 4096 rows 9.5 / 11.9 / 12.5, 8192 16.1 / 14.4 / 16.6,
+//   16384 27.5 / 24.2 / 24.3; 8 tokens 5120 rows 8.9 / 8.5 / 13.6, 12288 13.5 / 16.0 / 23.1
+static int few_row_tiles(int tokens, int n, int K, int dt) {
+  if (tokens > 32 || tokens < 1) return 0;
+  const double row = (double)K * es_of(dt), lines = row / 128, all = 1e-6 * row * n;
+  auto us = [&](int tiles, double launch, double wait, double mb, double w_kb, double x_kb) {
+    const int rounds = gg::cdiv(gg::cdiv(n, 16 * tiles), 256);  // workgroups of the fullest CU
+    const double waits = lines / (kFewWaves * few_lines(tiles, tokens));
+    return launch + mb * all + rounds * (wait * (waits > 1 ? waits : 1) + 1e-3 * row * (16 * tiles * w_kb + tokens * x_kb));
+  };
+  const double one = us(1, 2.2, 0.4, 0.1, 0.016, 0.028), two = us(2, 2.45, 0.55, 0.129, 0.0203, 0.0212);
+  const int tiles = two < one ? 2 : 1;
+  // the other tiles: 4.5 TB/s, or their plan, which has a least that saves asking it
+  const double best = two < one ? two : one, least = 1.05 * (3.45 + (lines < 30 ? lines * 0.175 : 5.25));
+  if (best <= all / 4.5 || best <= least) return tiles;
+  return best <= 1.05 * plan_of(tokens, n, K, dt).us ? tiles : 0;
+}
 
 template <class Few, class T, int ACT>
-static hipError_t few(const T* x, const T* w, const T* bias, const T* res, int tokens, int n, int K, T* z, T* y,
-                      hipStream_t s) {
-  auto go = [&](auto kernel, int nm, int waves) {
-    kernel<<<gg::cdiv(n, 16 * nm), 64 * waves, 0, s>>>(x, w, bias, res, tokens, n, K, z, y);
+static hipError_t few(int row_tiles, const T* x, const T* w, const T* bias, const T* res, int tokens, int n, int K, T* z,
+                      T* y, hipStream_t s) {
+  auto go = [&](auto NM, auto NT) {
+    constexpr int nm = decltype(NM)::value, nt = decltype(NT)::value;
+    linear_few_kernel<Few, T, ACT, nm, nt, few_lines(nm, nt * 16), kFewWaves>
+        <<<gg::cdiv(n, 16 * nm), 64 * kFewWaves, 0, s>>>(x, w, bias, res, tokens, n, K, z, y);
   };
-  const bool two = n >= 6144 && tokens > 4;
-  if (tokens <= 16 && !two) go(linear_few_kernel<Few, T, ACT, 1, 1, 4, 8>, 1, 8);
-  else if (tokens <= 16) go(linear_few_kernel<Few, T, ACT, 2, 1, 4, 8>, 2, 8);
-  else if (!two) go(linear_few_kernel<Few, T, ACT, 1, 2, 4, 8>, 1, 8);
-  else go(linear_few_kernel<Few, T, ACT, 2, 2, 2, 8>, 2, 8);
+  const std::integral_constant<int, 1> c1{};
+  const std::integral_constant<int, 2> c2{};
+  if (tokens <= 16) row_tiles == 1 ? go(c1, c1) : go(c2, c1);
+  else row_tiles == 1 ? go(c1, c2) : go(c2, c2);
   return hipGetLastError();
 }
 
@@ -378,9 +400,9 @@ static hipError_t fwd(const void* x, const void* w, const void* bias, const void
                       int dt, void* z, void* y, void* ws, hipStream_t s) {
   const Args a = product(x, K, w, K, rows, n, K);
   return with_act(act, [&](auto ACT) {
-    if (takes_few(rows, (long)K * sizeof(T)))
+    if (const int row_tiles = few_row_tiles(rows, n, K, dt))
       return few<std::conditional_t<sizeof(T) == 4, FewF32, FewBf16>, T, decltype(ACT)::value>(
-          (const T*)x, (const T*)w, (const T*)bias, (const T*)res, rows, n, K, (T*)z, (T*)y, s);
+          row_tiles, (const T*)x, (const T*)w, (const T*)bias, (const T*)res, rows, n, K, (T*)z, (T*)y, s);
     const EpiLinear<T, decltype(ACT)::value> e{(T*)y, (T*)z, (const T*)bias, (const T*)res, n};
     return run<El, true, true>(plan_of(rows, n, K, dt), a, e, (float*)ws, s);
   });
@@ -423,8 +445,18 @@ static hipError_t bwd(const void* dy, const void* x, const void* w, const void* 
 
 using namespace dn;
 
+DensePlan linear_plan(int T, int n, int K, int dt) {
+  const Plan p = plan_of(T, n, K, dt);
+  return {few_row_tiles(T, n, K, dt), p.tile, p.nsplit};
+}
+
+DensePlan linear_bwd_plan(int T, int n, int K, int dt, bool dw) {
+  const Plan p = dw ? plan_of(n, K, T, dt) : plan_of(T, K, n, dt);
+  return {0, p.tile, p.nsplit};
+}
+
 size_t linear_ws_bytes(int T, int n, int K, int dt) {
-  return takes_few(T, (long)K * es_of(dt)) ? 0 : plan_of(T, n, K, dt).part_bytes(1, T, n);
+  return few_row_tiles(T, n, K, dt) ? 0 : plan_of(T, n, K, dt).part_bytes(1, T, n);
 }
 
 size_t linear_bwd_ws_bytes(int T, int n, int K, int dt) {

@@ -576,6 +576,7 @@ __global__ __launch_bounds__(256) void join_sym_kernel(EpiPart in, int nsplit, i
 struct Plan {
   int tile;    // 256, 128 or 64
   int nsplit;  // parts of K
+  double us;   // the estimate
   size_t part_bytes(int batch, int M, int N) const {
     return nsplit > 1 ? (size_t)nsplit * batch * M * ((N + 7) / 8 * 8) * 4 : 0;
   }
@@ -593,8 +594,7 @@ inline long tiles_of(int M, int N, int tile, bool sym) {
 // all runs; a part has two at least.
 inline Plan plan(int batch, int M, int N, long ksteps, int es, bool sym) {
   const bool f32 = es == 4;
-  Plan best{128, 1};
-  double t_best = 1e300;
+  Plan best{128, 1, 1e300};
   for (int tile = 256; tile >= 64; tile /= 2) {
     if (tile == 256 && f32) continue;
     for (int split = 1; split <= 16 && (split == 1 || ksteps >= 2L * split); ++split) {
@@ -613,10 +613,7 @@ inline Plan plan(int batch, int M, int N, long ksteps, int es, bool sym) {
       else t = 3.5 + rounds(f32 ? 3.9 : 0.742, f32 ? 1.92 : 0.402, 1.6);
       // the sums' way out and in again (a symmetric product's: half as many)
       if (split > 1) t += 4.9 + (sym ? 1.1e-6 : 2.17e-6) * split * batch * (double)M * N;
-      if (t < t_best) {
-        t_best = t;
-        best = Plan{tile, split};
-      }
+      if (t < best.us) best = Plan{tile, split, t};
     }
   }
   return best;

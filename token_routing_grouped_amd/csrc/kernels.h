@@ -68,6 +68,14 @@ hipError_t launch_dequantize_e2m1(const uint8_t* q, const uint8_t* s, bool bf16,
 hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s, int T, int n, int K, void* y,
                               hipStream_t st);
 
+// Which variants of its launches a dense product takes: row tiles of the few-token kernel's workgroups (0: it is
+// not taken), else the width of the tiles and the parts of K.
+struct DensePlan {
+  int row_tiles, tile, parts;
+};
+DensePlan linear_plan(int T, int n, int K, int dt);
+DensePlan linear_bwd_plan(int T, int n, int K, int dt, bool dw);
+
 // dense products with an epilogue, and the orthogonalised weight update.  act: MOE_ACT_*
 size_t linear_ws_bytes(int T, int n, int K, int dt);
 hipError_t launch_linear_fwd(const void* x, const void* w, const void* bias, const void* res, int T, int n, int K,
