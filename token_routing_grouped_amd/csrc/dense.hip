@@ -445,14 +445,15 @@ static hipError_t bwd(const void* dy, const void* x, const void* w, const void* 
 
 using namespace dn;
 
-DensePlan linear_plan(int T, int n, int K, int dt) {
-  const Plan p = plan_of(T, n, K, dt);
-  return {few_row_tiles(T, n, K, dt), p.tile, p.nsplit};
+static DensePlan chosen(int M, int N, int K, int dt, int row_tiles) {
+  const Plan p = plan_of(M, N, K, dt);
+  return {row_tiles, p.tile, p.stages(p.nsplit * tiles_of(M, N, p.tile, false)), p.nsplit};
 }
 
+DensePlan linear_plan(int T, int n, int K, int dt) { return chosen(T, n, K, dt, few_row_tiles(T, n, K, dt)); }
+
 DensePlan linear_bwd_plan(int T, int n, int K, int dt, bool dw) {
-  const Plan p = dw ? plan_of(n, K, T, dt) : plan_of(T, K, n, dt);
-  return {0, p.tile, p.nsplit};
+  return dw ? chosen(n, K, T, dt, 0) : chosen(T, K, n, dt, 0);
 }
 
 size_t linear_ws_bytes(int T, int n, int K, int dt) {

@@ -580,6 +580,8 @@ struct Plan {
   size_t part_bytes(int batch, int M, int N) const {
     return nsplit > 1 ? (size_t)nsplit * batch * M * ((N + 7) / 8 * 8) * 4 : 0;
   }
+  // of a tile's K steps in LDS, for so many tiles in all (128-wide ones have a CU each or share it)
+  int stages(long tiles) const { return tile == 256 || (tile == 128 && tiles > 256) ? 2 : 4; }
 };
 
 inline long tiles_of(int M, int N, int tile, bool sym) {
@@ -638,7 +640,7 @@ hipError_t run(const Plan& p, Args a, const Epi& epi, float* parts, hipStream_t 
       if constexpr (El::ES == 2)
         dense_kernel<El, 256, 256, 2, 4, 2, AKC, BKC><<<need < 256 ? need : 256, 512, 0, s>>>(a, e);
     } else {
-      if (total <= 256) dense_kernel<El, 128, 128, 2, 4, 4, AKC, BKC><<<need, 512, 0, s>>>(a, e);
+      if (p.stages(total) == 4) dense_kernel<El, 128, 128, 2, 4, 4, AKC, BKC><<<need, 512, 0, s>>>(a, e);
       else dense_kernel<El, 128, 128, 2, 2, 2, AKC, BKC><<<need < 512 ? need : 512, 256, 0, s>>>(a, e);
     }
   };

@@ -69,12 +69,18 @@ hipError_t launch_linear_e2m1(const void* x, const uint8_t* q, const uint8_t* s,
                               hipStream_t st);
 
 // Which variants of its launches a dense product takes: row tiles of the few-token kernel's workgroups (0: it is
-// not taken), else the width of the tiles and the parts of K.
+// not taken), else the width of the tiles, the stages of each and the parts of K.
 struct DensePlan {
-  int row_tiles, tile, parts;
+  int row_tiles, tile, stages, parts;
 };
 DensePlan linear_plan(int T, int n, int K, int dt);
 DensePlan linear_bwd_plan(int T, int n, int K, int dt, bool dw);
+// The three products of an orthogonalisation's step, for the first chunk of the batch.
+struct OrthoPlan {
+  int planes, chunk;
+  DensePlan gram, square, update;
+};
+OrthoPlan ortho_plan(int B, int rows, int cols, int dt, bool master);
 
 // dense products with an epilogue, and the orthogonalised weight update.  act: MOE_ACT_*
 size_t linear_ws_bytes(int T, int n, int K, int dt);

@@ -436,6 +436,14 @@ size_t orthogonalize_ws_bytes(int B, int rows, int cols, int dt) {
   return two > one ? two : one;
 }
 
+OrthoPlan ortho_plan(int B, int rows, int cols, int dt, bool master) {
+  const Layout l = layout(B, rows, cols, takes_planes(rows, cols, dt, master));
+  auto of = [&](const Plan& p, int M, int N, bool sym) {
+    return DensePlan{0, p.tile, p.stages((long)l.chunk * p.nsplit * tiles_of(M, N, p.tile, sym)), p.nsplit};
+  };
+  return {l.planes, l.chunk, of(l.gram, l.m, l.lda, true), of(l.sq, l.m, l.lda, true), of(l.upd, rows, l.ldx, false)};
+}
+
 hipError_t launch_orthogonalize(const void* g, int B, int rows, int cols, int dt, int steps, float eps, void* out,
                                 void* ws, hipStream_t s) {
   Update u{};
