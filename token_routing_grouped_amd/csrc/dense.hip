@@ -5,7 +5,8 @@
 // The products are dense_impl.h's tiles; dz is made by one pass over dy and z
 // that also sums the bias gradient's partials in fp32 (HBM bound; formed inside the
 // products instead, every tile of a row would evaluate the slope again).  A training
-// step's gradients, 16384 x 6144 x 2048 gelu, 800 us: the pass, dx 349, dW 372.
+// step's gradients, 16384 x 6144 x 2048 gelu, 812 us: the pass 116, the bias 5, dx 332, dW
+// 375.
 #include <math.h>
 
 #include "dense_impl.h"
@@ -20,7 +21,7 @@ namespace dn {
 // P of degree 6 and p fitted over x in [0, 9.5] (all that fp32 holds) for the least largest
 // relative error, 5.3e-7; the exponential and the reciprocal are the hardware's (1 ulp):
 // with erff and expf an epilogue of 256 x 256 values took a sixth of its tile's products
-// (16384 x 6144 x 2048, gelu and z kept: 398 us, 1036 TFLOP/s).
+// (16384 x 6144 x 2048, gelu and z kept: 412 us, 1001 TFLOP/s).
 // The exponential is that of the density, too.
 template <class T>
 TRG_DEV float phi_f(float z, float& density) {
@@ -125,6 +126,10 @@ TRG_DEV void st8(float* p, bool both, const float (&f)[8]) {
 // columns of every 8th row of its block's rows (wave w of 8: rows w, w + 8, ...),
 // adds them in fp32, and the waves' sums are added in order.  dz or part may be
 // absent; z too where the activation has none.
+// dz is rounded to its type here, once, for the two products (the bias sums what is not
+// rounded): bf16 gradients are 2.3e-3 off the exact ones in the norm, where rounding the
+// results alone leaves 1.7e-3.  Two bf16 planes of dz would keep those at twice both
+// products' time (16384 x 6144 x 2048: 707 of 812 us).
 constexpr int kDzWaves = 8;
 template <class T, int ACT>
 __global__ __launch_bounds__(64 * kDzWaves) void dz_kernel(const T* __restrict__ dy, const T* __restrict__ z,
@@ -165,9 +170,10 @@ __global__ __launch_bounds__(64 * kDzWaves) void dz_kernel(const T* __restrict__
 
 // The same for at most kDzShort rows, in one launch with the bias gradient: a
 // workgroup has 64 columns and every row, eight lanes a row and 64 rows at a time;
-// its lanes' sums are added in order.  With dx, 2048 columns: 253 rows bf16 16.5 ->
-// 13.8 us, fp32 22.3 -> 19.5; 320 rows 16.4 -> 14.4 and 22.4 -> 20.6; 500 rows 16.2 ->
-// 15.7, but fp32 22.7 -> 25.2.
+// its lanes' sums are added in order.  The border depends on the rows alone: of the two
+// launches' time this takes, over 64, 256, ... 16384 columns with gelu, bf16 0.42-0.79 at
+// 64 rows, 0.62-0.89 at 320, 0.67-0.97 at 384, 0.78-1.11 at 512; fp32 0.44-0.82, 0.79-1.02,
+// 0.89-1.12, 1.03-1.33 (without activation 0.57-0.67 at 320, 0.72-0.84 at 512).
 constexpr int kDzShort = 320;
 template <class T, int ACT>
 __global__ __launch_bounds__(512) void dz_short_kernel(const T* __restrict__ dy, const T* __restrict__ z, int rows,
@@ -267,7 +273,8 @@ struct FewF32 {  // (instruction r takes value r of both pieces)
 };
 
 // NM: tiles of 16 rows; NT: of 16 tokens; U: lines of a row in one round of a wave's
-// loop.  (y may be res.)
+// loop, whose loads the compiler spreads over the products: two to eight 16-byte pieces
+// are under way at a time.  (y may be res.)
 template <class Few, class T, int ACT, int NM, int NT, int U, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const T* __restrict__ x, const T* __restrict__ w,
                                                                 const T* __restrict__ bias, const T* res, int tokens,
@@ -334,7 +341,7 @@ __global__ __launch_bounds__(64 * WAVES) void linear_few_kernel(const T* __restr
 // of 64 to 17000 values, bf16 and fp32, weights that come from memory): a launch, the
 // rounds of loads that a wave waits for, all weights, and the fullest CU's weights and
 // tokens (every token's whole row for each workgroup, which two row tiles halve).  What
-// is picked takes 0.8 % longer than the best of the three on average, 26 % at most.  Both
+// is picked takes 0.7 % longer than the best of the three on average, 26 % at most.  Both
 // sides of some borders, us with one row tile / two / the other tiles:
 //   16 tokens, rows of 2048 bf16: 4096 rows 6.9 / 9.0 / 10.4, 5120 10.1 / 8.8 / 9.7, 8192
 //   11.3 / 11.9 / 11.4, 12288 14.9 / 17.1 / 11.9
